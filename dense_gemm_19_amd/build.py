@@ -30,8 +30,9 @@ EXTRA_FLAGS = {"gemm_dtl_f8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
 HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-I" + os.path.join(ROOT, "include"), "-I" + CSRC]
 
 HIP_SOURCES = ["gemm_mfma.hip", "gemm_dtl_f16.hip", "gemm_dtl_bf16.hip", "gemm_dtl_f8.hip", "gemm_dtl_f8s.hip", "skinny.hip",
-               "epilogue.hip", "calib.hip", "quant.hip", "noalloc.hip"]
-HOST_SOURCES = ["view.cpp", "plan.cpp", "dg.cpp", "gemm_dtl.cpp"]
+               "epilogue.hip", "calib.hip", "quant.hip", "noalloc.hip", "moe_gemm_f16.hip", "moe_gemm_bf16.hip", "w4.hip",
+               "moe_route.hip"]
+HOST_SOURCES = ["view.cpp", "plan.cpp", "dg.cpp", "gemm_dtl.cpp", "moe.cpp"]
 
 
 def _newest_header() -> float:

@@ -21,15 +21,17 @@
 #include "kernels.hpp"
 #include "plan.hpp"
 #include "quant.hpp"
+#include "runtime.hpp"
 #include "view.hpp"
 
 namespace dg {
-namespace {
 
 bool env_on(const char *name) {
     const char *s = std::getenv(name);
     return s && s[0] == '1';
 }
+
+namespace {
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -110,6 +112,8 @@ DevCache &devcache() {
     return c;
 }
 
+}  // namespace
+
 dg_status current_device(Device *d, bool require) {
     int id = 0;
     if (hipGetDevice(&id) != hipSuccess || id < 0 || id >= 64) {
@@ -140,6 +144,8 @@ dg_status current_device(Device *d, bool require) {
     *d = c.dev[id];
     return DG_SUCCESS;
 }
+
+namespace {
 
 // Split-K scratch: per (device, stream), one block of FP32 partial sums and one
 // of arrival counters, allocated in stream order on that stream (sheratonhq.com
@@ -233,6 +239,8 @@ hipError_t lease_workspace(hipStream_t stream, size_t bytes, size_t ncounters, W
     return hipSuccess;
 }
 
+}  // namespace
+
 dg_status check_pointer(const void *p) {
     if (!p) return DG_SUCCESS;
     hipPointerAttribute_t attr;
@@ -243,6 +251,8 @@ dg_status check_pointer(const void *p) {
     if (attr.type != hipMemoryTypeDevice && attr.type != hipMemoryTypeManaged) return DG_ERR_POINTER;
     return DG_SUCCESS;
 }
+
+namespace {
 
 Epilogue make_epi(const Problem &p) {
     Epilogue e;

@@ -124,9 +124,11 @@ struct DtlIO {
     // the tile origin (row r0 at K tile 0); K tile kt adds kt * (K elements per
     // tile) * k_stride to the origin, the same for every lane.  The host keeps
     // these offsets below 2^31 (rows clamp into [r0, Rlim): r0 < Rlim, and for
-    // M/N-contiguous operands Rlim is a multiple of EPC).
+    // M/N-contiguous operands Rlim is a multiple of EPC).  K elements from Klim
+    // on (a ragged last tile; a multiple of EPC for K-contiguous operands) read
+    // the last one inside: the kernel clears them in LDS.
     struct Src { uint32_t off[INSTS]; };
-    __device__ static Src sources(const Operand &op, int r0, int Rlim, int wave, int lane) {
+    __device__ static Src sources(const Operand &op, int r0, int Rlim, int wave, int lane, int Klim = 1 << 30) {
         Src s;
 #pragma unroll
         for (int j = 0; j < INSTS; ++j) {
@@ -142,12 +144,22 @@ struct DtlIO {
                 k = kk;
                 r = (p ^ mn_swz<EB, CPR>(kk)) * EPC;
             }
+            k = min(k, MODE == KMAJ ? Klim - EPC : Klim - 1);
             // rows past the edge read a real row (a whole in-range chunk for
             // MNMAJ, where a chunk spans EPC rows); their results are not stored
             const int gr = min(r0 + r, MODE == KMAJ ? Rlim - 1 : Rlim - EPC);
             s.off[j] = (uint32_t)((int64_t)(gr - r0) * op.r_stride + (int64_t)k * op.k_stride);
         }
         return s;
+    }
+
+    // Clear the K elements from Klim on of the tile at `lds`, all threads of the
+    // workgroup (tid of nt) together.
+    __device__ static void clear_tail(char *lds, int Klim, int tid, int nt) {
+        for (int pos = tid; pos < R * 8; pos += nt) {
+            const int k = MODE == KMAJ ? ((pos & 7) ^ ((pos >> 3) & 7)) * EPC : pos / CPR;
+            if (k >= Klim) *reinterpret_cast<u32x4 *>(lds + pos * 16) = u32x4{0u, 0u, 0u, 0u};
+        }
     }
 
     // Issue the wave's loads of the tile whose origin is `base` (uniform) into
@@ -273,10 +285,15 @@ __device__ __forceinline__ void raster(int t, int tiles_m, int tiles_n, int grou
 // is a Stream-K-style hybrid: the pieces of the leftover tiles fill the last
 // wave of workgroup slots instead of leaving part of it idle (sheratonhq.com
 // deep dive, section 5.2, names Stream-K for balancing tails).
+// RAGGED: K need not be a whole number of tiles (16-bit inputs).  The last
+// tile's loads read in-range elements in place of those past K, and both
+// operands' are cleared in LDS before the tile is multiplied (both, since what
+// was read instead may hold infinities or NaN).
 // The workgroup body.  t_direct >= 0: this workgroup computes tile t_direct of
 // p whole (the grouped kernel, which maps its grid itself); otherwise the tile
 // (and K piece) follows from blockIdx.x and gridDim.x as described above.
-template <int IN, int BM, int BN, int WGM, int WGN, int NS, int AMODE, int BMODE, bool SPLIT, int NL, bool SA4>
+template <int IN, int BM, int BN, int WGM, int WGN, int NS, int AMODE, int BMODE, bool SPLIT, int NL, bool SA4,
+          bool RAGGED = false>
 __device__ __forceinline__ void mfma_dtl_body(const MfmaArgs &p, const int t_direct) {
     constexpr int NW = WGM * WGN;
     // Waves 0 .. NLD-1 issue the tile loads; NLD < NW leaves the others to
@@ -298,6 +315,7 @@ __device__ __forceinline__ void mfma_dtl_body(const MfmaArgs &p, const int t_dir
     static_assert(WTN <= 128 && 128 % WTN == 0, "a wave's columns lie in one 128-column scale block");
     static_assert(BM % 64 == 0 || !F8, "row scales are staged 64 per wave");
     static_assert(!F8 || NLD >= BM / 64, "row scales are staged by the loader waves");
+    static_assert(!RAGGED || !F8, "a ragged K is for 16-bit inputs");
     static_assert((NS - 2) * PER_FILL <= 63, "vmcnt range");
     // SA4: FP8 row scales 4 K blocks at a time (see sa4_group below), in
     // SA4_NB buffers of [BM rows][4 blocks] floats.
@@ -395,18 +413,27 @@ __device__ __forceinline__ void mfma_dtl_body(const MfmaArgs &p, const int t_dir
         g = min(g, (p.ktiles >> 2) - 1);
         if ((lane >> 4) == j)
             lds_load16(reinterpret_cast<const char *>(p.sa) + (int64_t)g * 16, sa4_off,
-                       sa4_lds + (uint32_t)((g & (SA4_NB - 1)) * SA4_BUF + 1024 * (wave_u % (BM / 64))));
+                       sa4_lds + (uint32_t)((g & (SA4_NB - 1)) * SA4_BUF + 1024 * (wave_u % (F8 ? BM / 64 : 1))));
     };
 
     auto fill = [&](int stage_idx, int kt) __attribute__((always_inline)) {   // K tile kt into a stage
         if (NLD < NW && wave_u >= NLD) return;
         const uint32_t st = ring_lds + (uint32_t)(stage_idx * STAGE);
+        if constexpr (RAGGED) {
+            if (kt == p.ktiles - 1 && p.K % KEL != 0) {
+                const typename AIO::Src at = AIO::sources(p.a, m0, p.M, wave % NLD, lane, p.K % KEL);
+                AIO::issue(st, at, a_org + kt * a_kstep, wave_u);
+                const typename BIO::Src bt = BIO::sources(p.b, n0, p.N, wave % NLD, lane, p.K % KEL);
+                BIO::issue(st + A_BYTES, bt, b_org + kt * b_kstep, wave_u);
+                return;
+            }
+        }
         AIO::issue(st, a_src, a_org + kt * a_kstep, wave_u);
         BIO::issue(st + A_BYTES, b_src, b_org + kt * b_kstep, wave_u);
         if constexpr (F8) {
             if constexpr (!SA4)
                 lds_load4(reinterpret_cast<const char *>(p.sa) + (int64_t)kt * p.sa_cs, sa_off,
-                          st + SA_OFF + 256 * (wave_u % (BM / 64)));
+                          st + SA_OFF + 256 * (wave_u % (F8 ? BM / 64 : 1)));
             else if constexpr (NS > 2)
                 sa4_quarter((kt >> 2) + 1, kt & 3);
             lds_load4(reinterpret_cast<const char *>(p.sb) + (int64_t)kt * p.sb_rs, sb_off, st + SB_OFF);
@@ -586,6 +613,13 @@ __device__ __forceinline__ void mfma_dtl_body(const MfmaArgs &p, const int t_dir
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
         const int nxt = cur == 0 ? NS - 1 : cur - 1;
         if (kt + NS - 1 < kt1) fill(nxt, kt + NS - 1);
+        if constexpr (RAGGED) {
+            if (kt == p.ktiles - 1 && p.K % KEL != 0) {
+                AIO::clear_tail(ring + cur * STAGE, p.K % KEL, tid, 64 * NW);
+                BIO::clear_tail(ring + cur * STAGE + A_BYTES, p.K % KEL, tid, 64 * NW);
+                asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            }
+        }
         compute(ring + cur * STAGE, kt);
     };
     // With NS = 2 and 4 waves the loop runs two tiles per trip, so that each

@@ -1,0 +1,449 @@
+// moe.cpp -- the entry points of the mixture-of-experts and 4-bit operators:
+// validation, kernel selection and launch (see include/dg.h for the contracts).
+#include <hip/hip_runtime_api.h>
+
+#include <algorithm>
+#include <initializer_list>
+
+#include "dg.h"
+#include "moe.hpp"
+#include "runtime.hpp"
+#include "view.hpp"
+
+namespace dg {
+namespace {
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+#define DG_TRY(expr) \
+    do { const dg_status st_ = (expr); if (st_ != DG_SUCCESS) return st_; } while (0)
+
+bool is_float(dg_dtype t) { return t == DG_F32 || t == DG_F16 || t == DG_BF16; }
+bool is_half(dg_dtype t) { return t == DG_F16 || t == DG_BF16; }
+
+// A vector of `len` 32-bit integers ([len] or [1][len]).
+dg_status index_vector(const dg_view *v, int64_t len, Mat *m) {
+    DG_TRY(canonicalize(v, m));
+    if (m->dtype != DG_I32) return DG_ERR_DTYPE;
+    if (m->rows * m->cols != len || (len > 0 && m->rows != 1)) return DG_ERR_SHAPE_MISMATCH;
+    return DG_SUCCESS;
+}
+
+// Elements one after another in row-major order.
+bool contiguous(const Mat &m) { return m.empty() || (m.cols_contig() && (m.rows <= 1 || m.rs == m.cols * m.esize)); }
+
+// A [E][rows][cols] view: one expert's matrix and the byte stride of experts.
+// span: the same matrix with the byte span of all experts.
+struct Stack {
+    Mat one;
+    int64_t E = 0, es = 0;
+    Mat span;
+};
+
+dg_status canonicalize_stack(const dg_view *v, Stack *s) {
+    if (!v) return DG_ERR_NULL;
+    if (v->ndim != 3) return DG_ERR_NDIM;
+    if (v->shape[0] < 0 || v->stride[0] < 0) return DG_ERR_STRIDE;
+    dg_view m = *v;
+    m.ndim = 2;
+    for (int d = 0; d < 2; ++d) {
+        m.shape[d] = v->shape[d + 1];
+        m.stride[d] = v->stride[d + 1];
+    }
+    if (v->shape[0] == 0) m.shape[0] = 0;   // no experts: nothing is read
+    DG_TRY(canonicalize(&m, &s->one));
+    if (v->shape[0] == 0) s->one.rows = v->shape[1];
+    if (v->stride[0] % s->one.esize != 0) return DG_ERR_STRIDE;
+    s->E = v->shape[0];
+    s->es = v->stride[0];
+    s->span = s->one;
+    int64_t reach;
+    if (s->E > 0 && !s->one.empty()) {
+        if (__builtin_mul_overflow(s->E - 1, s->es, &reach) ||
+            __builtin_add_overflow(s->one.hi, (uintptr_t)reach, &s->span.hi))
+            return DG_ERR_OVERFLOW;
+    }
+    return DG_SUCCESS;
+}
+
+// A written stack must not overlap itself: its matrices do not, and each starts
+// past the end of the one before.
+bool stack_overlaps(const Stack &s) {
+    if (s.E == 0 || s.one.empty()) return false;
+    return self_overlaps(s.one) || (s.E > 1 && s.es < (int64_t)(s.one.hi - s.one.lo));
+}
+
+dg_status ready(std::initializer_list<const Mat *> ms, Device *d) {
+    DG_TRY(current_device(d, true));
+    if (!d->gfx950) return DG_ERR_ARCH;
+    if (env_on("DG_CHECK_POINTERS"))
+        for (const Mat *m : ms)
+            if (m && m->ptr && m->hi > m->lo) DG_TRY(check_pointer(m->ptr));
+    return DG_SUCCESS;
+}
+
+dg_status done(hipError_t e, hipStream_t stream) {
+    if (e != hipSuccess) {
+        (void)hipGetLastError();
+        return DG_ERR_HIP;
+    }
+    if (env_on("DG_SYNC_DEBUG") && (hipStreamSynchronize(stream) != hipSuccess || hipGetLastError() != hipSuccess))
+        return DG_ERR_HIP;
+    return DG_SUCCESS;
+}
+
+char *out_ptr(const Mat &m) { return const_cast<char *>(m.ptr); }
+
+// ---------------------------------------------------------------- routing
+
+dg_status sort_entry(const dg_view *ids, int32_t E, const dg_view *offsets, const dg_view *order, const dg_view *pos,
+                     hipStream_t stream) {
+    Mat i, off, ord, p;
+    if (E < 1 || E > MOE_MAX_EXPERTS) return DG_ERR_INVALID_ARG;
+    DG_TRY(canonicalize(ids, &i));
+    if (i.dtype != DG_I32 && i.dtype != DG_I64) return DG_ERR_DTYPE;
+    const int64_t n = i.rows * i.cols;
+    if (n > INT32_MAX) return DG_ERR_OVERFLOW;
+    DG_TRY(index_vector(offsets, (int64_t)E + 1, &off));
+    DG_TRY(index_vector(order, n, &ord));
+    DG_TRY(canonicalize(pos, &p));
+    if (p.dtype != DG_I32) return DG_ERR_DTYPE;
+    if (p.rows != i.rows || p.cols != i.cols) return DG_ERR_SHAPE_MISMATCH;
+    if (!contiguous(off) || !contiguous(ord) || !contiguous(p)) return DG_ERR_UNSUPPORTED_VIEW;
+    if (spans_overlap(off, i) || spans_overlap(ord, i) || spans_overlap(p, i) || spans_overlap(off, ord) ||
+        spans_overlap(off, p) || spans_overlap(ord, p))
+        return DG_ERR_ALIAS;
+    Device d;
+    DG_TRY(ready({&i, &off, &ord, &p}, &d));
+    SortArgs a;
+    a.ids = i.ptr; a.i_rs = i.rs; a.i_cs = i.cs;
+    a.wide = i.dtype == DG_I64;
+    a.n = (int)n;
+    a.k = i.rows <= 1 || (i.cols > 0 && i.rs == i.cols * i.cs) ? 0 : (int)i.cols;   // 0: one run of n ids
+    if (a.k == 0 && i.cols == 1 && i.rows > 1) a.i_cs = i.rs;
+    a.E = E;
+    a.bits = 0;
+    while ((1 << a.bits) < E) ++a.bits;
+    a.offsets = reinterpret_cast<int *>(out_ptr(off));
+    a.order = reinterpret_cast<int *>(out_ptr(ord));
+    a.pos = reinterpret_cast<int *>(out_ptr(p));
+    a.blocks = (int)cdiv(n, SORT_BLOCK);
+    return done(launch_moe_sort(a, stream), stream);
+}
+
+dg_status gather_entry(const dg_view *X, const dg_view *order, int32_t k, const dg_view *Xs, hipStream_t stream) {
+    Mat x, o, y;
+    if (k < 1) return DG_ERR_INVALID_ARG;
+    DG_TRY(canonicalize(X, &x));
+    DG_TRY(canonicalize(Xs, &y));
+    if (!(is_float(x.dtype) || x.dtype == DG_F8E4M3) || y.dtype != x.dtype) return DG_ERR_DTYPE;
+    if (y.cols != x.cols) return DG_ERR_SHAPE_MISMATCH;
+    DG_TRY(index_vector(order, y.rows, &o));
+    if (x.rows > INT32_MAX || x.cols > INT32_MAX || y.rows > INT32_MAX) return DG_ERR_OVERFLOW;
+    if (self_overlaps(y)) return DG_ERR_STRIDE;
+    if (spans_overlap(y, x) || spans_overlap(y, o)) return DG_ERR_ALIAS;
+    if (y.empty()) return DG_SUCCESS;
+    Device d;
+    DG_TRY(ready({&x, &o, &y}, &d));
+    GatherArgs a;
+    a.X = x.ptr; a.x_rs = x.rs; a.x_cs = x.cs;
+    a.Y = out_ptr(y); a.y_rs = y.rs; a.y_cs = y.cs;
+    a.order = o.ptr; a.o_s = o.cs;
+    a.T = (int)x.rows; a.k = k; a.n = (int)y.rows; a.H = (int)y.cols; a.esize = y.esize;
+    a.vec = x.cols_contig() && y.cols_contig();
+    return done(launch_moe_gather(a, stream), stream);
+}
+
+// combine (grad false: Y is written) and its gradient (Y is dY, read)
+dg_status combine_entry(const dg_view *Ys, const dg_view *pos, const dg_view *w, const dg_view *Y, const dg_view *dYs,
+                        const dg_view *dw, bool grad, hipStream_t stream) {
+    Mat s, p, wt, y, ds, dv;
+    DG_TRY(canonicalize(Ys, &s));
+    DG_TRY(canonicalize(pos, &p));
+    DG_TRY(canonicalize(Y, &y));
+    if (w) DG_TRY(canonicalize(w, &wt));
+    if (grad) {
+        DG_TRY(canonicalize(dYs, &ds));
+        if (dw && !w) return DG_ERR_NULL;
+        if (dw) DG_TRY(canonicalize(dw, &dv));
+    }
+    if (!is_float(s.dtype) || y.dtype != s.dtype || p.dtype != DG_I32) return DG_ERR_DTYPE;
+    if (w && !is_float(wt.dtype)) return DG_ERR_DTYPE;
+    if (grad && (ds.dtype != s.dtype || (dw && dv.dtype != wt.dtype))) return DG_ERR_DTYPE;
+    if (y.cols != s.cols || p.rows != y.rows) return DG_ERR_SHAPE_MISMATCH;
+    if (w && (wt.rows != p.rows || wt.cols != p.cols)) return DG_ERR_SHAPE_MISMATCH;
+    if (grad && (ds.rows != s.rows || ds.cols != s.cols)) return DG_ERR_SHAPE_MISMATCH;
+    if (dw && (dv.rows != p.rows || dv.cols != p.cols)) return DG_ERR_SHAPE_MISMATCH;
+    if (s.rows > INT32_MAX || y.rows > INT32_MAX || y.cols > INT32_MAX || p.cols > INT32_MAX) return DG_ERR_OVERFLOW;
+    // what is written overlaps neither itself nor any other view
+    if (!grad) {
+        if (self_overlaps(y)) return DG_ERR_STRIDE;
+        if (spans_overlap(y, s) || spans_overlap(y, p) || spans_overlap(y, wt)) return DG_ERR_ALIAS;
+        if (y.empty()) return DG_SUCCESS;
+    } else {
+        if (self_overlaps(ds) || self_overlaps(dv)) return DG_ERR_STRIDE;
+        for (const Mat *o : {&ds, &dv})
+            for (const Mat *m : {&s, &p, &wt, &y})
+                if (spans_overlap(*o, *m)) return DG_ERR_ALIAS;
+        if (spans_overlap(ds, dv)) return DG_ERR_ALIAS;
+        if (ds.empty() && dv.empty()) return DG_SUCCESS;
+    }
+    Device d;
+    DG_TRY(ready({&s, &p, &wt, &y, &ds, &dv}, &d));
+    CombineArgs a = {};
+    a.Ys = s.ptr; a.s_rs = s.rs; a.s_cs = s.cs;
+    a.Y = out_ptr(y); a.y_rs = y.rs; a.y_cs = y.cs;
+    a.pos = p.ptr; a.p_rs = p.rs; a.p_cs = p.cs;
+    if (w) { a.w = wt.ptr; a.w_rs = wt.rs; a.w_cs = wt.cs; a.w_kind = wt.dtype; }
+    a.T = (int)y.rows; a.k = (int)p.cols; a.R = (int)s.rows; a.H = (int)s.cols;
+    a.vec = s.cols_contig() && y.cols_contig();
+    if (!grad) return done(launch_moe_combine(s.dtype, a, stream), stream);
+    a.dYs = out_ptr(ds); a.d_rs = ds.rs; a.d_cs = ds.cs;
+    if (dw) { a.dw = out_ptr(dv); a.g_rs = dv.rs; a.g_cs = dv.cs; }
+    a.vec = a.vec && ds.cols_contig();
+    return done(launch_moe_combine_grad(s.dtype, a, stream), stream);
+}
+
+// ---------------------------------------------------------------- expert products
+
+struct OpLayout {
+    int mode = KMAJ;
+    bool dtl = false, vec = false;   // what the loaders ask of the operand
+};
+
+// An operand whose rows (extent `rows`, `rs` bytes apart) are summed along k.
+// aligned: every further base offset (experts) is a multiple of 16 bytes.
+OpLayout layout(const char *ptr, int64_t rows, int64_t rs, int64_t k, int64_t ks, bool aligned) {
+    OpLayout o;
+    const bool base = reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && aligned;
+    // lane offsets within a 256-row, 64-element tile stay below 2^31
+    const bool near = 256 * rs + 64 * ks < ((int64_t)1 << 31);
+    if (ks == 2 || k <= 1) {
+        o.mode = KMAJ;
+        o.vec = k >= 8;
+        o.dtl = base && near && ks == 2 && rs % 16 == 0 && k % 8 == 0;
+    } else if (rs == 2 || rows <= 1) {
+        o.mode = MNMAJ;
+        o.vec = rows >= 8;
+        o.dtl = base && near && rs == 2 && ks % 16 == 0 && rows % 8 == 0;
+    }
+    return o;
+}
+
+Epilogue plain_epilogue(const Mat &c, int act, bool aligned) {
+    Epilogue e = {};
+    e.C = out_ptr(c);
+    e.c_rs = c.rs;
+    e.c_cs = c.cs;
+    e.out_kind = c.dtype;
+    e.alpha = 1.0f;
+    e.beta = 0.0f;
+    e.act = act;
+    const int64_t v = 4 * c.esize;
+    e.vec4 = aligned && c.cs == c.esize && reinterpret_cast<uintptr_t>(c.ptr) % v == 0 && (c.rows <= 1 || c.rs % v == 0);
+    return e;
+}
+
+hipError_t launch_product(int in_kind, int load, int tile, int b_mode, bool wgrad, const MoeArgs &a, int64_t units,
+                          hipStream_t s) {
+    return in_kind == IN_F16 ? launch_moe_gemm_f16(load, tile, b_mode, wgrad, a, units, s)
+                             : launch_moe_gemm_bf16(load, tile, b_mode, wgrad, a, units, s);
+}
+
+int tile_rows(int load, int tile) { return load == MOE_DTL && tile == T64x128 ? 32 : mfma_tile_bm(tile); }
+int tile_cols(int tile) { return mfma_tile_bn(tile); }
+
+dg_status moe_gemm_entry(const dg_view *A, const dg_view *offsets, const dg_view *W, const dg_view *C, int act,
+                         hipStream_t stream) {
+    Mat x, off, c;
+    Stack w;
+    DG_TRY(canonicalize(A, &x));
+    DG_TRY(canonicalize_stack(W, &w));
+    DG_TRY(canonicalize(C, &c));
+    if (!is_half(x.dtype) || w.one.dtype != x.dtype || !is_float(c.dtype)) return DG_ERR_DTYPE;
+    if (w.E < 1 || w.one.rows != x.cols || c.rows != x.rows || c.cols != w.one.cols) return DG_ERR_SHAPE_MISMATCH;
+    DG_TRY(index_vector(offsets, w.E + 1, &off));
+    const int64_t n = x.rows, K = x.cols, N = c.cols;
+    if (n > INT32_MAX || K > INT32_MAX || N > INT32_MAX || w.E > INT32_MAX / 2) return DG_ERR_OVERFLOW;
+    if (act != DG_ACT_NONE && act != DG_ACT_RELU && act != DG_ACT_GELU_TANH) return DG_ERR_INVALID_ARG;
+    if (self_overlaps(c)) return DG_ERR_STRIDE;
+    if (spans_overlap(c, x) || spans_overlap(c, w.span) || spans_overlap(c, off)) return DG_ERR_ALIAS;
+    if (c.empty()) return DG_SUCCESS;
+    Device d;
+    DG_TRY(ready({&x, &off, &w.span, &c}, &d));
+
+    const OpLayout la = layout(x.ptr, n, x.rs, K, x.cs, true);
+    const OpLayout lb = layout(w.one.ptr, N, w.one.cs, K, w.one.rs, w.es % 16 == 0 || w.E == 1);
+    int load = MOE_ELEM;
+    if (la.mode == KMAJ && la.vec && lb.vec) load = la.dtl && lb.dtl ? MOE_DTL : MOE_VEC;
+    // Tile rows by the mean count of the experts that can have rows.
+    const int64_t used = std::min(w.E, n), mean = n / std::max<int64_t>(used, 1);
+    int tile = T64x64;
+    if (load == MOE_DTL) tile = mean <= 48 ? T64x128 : mean <= 192 ? T128x128 : T256x256;
+    else if (load == MOE_VEC) tile = mean <= 64 ? T64x64 : T128x128;
+    const int bm = tile_rows(load, tile), bn = tile_cols(tile);
+
+    MoeArgs a = {};
+    a.p.a = Operand{x.ptr, x.rs, x.cs, 1};
+    a.p.b = Operand{w.one.ptr, w.one.cs, w.one.rs, 1};
+    a.p.epi = plain_epilogue(c, act, true);
+    a.p.N = (int)N; a.p.K = (int)K;
+    a.p.tiles_n = (int)cdiv(N, bn);
+    a.p.ktiles = (int)cdiv(K, 64);
+    a.p.splits = 1;
+    a.p.group_m = tile == T256x256 ? 4 : 8;
+    a.offsets = off.ptr; a.o_s = off.cs;
+    a.E = (int)w.E; a.n = (int)n;
+    a.e_bs = w.es;
+    // every group with rows (the experts and the rows of none) ends in a partial tile at most
+    const int64_t units = ((n + std::min(w.E + 1, n) * (bm - 1)) / bm) * a.p.tiles_n;
+    if (units > INT32_MAX) return DG_ERR_OVERFLOW;
+    return done(launch_product(x.dtype == DG_F16 ? IN_F16 : IN_BF16, load, tile, lb.mode, false, a, units, stream), stream);
+}
+
+dg_status moe_wgrad_entry(const dg_view *A, const dg_view *D, const dg_view *offsets, const dg_view *dW,
+                          hipStream_t stream) {
+    Mat x, g, off;
+    Stack w;
+    DG_TRY(canonicalize(A, &x));
+    DG_TRY(canonicalize(D, &g));
+    DG_TRY(canonicalize_stack(dW, &w));
+    if (!is_half(x.dtype) || g.dtype != x.dtype || !is_float(w.one.dtype)) return DG_ERR_DTYPE;
+    if (w.E < 1 || g.rows != x.rows || w.one.rows != x.cols || w.one.cols != g.cols) return DG_ERR_SHAPE_MISMATCH;
+    DG_TRY(index_vector(offsets, w.E + 1, &off));
+    const int64_t n = x.rows, K = x.cols, N = g.cols;
+    if (n > INT32_MAX || K > INT32_MAX || N > INT32_MAX || w.E > INT32_MAX / 2) return DG_ERR_OVERFLOW;
+    if (stack_overlaps(w)) return DG_ERR_STRIDE;
+    if (spans_overlap(w.span, x) || spans_overlap(w.span, g) || spans_overlap(w.span, off)) return DG_ERR_ALIAS;
+    if (w.one.empty()) return DG_SUCCESS;
+    Device d;
+    DG_TRY(ready({&x, &g, &off, &w.span}, &d));
+
+    // dW[e] is a product summed over rows: A's columns are its rows
+    const OpLayout la = layout(x.ptr, K, x.cs, n, x.rs, true), lb = layout(g.ptr, N, g.cs, n, g.rs, true);
+    int load = MOE_ELEM;
+    if (x.cs == 2 && g.cs == 2 && K >= 8 && N >= 8)
+        load = la.mode == MNMAJ && lb.mode == MNMAJ && la.dtl && lb.dtl ? MOE_DTL : MOE_VEC;
+    int tile = load == MOE_ELEM ? T64x64 : T128x128;
+    if (load == MOE_DTL && w.E * cdiv(K, 256) * cdiv(N, 256) >= d.cus) tile = T256x256;
+    if (load == MOE_VEC && w.E * cdiv(K, 128) * cdiv(N, 128) < d.cus) tile = T64x64;
+    const int bm = mfma_tile_bm(tile), bn = mfma_tile_bn(tile);
+
+    MoeArgs a = {};
+    a.p.a = Operand{x.ptr, x.cs, x.rs, 1};
+    a.p.b = Operand{g.ptr, g.cs, g.rs, 1};
+    a.p.epi = plain_epilogue(w.one, DG_ACT_NONE, w.E == 1 || w.es % (4 * w.one.esize) == 0);
+    a.p.M = (int)K; a.p.N = (int)N;
+    a.p.tiles_m = (int)cdiv(K, bm); a.p.tiles_n = (int)cdiv(N, bn);
+    a.p.splits = 1;
+    a.p.group_m = tile == T256x256 ? 4 : 8;
+    a.offsets = off.ptr; a.o_s = off.cs;
+    a.E = (int)w.E; a.n = (int)n;
+    a.e_cs = w.es;
+    const int64_t tiles = (int64_t)a.p.tiles_m * a.p.tiles_n;
+    if (tiles > INT32_MAX || tiles * w.E > INT32_MAX) return DG_ERR_OVERFLOW;
+    return done(launch_product(x.dtype == DG_F16 ? IN_F16 : IN_BF16, load, tile, lb.mode, true, a, tiles * w.E, stream), stream);
+}
+
+// ---------------------------------------------------------------- 4-bit weights
+
+dg_status w4_entry(const dg_view *A, const dg_view *offsets, const dg_view *Q, const dg_view *S, const dg_view *Z,
+                   const dg_view *C, int32_t group, int act, bool experts, hipStream_t stream) {
+    Mat x, c, off;
+    Stack q, s, z;
+    DG_TRY(canonicalize(A, &x));
+    DG_TRY(canonicalize(C, &c));
+    if (experts) {
+        DG_TRY(canonicalize_stack(Q, &q));
+        DG_TRY(canonicalize_stack(S, &s));
+        if (Z) DG_TRY(canonicalize_stack(Z, &z));
+    } else {
+        DG_TRY(canonicalize(Q, &q.one));
+        DG_TRY(canonicalize(S, &s.one));
+        if (Z) DG_TRY(canonicalize(Z, &z.one));
+        for (Stack *t : {&q, &s, &z}) { t->E = 1; t->span = t->one; }
+    }
+    if (!is_half(x.dtype) || !is_float(c.dtype) || q.one.dtype != DG_U8 || !is_float(s.one.dtype)) return DG_ERR_DTYPE;
+    if (Z && z.one.dtype != DG_U8) return DG_ERR_DTYPE;
+    if (group < 32 || group % 32 != 0) return DG_ERR_INVALID_ARG;
+    if (act != DG_ACT_NONE && act != DG_ACT_RELU && act != DG_ACT_GELU_TANH) return DG_ERR_INVALID_ARG;
+    const int64_t M = x.rows, K = x.cols, N = c.cols, groups = cdiv(K, group);
+    if (c.rows != M || q.one.rows != N || q.one.cols != cdiv(K, 2)) return DG_ERR_SHAPE_MISMATCH;
+    if (q.E < 1 || s.E != q.E || s.one.rows != N || s.one.cols != groups) return DG_ERR_SHAPE_MISMATCH;
+    if (Z && (z.E != q.E || z.one.rows != N || z.one.cols != groups)) return DG_ERR_SHAPE_MISMATCH;
+    if (experts) DG_TRY(index_vector(offsets, q.E + 1, &off));
+    if (M > INT32_MAX || K > INT32_MAX / 4 || N > INT32_MAX || q.E > INT32_MAX / 2) return DG_ERR_OVERFLOW;
+    if (!x.cols_contig() || !q.one.cols_contig()) return DG_ERR_UNSUPPORTED_VIEW;
+    // lane offsets within a workgroup's rows and columns are 32-bit
+    const int64_t lim = ((int64_t)1 << 31) / 64;
+    if (x.rs >= lim || q.one.rs >= lim || s.one.rs >= lim || z.one.rs >= lim) return DG_ERR_OVERFLOW;
+    if (self_overlaps(c)) return DG_ERR_STRIDE;
+    for (const Mat *m : {&x, &q.span, &s.span, &z.span, &off})
+        if (spans_overlap(c, *m)) return DG_ERR_ALIAS;
+    if (c.empty()) return DG_SUCCESS;
+    Device d;
+    DG_TRY(ready({&x, &off, &q.span, &s.span, &z.span, &c}, &d));
+
+    W4Args a = {};
+    a.A = x.ptr; a.a_rs = x.rs;
+    a.Q = q.one.ptr; a.q_rs = q.one.rs; a.q_es = q.es;
+    a.S = s.one.ptr; a.s_rs = s.one.rs; a.s_cs = s.one.cs; a.s_es = s.es;
+    if (Z) { a.Z = z.one.ptr; a.z_rs = z.one.rs; a.z_cs = z.one.cs; a.z_es = z.es; }
+    a.s_kind = s.one.dtype;
+    a.C = out_ptr(c); a.c_rs = c.rs; a.c_cs = c.cs; a.out_kind = c.dtype; a.act = act;
+    a.M = (int)M; a.N = (int)N; a.K = (int)K; a.G = group;
+    if (experts) { a.offsets = off.ptr; a.o_s = off.cs; }
+    a.E = (int)q.E;
+    a.slabs = (int)cdiv(N, W4_COLS);
+    a.s_vec = s.one.cols_contig() && (!Z || z.one.cols_contig()) && (group == 32 || group == 64 || group % 128 == 0);
+    const int64_t used = experts ? std::min(q.E, M) : 1, mean = M / std::max<int64_t>(used, 1);
+    const int tm = mean <= 16 ? 1 : 2, bm = 16 * tm;
+    const int64_t tiles_m = experts ? (M + std::min(q.E + 1, M) * (bm - 1)) / bm : cdiv(M, bm);
+    if (tiles_m * a.slabs > INT32_MAX) return DG_ERR_OVERFLOW;
+    return done(launch_w4(x.dtype == DG_F16 ? IN_F16 : IN_BF16, tm, a, tiles_m * a.slabs, stream), stream);
+}
+
+}  // namespace
+}  // namespace dg
+
+extern "C" {
+
+dg_status dg_moe_sort(const dg_view *ids, int32_t E, const dg_view *offsets, const dg_view *order, const dg_view *pos,
+                      hipStream_t stream) {
+    return dg::sort_entry(ids, E, offsets, order, pos, stream);
+}
+
+dg_status dg_moe_gather(const dg_view *X, const dg_view *order, int32_t k, const dg_view *Xs, hipStream_t stream) {
+    return dg::gather_entry(X, order, k, Xs, stream);
+}
+
+dg_status dg_moe_combine(const dg_view *Ys, const dg_view *pos, const dg_view *w, const dg_view *Y, hipStream_t stream) {
+    return dg::combine_entry(Ys, pos, w, Y, nullptr, nullptr, false, stream);
+}
+
+dg_status dg_moe_combine_grad(const dg_view *dY, const dg_view *Ys, const dg_view *pos, const dg_view *w,
+                              const dg_view *dYs, const dg_view *dw, hipStream_t stream) {
+    return dg::combine_entry(Ys, pos, w, dY, dYs, dw, true, stream);
+}
+
+dg_status dg_moe_gemm(const dg_view *A, const dg_view *offsets, const dg_view *W, const dg_view *C, dg_act act,
+                      hipStream_t stream) {
+    return dg::moe_gemm_entry(A, offsets, W, C, (int)act, stream);
+}
+
+dg_status dg_moe_gemm_wgrad(const dg_view *A, const dg_view *D, const dg_view *offsets, const dg_view *dW,
+                            hipStream_t stream) {
+    return dg::moe_wgrad_entry(A, D, offsets, dW, stream);
+}
+
+dg_status dg_gemm_w4(const dg_view *A, const dg_view *Q, const dg_view *S, const dg_view *Z, const dg_view *C,
+                     int32_t group, dg_act act, hipStream_t stream) {
+    return dg::w4_entry(A, nullptr, Q, S, Z, C, group, (int)act, false, stream);
+}
+
+dg_status dg_moe_gemm_w4(const dg_view *A, const dg_view *offsets, const dg_view *Q, const dg_view *S,
+                         const dg_view *Z, const dg_view *C, int32_t group, dg_act act, hipStream_t stream) {
+    return dg::w4_entry(A, offsets, Q, S, Z, C, group, (int)act, true, stream);
+}
+
+}  // extern "C"

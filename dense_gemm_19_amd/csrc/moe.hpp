@@ -1,0 +1,103 @@
+// moe.hpp -- argument blocks and launchers of the mixture-of-experts operators
+// (host and device).  All strides are in bytes.
+#pragma once
+#include <cstdint>
+
+#include <hip/hip_runtime_api.h>
+
+#include "kernels.hpp"
+
+namespace dg {
+
+// ---------------------------------------------------------------- routing (moe_route.hip)
+
+constexpr int MOE_MAX_EXPERTS = 2048;    // LDS counters of a sort workgroup: 16 waves x E
+constexpr int SORT_ONE_MAX = 16384;      // ids sorted by one workgroup; more take three launches
+constexpr int SORT_BLOCK = 4096;         // ids per workgroup of the three-launch sort (at least E fit half of it)
+
+struct SortArgs {
+    const char *ids; int64_t i_rs, i_cs;   // [T][k]
+    int wide;                              // ids are 64-bit integers
+    int k, n;                              // n = T * k
+    int E, bits;                           // E < 2^bits + 1: every expert id fits `bits` bits
+    int *offsets, *order, *pos;            // contiguous: [E + 1], [n], [T][k]
+    int blocks;                            // workgroups of the three-launch sort
+};
+
+struct GatherArgs {
+    const char *X; int64_t x_rs, x_cs;     // [T][H]
+    char *Y; int64_t y_rs, y_cs;           // [n][H]
+    const char *order; int64_t o_s;        // [n] int32
+    int T, k, n, H, esize;
+    int vec;                               // both operands' rows are contiguous
+};
+
+// combine (Y = sum of w * Ys) and its gradient (dYs = w * dY, dw = <dY, Ys>)
+struct CombineArgs {
+    const char *Ys; int64_t s_rs, s_cs;    // [R][H]
+    char *Y; int64_t y_rs, y_cs;           // [T][H]: written by combine, read by its gradient
+    const char *pos; int64_t p_rs, p_cs;   // [T][k] int32
+    const char *w; int64_t w_rs, w_cs;     // [T][k], or null (weights of 1)
+    int w_kind;                            // OutKind numbering
+    char *dYs; int64_t d_rs, d_cs;         // gradient: [R][H]
+    char *dw; int64_t g_rs, g_cs;          // gradient: [T][k] in w_kind, or null
+    int T, k, R, H;
+    int vec;                               // every operand's rows are contiguous
+    int zero_blocks, zero_rows;            // gradient: workgroups that clear unnamed rows, rows of each
+};
+
+hipError_t launch_moe_sort(const SortArgs &a, hipStream_t stream);
+hipError_t launch_moe_gather(const GatherArgs &a, hipStream_t stream);
+// kind: OutKind numbering of Ys, Y and dYs
+hipError_t launch_moe_combine(int kind, const CombineArgs &a, hipStream_t stream);
+hipError_t launch_moe_combine_grad(int kind, const CombineArgs &a, hipStream_t stream);
+
+// ---------------------------------------------------------------- expert products (moe_gemm.hpp)
+
+// p describes one expert's product with the whole operands' pointers; the
+// kernel adds the expert's offsets.  Forward: A's rows are grouped (M is the
+// expert's row count), B moves by e_bs per expert.  Weight gradient (wgrad): K
+// is the expert's row count, C moves by e_cs per expert.
+struct MoeArgs {
+    MfmaArgs p;
+    const char *offsets; int64_t o_s;      // [E + 1] int32
+    int E, n;                              // experts, grouped rows
+    int64_t e_bs, e_cs;                    // bytes per expert of B (forward) and C (wgrad)
+};
+
+// Loaders of the expert products.
+//  MOE_DTL : direct HBM -> LDS loads (gemm_dtl.hpp): 16-byte aligned chunks.
+//  MOE_VEC : register-staged 16-byte loads at any alignment; the operands are
+//            contiguous along one of their dims, at least 8 long.
+//  MOE_ELEM: element loads, any strides.
+enum MoeLoad : int { MOE_DTL = 0, MOE_VEC = 1, MOE_ELEM = 2 };
+
+// tile: MfmaTile (T64x128 here stands for the 32 x 128 tile of MOE_DTL).
+// units: an upper bound of the work units (forward) or their number (wgrad).
+hipError_t launch_moe_gemm_f16(int load, int tile, int b_mode, bool wgrad, const MoeArgs &a, int64_t units,
+                               hipStream_t stream);
+hipError_t launch_moe_gemm_bf16(int load, int tile, int b_mode, bool wgrad, const MoeArgs &a, int64_t units,
+                                hipStream_t stream);
+
+// ---------------------------------------------------------------- 4-bit weights (w4.hip)
+
+struct W4Args {
+    const char *A; int64_t a_rs;           // [M][K] 16-bit, K-contiguous
+    const char *Q; int64_t q_rs, q_es;     // [E][N][ceil(K/2)] bytes, K-contiguous
+    const char *S; int64_t s_rs, s_cs, s_es;   // [E][N][ceil(K/G)]
+    const char *Z; int64_t z_rs, z_cs, z_es;   // [E][N][ceil(K/G)] bytes, or null (8)
+    int s_kind;                            // OutKind numbering
+    char *C; int64_t c_rs, c_cs;
+    int out_kind, act;
+    int M, N, K, G;
+    const char *offsets; int64_t o_s; int E;   // offsets null: one group of all M rows
+    int slabs;                             // column slabs
+    int s_vec;                             // a window's groups are adjacent in S's and Z's rows
+};
+
+constexpr int W4_COLS = 32;   // columns of a workgroup
+
+// tm: rows of a workgroup / 16 (1 or 2)
+hipError_t launch_w4(int in_kind, int tm, const W4Args &a, int64_t units, hipStream_t stream);
+
+}  // namespace dg

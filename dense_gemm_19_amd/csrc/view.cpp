@@ -7,7 +7,9 @@ int esize_of(dg_dtype t) {
     switch (t) {
     case DG_F32: return 4;
     case DG_F16: case DG_BF16: return 2;
-    case DG_F8E4M3: return 1;
+    case DG_F8E4M3: case DG_U8: return 1;
+    case DG_I32: return 4;
+    case DG_I64: return 8;
     }
     return 0;
 }

@@ -69,7 +69,10 @@ typedef enum {
     DG_F32 = 0,
     DG_F16 = 1,     /* IEEE binary16 */
     DG_BF16 = 2,    /* bfloat16 */
-    DG_F8E4M3 = 3   /* OCP E4M3FN: bias 7, 3 mantissa bits, max 448, no Inf */
+    DG_F8E4M3 = 3,  /* OCP E4M3FN: bias 7, 3 mantissa bits, max 448, no Inf */
+    DG_I32 = 4,     /* 32-bit integers (expert ids, offsets and places) */
+    DG_I64 = 5,     /* 64-bit integers (expert ids) */
+    DG_U8 = 6       /* bytes (two 4-bit codes each, or zero points) */
 } dg_dtype;
 
 typedef enum {
@@ -373,6 +376,111 @@ typedef enum { DG_QUANT_TOKEN = 0, DG_QUANT_BLOCK = 1 } dg_quant_mode;
 
 dg_status dg_quant_fp8(const dg_view *X, const dg_view *Q, const dg_view *S, dg_quant_mode mode,
                        hipStream_t stream);
+
+/*
+ * Mixture of experts and 4-bit weights.
+ *
+ * The experts of an MoE layer are small products whose row counts only the
+ * router's output decides ("DeepGEMM is not a new model" article, cf-1.com,
+ * section 1: 8 experts per token).  dg_gemm_grouped needs those counts on the
+ * host; the entry points below take them from device memory, so that a layer
+ * runs without a copy to the host: sort the router's choices, copy the tokens'
+ * rows into expert order, multiply each expert's rows by its weights, and add
+ * the results back in token order; with the gradients of all of it.
+ *
+ *   T tokens, k choices each, E experts, n = T * k.
+ *   offsets  [E + 1]  int32: expert e has rows offsets[e] .. offsets[e+1] - 1
+ *   order    [n]      int32: the choice t * k + j that row r holds, or -1
+ *   pos      [T][k]   int32: the row of choice (t, j), or -1
+ *
+ * Index tensors are read on the device.  A value outside its range reaches no
+ * memory: a dropped choice.  Conventions as for the GEMM entry points
+ * (asynchronous on `stream`, outputs untouched on error, no scratch memory, no
+ * atomics on floating-point values: results are bitwise reproducible).  Every
+ * one may be captured in a HIP graph.  Views of index vectors are [len] or
+ * [1][len].
+ */
+
+/* Sort the router's choices by expert, stably (equal experts keep the order of
+ * t * k + j).
+ *   ids      [T][k] DG_I32 or DG_I64 (any strides); an id outside 0 .. E - 1 is
+ *            dropped: its pos is -1.
+ *   E        1 .. 2048.
+ *   offsets, order, pos: written; DG_I32, contiguous.  order[r] is -1 for the
+ *            rows from offsets[E] on.
+ * Errors: DG_ERR_INVALID_ARG (E), DG_ERR_DTYPE, DG_ERR_SHAPE_MISMATCH,
+ * DG_ERR_UNSUPPORTED_VIEW (an output is not contiguous), DG_ERR_OVERFLOW (n
+ * above 2^31 - 1), DG_ERR_ALIAS (an output overlaps another view), view errors. */
+dg_status dg_moe_sort(const dg_view *ids, int32_t E, const dg_view *offsets, const dg_view *order,
+                      const dg_view *pos, hipStream_t stream);
+
+/* Xs[r] <- X[order[r] / k], a row of zeros where order[r] is outside 0 .. T*k - 1.
+ *   X [T][H], Xs [n][H]: one dtype (DG_F32, DG_F16, DG_BF16 or DG_F8E4M3), any
+ *   strides; order [n] DG_I32, any stride; k >= 1.
+ * The gradient with respect to X is dg_moe_combine of dXs without weights.
+ * Errors: DG_ERR_INVALID_ARG (k), DG_ERR_DTYPE, DG_ERR_SHAPE_MISMATCH,
+ * DG_ERR_STRIDE / DG_ERR_ALIAS (Xs overlaps itself or an input), DG_ERR_OVERFLOW. */
+dg_status dg_moe_gather(const dg_view *X, const dg_view *order, int32_t k, const dg_view *Xs,
+                        hipStream_t stream);
+
+/* Y[t] <- sum over j of w[t][j] * Ys[pos[t][j]], in FP32 in the order of j, rounded
+ * once to Y's dtype.  A choice whose pos is outside Ys adds nothing.
+ *   Ys [R][H], Y [T][H]: one dtype, DG_F32, DG_F16 or DG_BF16, any strides.
+ *   pos [T][k] DG_I32; w [T][k] DG_F32, DG_F16 or DG_BF16, or NULL (weights of 1);
+ *   any strides.
+ * Errors as for dg_moe_gather. */
+dg_status dg_moe_combine(const dg_view *Ys, const dg_view *pos, const dg_view *w, const dg_view *Y,
+                         hipStream_t stream);
+
+/* The gradient of dg_moe_combine, given dY:
+ *   dYs[pos[t][j]] <- w[t][j] * dY[t]      (rows of dYs that no pos names: zero)
+ *   dw[t][j]       <- <dY[t], Ys[pos[t][j]]>, summed in FP32 (0 for a dropped choice)
+ *   dY [T][H], Ys and dYs [R][H]: one dtype, DG_F32, DG_F16 or DG_BF16; pos and w
+ *   as above, no two places equal (as dg_moe_sort writes them); dw [T][k] of w's
+ *   dtype.  dw may be NULL (not wanted), and has to be where w is.
+ * Errors as for dg_moe_combine, and DG_ERR_NULL (dw without w). */
+dg_status dg_moe_combine_grad(const dg_view *dY, const dg_view *Ys, const dg_view *pos, const dg_view *w,
+                              const dg_view *dYs, const dg_view *dw, hipStream_t stream);
+
+/* C[r] <- act(A[r] * W[e]) for every expert e and its rows r; rows from offsets[E]
+ * on are set to zero (rows before offsets[0], which dg_moe_sort never leaves, are
+ * not touched).  FP32 accumulation, one rounding to C's dtype.
+ *   A [n][K] and W [E][K][N]: both DG_F16 or both DG_BF16; W's three strides are
+ *   free, so that W's transpose (the gradient with respect to A: dA = dC * W^T) is
+ *   a view.  C [n][N] DG_F32, DG_F16 or DG_BF16.  offsets [E + 1] DG_I32.
+ *   act: a dg_act value.
+ * Errors: DG_ERR_NDIM (W not 3-D), DG_ERR_INVALID_ARG (act), DG_ERR_DTYPE,
+ * DG_ERR_SHAPE_MISMATCH, DG_ERR_STRIDE, DG_ERR_ALIAS, DG_ERR_OVERFLOW (more than
+ * 2^31 - 1 tiles), view errors. */
+dg_status dg_moe_gemm(const dg_view *A, const dg_view *offsets, const dg_view *W, const dg_view *C, dg_act act,
+                      hipStream_t stream);
+
+/* dW[e] <- sum over expert e's rows of A[r]^T * D[r] (zero for an expert without rows).
+ *   A [n][K] and D [n][N]: both DG_F16 or both DG_BF16; dW [E][K][N] DG_F32, DG_F16
+ *   or DG_BF16.  Otherwise as dg_moe_gemm. */
+dg_status dg_moe_gemm_wgrad(const dg_view *A, const dg_view *D, const dg_view *offsets, const dg_view *dW,
+                            hipStream_t stream);
+
+/* C <- act(A * W^T) with 4-bit weights in groups along K:
+ *   W[n][k] = S[n][k / group] * (q[n][k] - z[n][k / group])
+ *   A [M][K] DG_F16 or DG_BF16, K-contiguous.
+ *   Q [N][ceil(K / 2)] DG_U8: code k in the low (k even) or high (k odd) half of
+ *     byte k / 2; bytes of a row contiguous.
+ *   S [N][ceil(K / group)] DG_F32, DG_F16 or DG_BF16; Z the same shape, DG_U8 (any
+ *     value 0 .. 255), or NULL: 8.
+ *   group: a positive multiple of 32.  C [M][N] DG_F32, DG_F16 or DG_BF16.
+ * q - z enters the products exactly; each group's sum is formed in FP32 and then
+ * multiplied by its scale.
+ * Errors: DG_ERR_INVALID_ARG (group, act), DG_ERR_DTYPE, DG_ERR_SHAPE_MISMATCH,
+ * DG_ERR_UNSUPPORTED_VIEW (A's or Q's rows not contiguous), DG_ERR_STRIDE,
+ * DG_ERR_ALIAS, DG_ERR_OVERFLOW, view errors. */
+dg_status dg_gemm_w4(const dg_view *A, const dg_view *Q, const dg_view *S, const dg_view *Z, const dg_view *C,
+                     int32_t group, dg_act act, hipStream_t stream);
+
+/* The same for the experts of a mixture: C[r] <- act(A[r] * W[e]^T) with
+ * Q [E][N][ceil(K / 2)], S and Z [E][N][ceil(K / group)] and rows as in dg_moe_gemm. */
+dg_status dg_moe_gemm_w4(const dg_view *A, const dg_view *offsets, const dg_view *Q, const dg_view *S,
+                         const dg_view *Z, const dg_view *C, int32_t group, dg_act act, hipStream_t stream);
 
 /* Helper (no page passage): static, human-readable name of a status code
  * ("DG_ERR_ALIAS", ...); "DG_ERR_UNKNOWN" for a value outside dg_status. */
