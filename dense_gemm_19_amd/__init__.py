@@ -21,7 +21,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 
 import torch
 
@@ -117,14 +116,6 @@ def lib() -> ctypes.CDLL:
         L.dg_calib_read.argtypes = [ctypes.c_void_p, ctypes.c_size_t, D, ctypes.c_void_p]
         L.dg_calib_launch.argtypes = [D, ctypes.c_void_p]
         for f in ("dg_calib_mfma", "dg_calib_read", "dg_calib_launch"):
-            getattr(L, f).restype = ctypes.c_int
-        B, I, S = ctypes.c_char_p, ctypes.c_int32, ctypes.c_void_p   # B: a packed dg_view (_packed)
-        for f, args in (("dg_moe_sort", [B, I, B, B, B, S]), ("dg_moe_gather", [B, B, I, B, S]),
-                        ("dg_moe_combine", [B, B, B, B, S]), ("dg_moe_combine_grad", [B, B, B, B, B, B, S]),
-                        ("dg_moe_gemm", [B, B, B, B, ctypes.c_int, S]), ("dg_moe_gemm_wgrad", [B, B, B, B, S]),
-                        ("dg_gemm_w4", [B, B, B, B, B, I, ctypes.c_int, S]),
-                        ("dg_moe_gemm_w4", [B, B, B, B, B, B, I, ctypes.c_int, S])):
-            getattr(L, f).argtypes = args
             getattr(L, f).restype = ctypes.c_int
         L.dg_status_str.argtypes = [ctypes.c_int]
         L.dg_status_str.restype = ctypes.c_char_p
@@ -334,19 +325,22 @@ def quant_fp8(X: torch.Tensor, Q: torch.Tensor, S: torch.Tensor, mode: int = DG_
 
 # ---- mixture of experts and 4-bit weights
 
-_PACK = {d: struct.Struct(f"Pi4x{d}q{32 - 8 * d}x{d}q{32 - 8 * d}xi4x").pack for d in range(1, 5)}
+_bound = None
 
 
-def _packed(t: torch.Tensor) -> bytes:
-    """view_of(t) as the bytes of a dg_view (the quick form: one call packs it)."""
-    if t.dtype not in _DTYPE:
-        raise TypeError(f"unsupported dtype {t.dtype}")
-    if t.dim() == 0:
-        t = t.reshape(1)
-    shape, es = t.shape, t.element_size()
-    if len(shape) > 4:
-        raise ValueError("views have at most 4 dims")
-    return _PACK[len(shape)](t.data_ptr(), len(shape), *shape, *[s * es for s in t.stride()], _DTYPE[t.dtype])
+def _bind():
+    """The loaded tensor binding (_dgtorch.so, beside libdg.so; raises if it has not been built)."""
+    global _bound
+    if _bound is None:
+        lib()
+        from . import _dgtorch
+        _bound = _dgtorch
+    return _bound
+
+
+def _raw(stream):
+    """A stream argument for the binding: None (torch's current stream) or the stream's handle."""
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
 
 
 def moe_sort(ids: torch.Tensor, E: int, offsets: torch.Tensor, order: torch.Tensor, pos: torch.Tensor,
@@ -357,23 +351,21 @@ def moe_sort(ids: torch.Tensor, E: int, offsets: torch.Tensor, order: torch.Tens
     offsets[e]..offsets[e+1]-1, row r holds choice order[r] = t * k + j, and pos[t, j] is its row (-1: none).
     Returns (offsets, order, pos).
     """
-    _check(lib().dg_moe_sort(_packed(ids), E, _packed(offsets), _packed(order), _packed(pos), _stream(stream)),
-           "dg_moe_sort")
+    _check(_bind().moe_sort(ids, E, offsets, order, pos, _raw(stream)), "dg_moe_sort")
     return offsets, order, pos
 
 
 def moe_gather(X: torch.Tensor, order: torch.Tensor, k: int, Xs: torch.Tensor, stream=None) -> torch.Tensor:
     """Xs[r] <- X[order[r] // k], zeros where order[r] names no choice; returns Xs.
     The gradient of X is moe_combine of dXs without weights."""
-    _check(lib().dg_moe_gather(_packed(X), _packed(order), k, _packed(Xs), _stream(stream)), "dg_moe_gather")
+    _check(_bind().moe_gather(X, order, k, Xs, _raw(stream)), "dg_moe_gather")
     return Xs
 
 
 def moe_combine(Ys: torch.Tensor, pos: torch.Tensor, Y: torch.Tensor, w: torch.Tensor | None = None,
                 stream=None) -> torch.Tensor:
     """Y[t] <- sum over j of w[t, j] * Ys[pos[t, j]] (w None: 1), dropped choices left out; returns Y."""
-    _check(lib().dg_moe_combine(_packed(Ys), _packed(pos), None if w is None else _packed(w), _packed(Y),
-                                _stream(stream)), "dg_moe_combine")
+    _check(_bind().moe_combine(Ys, pos, w, Y, _raw(stream)), "dg_moe_combine")
     return Y
 
 
@@ -381,9 +373,7 @@ def moe_combine_grad(dY: torch.Tensor, Ys: torch.Tensor, pos: torch.Tensor, w: t
                      dYs: torch.Tensor, dw: torch.Tensor | None = None, stream=None):
     """The gradients of moe_combine: dYs[pos[t, j]] <- w[t, j] * dY[t] (other rows zero) and
     dw[t, j] <- <dY[t], Ys[pos[t, j]]>; returns (dYs, dw)."""
-    _check(lib().dg_moe_combine_grad(_packed(dY), _packed(Ys), _packed(pos), None if w is None else _packed(w),
-                                     _packed(dYs), None if dw is None else _packed(dw), _stream(stream)),
-           "dg_moe_combine_grad")
+    _check(_bind().moe_combine_grad(dY, Ys, pos, w, dYs, dw, _raw(stream)), "dg_moe_combine_grad")
     return dYs, dw
 
 
@@ -391,16 +381,14 @@ def moe_gemm(A: torch.Tensor, offsets: torch.Tensor, W: torch.Tensor, C: torch.T
              stream=None) -> torch.Tensor:
     """C[r] <- act(A[r] @ W[e]) for the rows r of every expert e (W [E, K, N], any strides); rows of no
     expert are zero.  dA is moe_gemm(dC, offsets, W.transpose(1, 2), dA).  Returns C."""
-    _check(lib().dg_moe_gemm(_packed(A), _packed(offsets), _packed(W), _packed(C), act, _stream(stream)),
-           "dg_moe_gemm")
+    _check(_bind().moe_gemm(A, offsets, W, C, act, _raw(stream)), "dg_moe_gemm")
     return C
 
 
 def moe_gemm_wgrad(A: torch.Tensor, D: torch.Tensor, offsets: torch.Tensor, dW: torch.Tensor,
                    stream=None) -> torch.Tensor:
     """dW[e] <- A[rows of e].T @ D[rows of e] for every expert; returns dW [E, K, N]."""
-    _check(lib().dg_moe_gemm_wgrad(_packed(A), _packed(D), _packed(offsets), _packed(dW), _stream(stream)),
-           "dg_moe_gemm_wgrad")
+    _check(_bind().moe_gemm_wgrad(A, D, offsets, dW, _raw(stream)), "dg_moe_gemm_wgrad")
     return dW
 
 
@@ -408,17 +396,14 @@ def gemm_w4(A: torch.Tensor, Q: torch.Tensor, S: torch.Tensor, C: torch.Tensor, 
             Z: torch.Tensor | None = None, act: int = DG_ACT_NONE, stream=None) -> torch.Tensor:
     """C <- act(A @ W.T), W[n, k] = S[n, k // group] * (q[n, k] - Z[n, k // group]): Q [N, ceil(K/2)] holds
     two 4-bit codes a byte (even k in the low half), Z None means 8; returns C."""
-    _check(lib().dg_gemm_w4(_packed(A), _packed(Q), _packed(S), None if Z is None else _packed(Z), _packed(C),
-                            group, act, _stream(stream)), "dg_gemm_w4")
+    _check(_bind().gemm_w4(A, Q, S, Z, C, group, act, _raw(stream)), "dg_gemm_w4")
     return C
 
 
 def moe_gemm_w4(A: torch.Tensor, offsets: torch.Tensor, Q: torch.Tensor, S: torch.Tensor, C: torch.Tensor,
                 group: int, Z: torch.Tensor | None = None, act: int = DG_ACT_NONE, stream=None) -> torch.Tensor:
     """gemm_w4 for the rows of every expert (Q, S and Z with a leading expert dim); returns C."""
-    _check(lib().dg_moe_gemm_w4(_packed(A), _packed(offsets), _packed(Q), _packed(S),
-                                None if Z is None else _packed(Z), _packed(C), group, act, _stream(stream)),
-           "dg_moe_gemm_w4")
+    _check(_bind().moe_gemm_w4(A, offsets, Q, S, Z, C, group, act, _raw(stream)), "dg_moe_gemm_w4")
     return C
 
 

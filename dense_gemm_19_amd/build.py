@@ -2,7 +2,9 @@
 
     python -m dense_gemm_19_amd.build [-v] [--incremental]
 
-Objects go to dense_gemm_19_amd/_build/; the library to dense_gemm_19_amd/libdg.so.
+Objects go to dense_gemm_19_amd/_build/; the library to dense_gemm_19_amd/libdg.so,
+the tensor binding of its newer entry points (torch_bind.cpp) to
+dense_gemm_19_amd/_dgtorch.so.
 """
 from __future__ import annotations
 
@@ -16,6 +18,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdg.so")
+BIND = os.path.join(HERE, "_dgtorch.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 # -packed-fp32-ops off: no packed FP32 instructions are emitted anywhere.
@@ -81,6 +84,40 @@ def _scratch_kernels(remarks) -> list:
     return out
 
 
+def _bind_object(verbose: bool, incremental: bool) -> str:
+    """torch_bind.cpp, compiled against torch's headers."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    src, obj = os.path.join(CSRC, "torch_bind.cpp"), os.path.join(BUILD, "torch_bind.cpp.o")
+    if incremental and os.path.exists(obj) and os.path.getmtime(obj) > max(
+            os.path.getmtime(src), os.path.getmtime(os.path.join(ROOT, "include", "dg.h"))):
+        return obj
+    inc = [f"-isystem{p}" for p in cpp_extension.include_paths()] + ["-isystem/opt/rocm/include"]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + os.path.join(ROOT, "include"),
+           "-isystem" + sysconfig.get_paths()["include"], *inc, "-c", src, "-o", obj]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compile failed: torch_bind.cpp\n{r.stderr}")
+    return obj
+
+
+def _link_bind(obj: str, verbose: bool) -> None:
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BIND + ".tmp"
+    cmd = ["g++", "-shared", "-fPIC", "-o", tmp, obj, LIB, "-Wl,-rpath,$ORIGIN", f"-L{libs}", "-ltorch_python", "-ltorch_cpu",
+           "-lc10_hip", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BIND)
+
+
 def build(verbose: bool = False, jobs: int | None = None, incremental: bool = False) -> str:
     """Compile every source (or, with incremental=True, those newer than their
     object) and link libdg.so."""
@@ -88,13 +125,15 @@ def build(verbose: bool = False, jobs: int | None = None, incremental: bool = Fa
     srcs = HIP_SOURCES + HOST_SOURCES
     jobs = jobs or min(len(srcs), max(1, (os.cpu_count() or 4)))
     with ThreadPoolExecutor(max_workers=jobs) as ex:
+        bind = ex.submit(_bind_object, verbose, incremental)
         objs = list(ex.map(lambda s: _compile(s, verbose, incremental), srcs))
     tmp = LIB + ".tmp"
-    cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs
+    cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-Wl,-soname,libdg.so", "-o", tmp] + objs
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    _link_bind(bind.result(), verbose)
     return LIB
 
 

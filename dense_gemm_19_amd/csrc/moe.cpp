@@ -201,6 +201,7 @@ dg_status combine_entry(const dg_view *Ys, const dg_view *pos, const dg_view *w,
     a.dYs = out_ptr(ds); a.d_rs = ds.rs; a.d_cs = ds.cs;
     if (dw) { a.dw = out_ptr(dv); a.g_rs = dv.rs; a.g_cs = dv.cs; }
     a.vec = a.vec && ds.cols_contig();
+    a.p_run = p.cols_contig() && (p.rows <= 1 || p.rs == p.cols * p.esize);
     return done(launch_moe_combine_grad(s.dtype, a, stream), stream);
 }
 

@@ -43,6 +43,7 @@ struct CombineArgs {
     char *dw; int64_t g_rs, g_cs;          // gradient: [T][k] in w_kind, or null
     int T, k, R, H;
     int vec;                               // every operand's rows are contiguous
+    int p_run;                             // pos is one contiguous run
     int zero_blocks, zero_rows;            // gradient: workgroups that clear unnamed rows, rows of each
 };
 

@@ -18,8 +18,8 @@ typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
 constexpr int SORT_T = 1024, SORT_W = SORT_T / 64;
 
 // The key of id i: its expert, or -1 (dropped).
-__device__ __forceinline__ int sort_key(const SortArgs &a, int64_t i) {
-    const char *p = a.ids + (a.k > 0 ? (i / a.k) * a.i_rs + (i % a.k) * a.i_cs : i * a.i_cs);
+__device__ __forceinline__ int sort_key(const SortArgs &a, int i) {
+    const char *p = a.ids + (a.k > 0 ? (int64_t)(i / a.k) * a.i_rs + (int64_t)(i % a.k) * a.i_cs : i * a.i_cs);
     const int64_t v = a.wide ? *reinterpret_cast<const int64_t *>(p) : *reinterpret_cast<const int32_t *>(p);
     return v >= 0 && v < a.E ? (int)v : -1;
 }
@@ -34,13 +34,50 @@ __device__ __forceinline__ uint64_t same_key(int key, int bits) {
     return m;
 }
 
-// Histogram of ids [i0, i1) of every wave: cnt[wave][E] += 1 per id.
-__device__ __forceinline__ void wave_counts(const SortArgs &a, int *cnt, int64_t i0, int64_t i1, int lane) {
-    for (int64_t i = i0 + lane; i < i1; i += 64) {
-        const int key = sort_key(a, i);
-        if (key >= 0) atomicAdd(cnt + key, 1);   // integer counts: the order does not matter
+// A wave's run of ids [i0, i1): at most STEPS steps of 64, whose keys stay in
+// registers from the count to the placing (every load is issued before any use).
+template <int STEPS>
+struct Run {
+    int key[STEPS];
+    int i0, i1;
+
+    __device__ void load(const SortArgs &a, int b, int e, int lane) {
+        i0 = b; i1 = e;
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            const int i = i0 + 64 * s + lane;
+            key[s] = i < i1 ? sort_key(a, i) : -1;
+        }
     }
-}
+    // cnt[key] += 1 per id (integer counts: the order does not matter)
+    __device__ void count(int *cnt) const {
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s)
+            if (key[s] >= 0) atomicAdd(cnt + key[s], 1);
+    }
+    // The places of the run's ids, in order, next[key] being the place of the
+    // wave's next id of each expert: the ids of one step with the same key take
+    // consecutive places in lane order.
+    __device__ void place(const SortArgs &a, int *next, int lane) const {
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            if (i0 + 64 * s >= i1) break;
+            const int i = i0 + 64 * s + lane;
+            const uint64_t m = same_key(key[s], a.bits);
+            const int rank = __popcll(m & ((1ull << lane) - 1));
+            int at = -1;
+            if (key[s] >= 0) at = __hip_atomic_load(next + key[s], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP) + rank;
+            __builtin_amdgcn_wave_barrier();   // every lane has read before the last of each key writes
+            if (key[s] >= 0 && (m >> lane) == 1)
+                __hip_atomic_store(next + key[s], at + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+            __builtin_amdgcn_wave_barrier();
+            if (i < i1) {
+                a.pos[i] = at;
+                if (at >= 0) a.order[at] = i;
+            }
+        }
+    }
+};
 
 // Exclusive scan of v[0..E) by one wave; returns the total.
 __device__ __forceinline__ int wave_scan(int *v, int E, int lane) {
@@ -59,41 +96,21 @@ __device__ __forceinline__ int wave_scan(int *v, int E, int lane) {
     return carry;
 }
 
-// Places of ids [i0, i1) of a wave, in order, next[key] being the place of the
-// wave's next id of each expert: the ids of one 64-id step with the same key
-// take consecutive places in lane order.
-__device__ __forceinline__ void wave_place(const SortArgs &a, int *next, int64_t i0, int64_t i1, int lane) {
-    for (int64_t b = i0; b < i1; b += 64) {
-        const int64_t i = b + lane;
-        const int key = i < i1 ? sort_key(a, i) : -1;
-        const uint64_t m = same_key(key, a.bits);
-        const int rank = __popcll(m & ((1ull << lane) - 1));
-        int at = -1;
-        if (key >= 0) at = __hip_atomic_load(next + key, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP) + rank;
-        __builtin_amdgcn_wave_barrier();   // every lane has read before the last of each key writes
-        if (key >= 0 && (m >> lane) == 1)
-            __hip_atomic_store(next + key, at + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-        __builtin_amdgcn_wave_barrier();
-        if (i < i1) {
-            a.pos[i] = at;
-            if (at >= 0) a.order[at] = (int)i;
-        }
-    }
-}
-
 // One workgroup sorts everything: each wave counts its own run of ids, the
 // counts become starting places (experts first, then waves within an expert,
 // which keeps the sort stable), and each wave places its run.
+template <int STEPS>
 __global__ void __launch_bounds__(SORT_T) moe_sort_one(SortArgs a) {
     extern __shared__ int lds[];              // cnt[SORT_W][E], total[E]
     int *total = lds + SORT_W * a.E;
     __shared__ int kept;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int run = ((a.n + SORT_T - 1) / SORT_T) * 64;   // ids per wave, whole steps
+    Run<STEPS> r;
+    r.load(a, min(wave * run, a.n), min(wave * run + run, a.n), lane);
     for (int i = tid; i < SORT_W * a.E; i += SORT_T) lds[i] = 0;
     __syncthreads();
-    const int run = ((a.n + SORT_T - 1) / SORT_T) * 64;   // ids per wave, whole steps
-    const int64_t i0 = (int64_t)wave * run, i1 = min<int64_t>(i0 + run, a.n);
-    wave_counts(a, lds + wave * a.E, i0, i1, lane);
+    r.count(lds + wave * a.E);
     __syncthreads();
     for (int e = tid; e < a.E; e += SORT_T) {
         int s = 0;
@@ -120,30 +137,40 @@ __global__ void __launch_bounds__(SORT_T) moe_sort_one(SortArgs a) {
     if (tid == 0) a.offsets[a.E] = kept;
     for (int i = kept + tid; i < a.n; i += SORT_T) a.order[i] = -1;
     __syncthreads();
-    wave_place(a, lds + wave * a.E, i0, i1, lane);
+    r.place(a, lds + wave * a.E, lane);
 }
 
-// The three-launch sort.  Workgroup b owns ids [b n / blocks, (b + 1) n /
-// blocks), never fewer than E of them.  Its part of pos, which it alone writes
-// in the last launch, carries its E counts between the launches, so that the
-// sort needs no scratch memory: counts (moe_sort_count), starting places
-// (moe_sort_scan), then the places themselves (moe_sort_place).
-__device__ __forceinline__ int64_t block_start(const SortArgs &a, int b) { return (int64_t)b * a.n / a.blocks; }
+// The three-launch sort.  Workgroup b owns a contiguous part of the ids (the
+// parts differ by one id at most, and none is shorter than E).  Its part of
+// pos, which it alone writes in the last launch, carries its E counts between
+// the launches, so that the sort needs no scratch memory: counts
+// (moe_sort_count), starting places (moe_sort_scan), then the places
+// themselves (moe_sort_place).
+__device__ __forceinline__ int block_start(const SortArgs &a, int b) {
+    return b * (a.n / a.blocks) + min(b, a.n % a.blocks);
+}
 
 __global__ void __launch_bounds__(SORT_T) moe_sort_count(SortArgs a) {
     extern __shared__ int lds[];
+    const int i0 = block_start(a, blockIdx.x), i1 = block_start(a, blockIdx.x + 1);
+    int key[SORT_BLOCK / SORT_T];
+#pragma unroll
+    for (int s = 0; s < SORT_BLOCK / SORT_T; ++s) {
+        const int i = i0 + s * SORT_T + threadIdx.x;
+        key[s] = i < i1 ? sort_key(a, i) : -1;
+    }
     for (int e = threadIdx.x; e < a.E; e += SORT_T) lds[e] = 0;
     __syncthreads();
-    const int64_t i0 = block_start(a, blockIdx.x), i1 = block_start(a, blockIdx.x + 1);
-    for (int64_t i = i0 + threadIdx.x; i < i1; i += SORT_T) {
-        const int key = sort_key(a, i);
-        if (key >= 0) atomicAdd(lds + key, 1);
-    }
+#pragma unroll
+    for (int s = 0; s < SORT_BLOCK / SORT_T; ++s)
+        if (key[s] >= 0) atomicAdd(lds + key[s], 1);
     __syncthreads();
     for (int e = threadIdx.x; e < a.E; e += SORT_T) a.pos[i0 + e] = lds[e];
 }
 
-// One workgroup: the E columns of the count table over `parts` runs of blocks.
+// One workgroup: each thread walks one expert's column of the count table over
+// its run of blocks, SCAN_U counts at a time.
+constexpr int SCAN_U = 16;
 __global__ void __launch_bounds__(SORT_T) moe_sort_scan(SortArgs a) {
     extern __shared__ int lds[];              // part[parts][E], total[E]
     const int tid = threadIdx.x, lane = tid & 63;
@@ -152,10 +179,18 @@ __global__ void __launch_bounds__(SORT_T) moe_sort_scan(SortArgs a) {
     __shared__ int kept;
     const int part = tid / cols, per = (a.blocks + parts - 1) / parts;
     const int b0 = min(part * per, a.blocks), b1 = part < parts ? min(b0 + per, a.blocks) : b0;
+    // column e of blocks [b, b + SCAN_U): all loads, then f(block, count) in order
+    auto column = [&](int e, int b, auto f) __attribute__((always_inline)) {
+        int c[SCAN_U];
+#pragma unroll
+        for (int u = 0; u < SCAN_U; ++u) c[u] = b + u < b1 ? a.pos[block_start(a, b + u) + e] : 0;
+#pragma unroll
+        for (int u = 0; u < SCAN_U; ++u)
+            if (b + u < b1) f(b + u, c[u]);
+    };
     for (int e = tid % cols; e < a.E && part < parts; e += cols) {
         int s = 0;
-#pragma unroll 8
-        for (int b = b0; b < b1; ++b) s += a.pos[block_start(a, b) + e];
+        for (int b = b0; b < b1; b += SCAN_U) column(e, b, [&](int, int c) { s += c; });
         lds[part * a.E + e] = s;
     }
     __syncthreads();
@@ -183,25 +218,25 @@ __global__ void __launch_bounds__(SORT_T) moe_sort_scan(SortArgs a) {
     __syncthreads();
     for (int e = tid % cols; e < a.E && part < parts; e += cols) {
         int s = lds[part * a.E + e];
-#pragma unroll 8
-        for (int b = b0; b < b1; ++b) {
-            int *p = a.pos + block_start(a, b) + e;
-            const int c = *p;
-            *p = s;
-            s += c;
-        }
+        for (int b = b0; b < b1; b += SCAN_U)
+            column(e, b, [&](int at, int c) {
+                a.pos[block_start(a, at) + e] = s;
+                s += c;
+            });
     }
 }
 
 __global__ void __launch_bounds__(SORT_T) moe_sort_place(SortArgs a) {
     extern __shared__ int lds[];              // cnt[SORT_W][E]
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int64_t b0 = block_start(a, blockIdx.x), b1 = block_start(a, blockIdx.x + 1);
+    const int b0 = block_start(a, blockIdx.x), b1 = block_start(a, blockIdx.x + 1);
+    const int run = (b1 - b0 + SORT_T - 1) / SORT_T * 64;
+    Run<SORT_BLOCK / SORT_T> r;
+    r.load(a, min(b0 + wave * run, b1), min(b0 + wave * run + run, b1), lane);
+    const int kept = a.offsets[a.E];
     for (int i = tid; i < SORT_W * a.E; i += SORT_T) lds[i] = 0;
     __syncthreads();
-    const int run = (int)((b1 - b0 + SORT_T - 1) / SORT_T) * 64;
-    const int64_t i0 = min<int64_t>(b0 + (int64_t)wave * run, b1), i1 = min<int64_t>(i0 + run, b1);
-    wave_counts(a, lds + wave * a.E, i0, i1, lane);
+    r.count(lds + wave * a.E);
     __syncthreads();
     for (int e = tid; e < a.E; e += SORT_T) {
         int s = a.pos[b0 + e];
@@ -212,11 +247,9 @@ __global__ void __launch_bounds__(SORT_T) moe_sort_place(SortArgs a) {
             s += c;
         }
     }
-    const int kept = a.offsets[a.E];
-    for (int64_t i = (int64_t)kept + (int64_t)blockIdx.x * SORT_T + tid; i < a.n; i += (int64_t)a.blocks * SORT_T)
-        a.order[i] = -1;
+    for (int64_t i = (int64_t)kept + blockIdx.x * SORT_T + tid; i < a.n; i += (int64_t)a.blocks * SORT_T) a.order[i] = -1;
     __syncthreads();   // every count of this workgroup's part of pos has been read
-    wave_place(a, lds + wave * a.E, i0, i1, lane);
+    r.place(a, lds + wave * a.E, lane);
 }
 
 // ------------------------------------------------------------------ row chunks
@@ -378,17 +411,25 @@ __device__ __forceinline__ void clear_unnamed(const CombineArgs &a, uint32_t *bi
     for (int i = threadIdx.x; i < (a.zero_rows + 31) / 32; i += NT) bits[i] = 0;
     __syncthreads();
     const int64_t n = (int64_t)a.T * a.k;
-    for (int64_t i0 = 0; i0 < n; i0 += 8 * NT) {
-        int64_t at[8];
+    auto mark = [&](int64_t at) __attribute__((always_inline)) {
+        if (at >= r0 && at < r1) atomicOr(bits + ((at - r0) >> 5), 1u << ((at - r0) & 31));
+    };
+    // pos whole, 16 bytes a load where it is one run (4 loads in flight)
+    const int64_t quads = a.p_run ? n / 4 : 0;
+    for (int64_t i0 = 0; i0 < quads; i0 += 4 * NT) {
+        u32x4 v[4];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
+        for (int q = 0; q < 4; ++q) {
             const int64_t i = i0 + q * NT + threadIdx.x;
-            at[q] = i < n ? *reinterpret_cast<const int *>(a.pos + (i / a.k) * a.p_rs + (i % a.k) * a.p_cs) : -1;
+            v[q] = i < quads ? *reinterpret_cast<const u32x4_any *>(a.pos + 16 * i) : u32x4{~0u, ~0u, ~0u, ~0u};
         }
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-            if (at[q] >= r0 && at[q] < r1) atomicOr(bits + ((at[q] - r0) >> 5), 1u << ((at[q] - r0) & 31));
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mark((int)v[q][e]);
     }
+    for (int64_t i = 4 * quads + threadIdx.x; i < n; i += NT)
+        mark(*reinterpret_cast<const int *>(a.p_run ? a.pos + 4 * i : a.pos + (i / a.k) * a.p_rs + (i % a.k) * a.p_cs));
     __syncthreads();
     Chunk<EB> zero;
     zero.v = u32x4{0u, 0u, 0u, 0u};
@@ -421,7 +462,6 @@ __global__ void __launch_bounds__(NT) moe_combine_grad_rows(CombineArgs a, int l
     const int64_t t = WPT > 1 ? b : (b * NT + threadIdx.x) / lanes;
     const int me = threadIdx.x % span;
     const bool in = t < a.T;                                     // (WPT > 1: always)
-    const int chunks = in ? (a.H + CN - 1) / CN : 0;
     for (int j0 = 0; j0 < a.k; j0 += KU) {
         int p[KU];
         float w[KU], dot[KU];
@@ -430,15 +470,19 @@ __global__ void __launch_bounds__(NT) moe_combine_grad_rows(CombineArgs a, int l
             p[j] = in && j0 + j < a.k ? pos_of(a, t, j0 + j) : -1;
             w[j] = in && j0 + j < a.k ? weight_of(a, t, j0 + j) : 0.0f;
             dot[j] = 0.0f;
+            // kept in vector registers: 2 x KU row addresses as scalars would spill
+            asm volatile("" : "+v"(p[j]));
         }
-        for (int c = me; c < chunks; c += span) {
-            const int left = a.H - c * CN;
+        const int whole = in && a.vec ? a.H / CN : 0;
+        // whole chunks: all of a chunk's loads, then the products and stores
+#pragma unroll 1
+        for (int c = me; c < whole; c += span) {
             Chunk<EB> g, y[KU];
-            g.load(a.Y + t * a.y_rs, a.y_cs, c, left, a.vec);
+            g.load(a.Y + t * a.y_rs, EB, c, CN, 1);
             if (a.dw) {
 #pragma unroll
                 for (int j = 0; j < KU; ++j)
-                    if (p[j] >= 0) y[j].load(a.Ys + (int64_t)p[j] * a.s_rs, a.s_cs, c, left, a.vec);
+                    if (p[j] >= 0) y[j].load(a.Ys + (int64_t)p[j] * a.s_rs, EB, c, CN, 1);
             }
 #pragma unroll
             for (int j = 0; j < KU; ++j)
@@ -450,7 +494,18 @@ __global__ void __launch_bounds__(NT) moe_combine_grad_rows(CombineArgs a, int l
                         if (a.dw) dot[j] = fmaf(x, V::get(y[j], e), dot[j]);
                         V::set(d, e, w[j] * x);
                     }
-                    d.store(a.dYs + (int64_t)p[j] * a.d_rs, a.d_cs, c, left, a.vec);
+                    d.store(a.dYs + (int64_t)p[j] * a.d_rs, EB, c, CN, 1);
+                }
+        }
+        // the row's last elements, or all of them where a row is not contiguous
+#pragma unroll 1
+        for (int h = whole * CN + me; in && h < a.H; h += span) {
+            const float x = load_out(a.Y + t * a.y_rs + h * a.y_cs, KIND);
+#pragma unroll
+            for (int j = 0; j < KU; ++j)
+                if (p[j] >= 0) {
+                    if (a.dw) dot[j] = fmaf(x, load_out(a.Ys + (int64_t)p[j] * a.s_rs + h * a.s_cs, KIND), dot[j]);
+                    store_out(a.dYs + (int64_t)p[j] * a.d_rs + h * a.d_cs, KIND, w[j] * x);
                 }
         }
         if (!a.dw) continue;
@@ -496,8 +551,10 @@ hipError_t launch_moe_sort(const SortArgs &a, hipStream_t s) {
     hipError_t e;
     if (a.n <= SORT_ONE_MAX) {
         const size_t lds = (SORT_W + 1) * a.E * sizeof(int);
-        if ((e = allow_lds(moe_sort_one, lds)) != hipSuccess) return e;
-        hipLaunchKernelGGL(moe_sort_one, dim3(1), dim3(SORT_T), lds, s, a);
+        // few steps per wave where few ids allow it: fewer registers and instructions to fetch
+        const auto k = a.n <= SORT_T ? moe_sort_one<1> : a.n <= 4 * SORT_T ? moe_sort_one<4> : moe_sort_one<SORT_ONE_MAX / SORT_T>;
+        if ((e = allow_lds(k, lds)) != hipSuccess) return e;
+        hipLaunchKernelGGL(k, dim3(1), dim3(SORT_T), lds, s, a);
         return hipGetLastError();
     }
     const int cols = a.E < SORT_T ? a.E : SORT_T, parts = SORT_T / cols;

@@ -150,14 +150,24 @@ def test_w4_experts_count():
     refused("NDIM", dg.moe_gemm_w4, **{**a, "Q": z(N, 32, dt=U8)})
 
 
-def test_packed_views_match_the_struct():
-    # the packed bytes of a view are those of the dg_view structure
-    for t in (z(3), z(3, 4).t(), z(2, 3, 4)[:, ::2], z(1, 2, 3, 4, dt=F32), torch.tensor(1.0)):
-        assert dg._packed(t) == bytes(dg.view_of(t))
+def test_views_of_the_binding_match_the_struct():
+    view = dg._bind().view
+    for t in (z(3), z(3, 4).t(), z(2, 3, 4)[:, ::2], z(1, 2, 3, 4, dt=F32), torch.tensor(1.0), z(0, 4, dt=U8), z(2, dt=I64),
+              z(5, dt=I32), z(2, dt=F16), z(4, dt=torch.float8_e4m3fn)):
+        a, b = dg.View.from_buffer_copy(view(t)), dg.view_of(t)
+        assert (a.ptr, a.ndim, list(a.shape), list(a.stride), a.dtype) == (b.ptr, b.ndim, list(b.shape), list(b.stride), b.dtype)
+
+
+@pytest.mark.parametrize("bad,error", [(torch.zeros(2, dtype=torch.int16), TypeError), ([1, 2], TypeError),
+                                       (torch.zeros(1, 1, 1, 1, 1), ValueError)])
+def test_arguments_that_are_no_views(bad, error):
+    with pytest.raises(error):
+        dg.moe_gather(z(T, H), bad, 2, z(R, H), stream=0)
     with pytest.raises(TypeError):
-        dg._packed(z(2, dt=torch.int16))
-    with pytest.raises(ValueError):
-        dg._packed(z(1, 1, 1, 1, 1))
+        dg._bind().moe_gather(z(T, H), z(R, dt=I32), 2)
+    with pytest.raises(OverflowError):
+        dg.moe_gather(z(T, H), z(R, dt=I32), 1 << 40, z(R, H), stream=0)
+    refused("NULL", dg.moe_gather, z(T, H), None, 2, z(R, H))
 
 
 def test_nothing_to_do():
