@@ -184,12 +184,7 @@ WsTable &ws_table() {
     return t;
 }
 
-// The blocks of one call (null when the plan needs none), locked while it lives.
-struct WsLease {
-    std::unique_lock<std::mutex> lock;
-    float *ws = nullptr;
-    int *counters = nullptr;
-};
+}  // namespace
 
 hipError_t lease_workspace(hipStream_t stream, size_t bytes, size_t ncounters, WsLease *out) {
     if (bytes == 0 && ncounters == 0) return hipSuccess;
@@ -238,8 +233,6 @@ hipError_t lease_workspace(hipStream_t stream, size_t bytes, size_t ncounters, W
     out->lock = std::move(lk);
     return hipSuccess;
 }
-
-}  // namespace
 
 dg_status check_pointer(const void *p) {
     if (!p) return DG_SUCCESS;

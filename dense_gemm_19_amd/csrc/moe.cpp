@@ -373,7 +373,7 @@ dg_status w4_entry(const dg_view *A, const dg_view *offsets, const dg_view *Q, c
     if (q.E < 1 || s.E != q.E || s.one.rows != N || s.one.cols != groups) return DG_ERR_SHAPE_MISMATCH;
     if (Z && (z.E != q.E || z.one.rows != N || z.one.cols != groups)) return DG_ERR_SHAPE_MISMATCH;
     if (experts) DG_TRY(index_vector(offsets, q.E + 1, &off));
-    if (M > INT32_MAX || K > INT32_MAX / 4 || N > INT32_MAX || q.E > INT32_MAX / 2) return DG_ERR_OVERFLOW;
+    if (M > INT32_MAX || K > (1 << 20) || N > INT32_MAX || q.E > INT32_MAX / 2) return DG_ERR_OVERFLOW;
     if (!x.cols_contig() || !q.one.cols_contig()) return DG_ERR_UNSUPPORTED_VIEW;
     // lane offsets within a workgroup's rows and columns are 32-bit
     const int64_t lim = ((int64_t)1 << 31) / 64;
@@ -393,15 +393,55 @@ dg_status w4_entry(const dg_view *A, const dg_view *offsets, const dg_view *Q, c
     a.s_kind = s.one.dtype;
     a.C = out_ptr(c); a.c_rs = c.rs; a.c_cs = c.cs; a.out_kind = c.dtype; a.act = act;
     a.M = (int)M; a.N = (int)N; a.K = (int)K; a.G = group;
+    a.groups = (int)groups;
+    a.g_mul = group == 32 ? 0u : (uint32_t)((((uint64_t)1 << 32) + group / 32 - 1) / (group / 32));
     if (experts) { a.offsets = off.ptr; a.o_s = off.cs; }
     a.E = (int)q.E;
-    a.slabs = (int)cdiv(N, W4_COLS);
     a.s_vec = s.one.cols_contig() && (!Z || z.one.cols_contig()) && (group == 32 || group == 64 || group % 128 == 0);
-    const int64_t used = experts ? std::min(q.E, M) : 1, mean = M / std::max<int64_t>(used, 1);
-    const int tm = mean <= 16 ? 1 : 2, bm = 16 * tm;
-    const int64_t tiles_m = experts ? (M + std::min(q.E + 1, M) * (bm - 1)) / bm : cdiv(M, bm);
-    if (tiles_m * a.slabs > INT32_MAX) return DG_ERR_OVERFLOW;
-    return done(launch_w4(x.dtype == DG_F16 ? IN_F16 : IN_BF16, tm, a, tiles_m * a.slabs, stream), stream);
+    a.direct = reinterpret_cast<uintptr_t>(x.ptr) % 16 == 0 && (M <= 1 || x.rs % 16 == 0) && K % 8 == 0;
+
+    // Rows of a tile: as few tiles as the largest allows, evenly filled (one
+    // matrix), or by the mean count of the experts that can have rows.
+    const int tm_max = w4_max_tm(group, s.one.dtype);
+    int64_t tiles_m;
+    int tm;
+    if (experts) {
+        const int64_t mean = M / std::min(q.E, M);
+        tm = std::min(tm_max, mean <= 10 ? 1 : mean <= 24 ? 2 : 4);
+        tiles_m = (M + std::min(q.E + 1, M) * (16 * tm - 1)) / (16 * tm);
+        a.rows_lds = 16 * tm;
+    } else {
+        tm = (int)cdiv(cdiv(M, cdiv(M, 16 * tm_max)), 16);
+        tiles_m = cdiv(M, 16 * tm);
+        a.rows_lds = (int)std::min<int64_t>(M, 16 * tm);
+    }
+    a.slabs = (int)cdiv(N, w4_cols(tm));
+    // K in pieces where one matrix has too few slabs to fill the device and
+    // several chunks: each piece keeps two.  A captured call runs whole: the
+    // pieces' workspace may have to be allocated.
+    const int64_t chunks = cdiv(K, W4_CHUNK), units = tiles_m * a.slabs;
+    int64_t splits = 1;
+    if (!experts && chunks > 4 && units < d.cus / 2) {
+        hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
+        if (hipStreamIsCapturing(stream, &cap) != hipSuccess) (void)hipGetLastError();
+        else if (cap == hipStreamCaptureStatusNone) splits = std::min<int64_t>(d.cus / units, chunks / 2);
+    }
+    a.chunks = (int)std::max<int64_t>(cdiv(chunks, splits), 1);
+    a.splits = (int)std::max<int64_t>(cdiv(chunks, a.chunks), 1);
+    // A's LDS ring: what the CU has for each workgroup that its registers let in
+    const int64_t lds = tm == 1 ? 80 * 1024 - 256 : 156 * 1024;
+    a.bufs = (int)std::max<int64_t>(1, std::min<int64_t>({8, lds / (a.rows_lds * W4_CHUNK * 2), a.chunks}));
+    if (units * a.splits > INT32_MAX) return DG_ERR_OVERFLOW;
+    WsLease lease;
+    if (a.splits > 1) {
+        if (lease_workspace(stream, (size_t)units * a.splits * 16 * tm * w4_cols(tm) * sizeof(float), (size_t)units, &lease) != hipSuccess) {
+            (void)hipGetLastError();
+            return DG_ERR_HIP;
+        }
+        a.ws = lease.ws;
+        a.counters = lease.counters;
+    }
+    return done(launch_w4(x.dtype == DG_F16 ? IN_F16 : IN_BF16, tm, a, units * a.splits, stream), stream);
 }
 
 }  // namespace

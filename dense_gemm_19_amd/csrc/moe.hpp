@@ -90,15 +90,24 @@ struct W4Args {
     int s_kind;                            // OutKind numbering
     char *C; int64_t c_rs, c_cs;
     int out_kind, act;
-    int M, N, K, G;
+    int M, N, K, G, groups;                // groups = ceil(K / G)
+    uint32_t g_mul;                        // ceil(2^32 / (G / 32)), 0 for G = 32
     const char *offsets; int64_t o_s; int E;   // offsets null: one group of all M rows
-    int slabs;                             // column slabs
+    int slabs;                             // column slabs of w4_cols(tm)
+    int chunks, splits;                    // K in pieces of `chunks` chunks of W4_CHUNK; splits > 1: one matrix only
+    float *ws; int *counters;              // splits > 1: [tiles][splits][16 tm x w4_cols(tm)] sums, a counter per tile (0)
+    int bufs, rows_lds;                    // A's LDS ring: chunks it holds, rows of each
+    int direct;                            // A in whole 16-byte pieces, aligned
     int s_vec;                             // a window's groups are adjacent in S's and Z's rows
 };
 
-constexpr int W4_COLS = 32;   // columns of a workgroup
+// Columns of a workgroup of 16 tm rows: few rows take narrow slabs, whose
+// registers let two workgroups share a CU.
+constexpr int w4_cols(int tm) { return tm == 1 ? 32 : 64; }
+constexpr int W4_CHUNK = 1024; // K elements that a workgroup's 8 waves take together
 
-// tm: rows of a workgroup / 16 (1 or 2)
+// tm: rows of a workgroup / 16, 1 to w4_max_tm
+int w4_max_tm(int group, int s_kind);
 hipError_t launch_w4(int in_kind, int tm, const W4Args &a, int64_t units, hipStream_t stream);
 
 }  // namespace dg

@@ -395,9 +395,11 @@ dg_status dg_quant_fp8(const dg_view *X, const dg_view *Q, const dg_view *S, dg_
  *
  * Index tensors are read on the device.  A value outside its range reaches no
  * memory: a dropped choice.  Conventions as for the GEMM entry points
- * (asynchronous on `stream`, outputs untouched on error, no scratch memory, no
- * atomics on floating-point values: results are bitwise reproducible).  Every
- * one may be captured in a HIP graph.  Views of index vectors are [len] or
+ * (asynchronous on `stream`, outputs untouched on error, no atomics on
+ * floating-point values: results are bitwise reproducible).  Every one may be
+ * captured in a HIP graph.  None needs scratch memory but dg_gemm_w4, which
+ * splits K over workgroups where N is small, on the stream's split-K workspace
+ * (a captured call does not split, so its last bits may differ).  Views of index vectors are [len] or
  * [1][len].
  */
 
@@ -469,11 +471,12 @@ dg_status dg_moe_gemm_wgrad(const dg_view *A, const dg_view *D, const dg_view *o
  *   S [N][ceil(K / group)] DG_F32, DG_F16 or DG_BF16; Z the same shape, DG_U8 (any
  *     value 0 .. 255), or NULL: 8.
  *   group: a positive multiple of 32.  C [M][N] DG_F32, DG_F16 or DG_BF16.
- * q - z enters the products exactly; each group's sum is formed in FP32 and then
- * multiplied by its scale.
+ * No weight is rounded: codes and zero points enter the products exactly, each
+ * group's sum is formed in FP32 and then multiplied by its scale.
  * Errors: DG_ERR_INVALID_ARG (group, act), DG_ERR_DTYPE, DG_ERR_SHAPE_MISMATCH,
  * DG_ERR_UNSUPPORTED_VIEW (A's or Q's rows not contiguous), DG_ERR_STRIDE,
- * DG_ERR_ALIAS, DG_ERR_OVERFLOW, view errors. */
+ * DG_ERR_ALIAS, DG_ERR_OVERFLOW (K above 2^20, row strides of 32 MiB or more),
+ * view errors. */
 dg_status dg_gemm_w4(const dg_view *A, const dg_view *Q, const dg_view *S, const dg_view *Z, const dg_view *C,
                      int32_t group, dg_act act, hipStream_t stream);
 

@@ -150,6 +150,12 @@ def test_w4_experts_count():
     refused("NDIM", dg.moe_gemm_w4, **{**a, "Q": z(N, 32, dt=U8)})
 
 
+def test_w4_too_long():
+    refused("OVERFLOW", dg.gemm_w4, torch.empty(1, 1 << 21, dtype=BF16), torch.empty(1, 1 << 20, dtype=U8),
+            torch.empty(1, 1 << 14), z(1, 1), 128)
+    refused("OVERFLOW", dg.gemm_w4, torch.empty_strided((2, 64), (1 << 24, 1), dtype=BF16), z(N, 32, dt=U8), z(N, 2), z(2, N), 32)
+
+
 def test_views_of_the_binding_match_the_struct():
     view = dg._bind().view
     for t in (z(3), z(3, 4).t(), z(2, 3, 4)[:, ::2], z(1, 2, 3, 4, dt=F32), torch.tensor(1.0), z(0, 4, dt=U8), z(2, dt=I64),

@@ -103,6 +103,36 @@ def test_non_finite_activations(dg):
     assert torch.equal(torch.isnan(C[1].cpu()), torch.isnan(inf)) and torch.equal(C[1].cpu().nan_to_num(0, 1, -1), inf.float().nan_to_num(0, 1, -1))
 
 
+@pytest.mark.parametrize("G", [32, 64, 96, 128, 160, 224, 384, 4096, 1 << 20])
+def test_group_of_every_element(dg, G):
+    # a one-hot A reads one weight: the scale of its group at the group's ends, along a long K
+    K, N = 8192 + 40, 3
+    Q = torch.full((N, K // 2), 0x99, dtype=torch.uint8)            # q - 8 = 1
+    groups = -(-K // G)
+    S = (torch.arange(N * groups, dtype=torch.float32) + 1).reshape(N, groups)
+    at = sorted({min(max(k, 0), K - 1) for g in range(0, groups, max(1, groups // 7)) for k in (g * G - 1, g * G, g * G + G - 1)})
+    for dtype in (BF16, F16):
+        A = torch.zeros(len(at), K, dtype=dtype)
+        for m, k in enumerate(at):
+            A[m, k] = 1
+        C = dg.gemm_w4(*dev(A, Q, S), torch.empty(len(at), N, device=DEV), group=G)
+        want = torch.stack([S[:, k // G] for k in at])
+        assert torch.equal(C.cpu(), want)
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+def test_split_k(dg, zeros):
+    # few columns and a long K: the sum meets in the workspace; twice gives the same bits
+    g = torch.Generator().manual_seed(3)
+    M, N, K, G = 6, 72, 9000, 64
+    A = torch.randn(M, K, generator=g).to(BF16)
+    Q, S, Z = weights(g, N, K, G, zeros, BF16)
+    args = dev(A, Q, S)
+    C = [dg.gemm_w4(*args, torch.empty(M, N, device=DEV), group=G, Z=dev(Z)[0]) for _ in range(3)]
+    om.check(C[0], om.w4(A, Q, S, Z, G, 0, F32), "split")
+    assert torch.equal(C[0], C[1]) and torch.equal(C[0], C[2])
+
+
 def test_empty(dg):
     Q, S = torch.zeros(8, 0, dtype=torch.uint8, device=DEV), torch.zeros(8, 0, device=DEV)
     C = torch.full((3, 8), 7.0, device=DEV)
