@@ -397,40 +397,65 @@ dg_status w4_entry(const dg_view *A, const dg_view *offsets, const dg_view *Q, c
     a.g_mul = group == 32 ? 0u : (uint32_t)((((uint64_t)1 << 32) + group / 32 - 1) / (group / 32));
     if (experts) { a.offsets = off.ptr; a.o_s = off.cs; }
     a.E = (int)q.E;
-    a.s_vec = s.one.cols_contig() && (!Z || z.one.cols_contig()) && (group == 32 || group == 64 || group % 128 == 0);
-    a.direct = reinterpret_cast<uintptr_t>(x.ptr) % 16 == 0 && (M <= 1 || x.rs % 16 == 0) && K % 8 == 0;
+    auto pieces = [](const Mat &m, int64_t es) {   // rows of whole, aligned 16-byte pieces
+        return reinterpret_cast<uintptr_t>(m.ptr) % 16 == 0 && es % 16 == 0 && (m.rows <= 1 || m.rs % 16 == 0) &&
+               m.cols * m.esize % 16 == 0;
+    };
+    a.direct = pieces(x, 0);
+    a.q_direct = pieces(q.one, q.E > 1 ? q.es : 0) && K % 32 == 0 && K > 0;
 
     // Rows of a tile: as few tiles as the largest allows, evenly filled (one
     // matrix), or by the mean count of the experts that can have rows.
-    const int tm_max = w4_max_tm(group, s.one.dtype);
     int64_t tiles_m;
-    int tm;
+    int tm, rows;
     if (experts) {
         const int64_t mean = M / std::min(q.E, M);
-        tm = std::min(tm_max, mean <= 10 ? 1 : mean <= 24 ? 2 : 4);
+        tm = mean <= 10 ? 1 : mean <= 24 ? 2 : 4;
         tiles_m = (M + std::min(q.E + 1, M) * (16 * tm - 1)) / (16 * tm);
-        a.rows_lds = 16 * tm;
+        rows = 16 * tm;
     } else {
-        tm = (int)cdiv(cdiv(M, cdiv(M, 16 * tm_max)), 16);
+        tm = (int)cdiv(cdiv(M, cdiv(M, 16 * W4_MAX_TM)), 16);
         tiles_m = cdiv(M, 16 * tm);
-        a.rows_lds = (int)std::min<int64_t>(M, 16 * tm);
+        rows = (int)std::min<int64_t>(M, 16 * tm);
     }
     a.slabs = (int)cdiv(N, w4_cols(tm));
     // K in pieces where one matrix has too few slabs to fill the device and
     // several chunks: each piece keeps two.  A captured call runs whole: the
     // pieces' workspace may have to be allocated.
-    const int64_t chunks = cdiv(K, W4_CHUNK), units = tiles_m * a.slabs;
+    const int chunk = w4_chunk(tm);
+    const int64_t chunks = cdiv(K, chunk), units = tiles_m * a.slabs;
     int64_t splits = 1;
-    if (!experts && chunks > 4 && units < d.cus / 2) {
+    if (!experts && chunks * chunk > 4096 && units < d.cus / 2) {
         hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
         if (hipStreamIsCapturing(stream, &cap) != hipSuccess) (void)hipGetLastError();
         else if (cap == hipStreamCaptureStatusNone) splits = std::min<int64_t>(d.cus / units, chunks / 2);
     }
     a.chunks = (int)std::max<int64_t>(cdiv(chunks, splits), 1);
     a.splits = (int)std::max<int64_t>(cdiv(chunks, a.chunks), 1);
-    // A's LDS ring: what the CU has for each workgroup that its registers let in
-    const int64_t lds = tm == 1 ? 80 * 1024 - 256 : 156 * 1024;
-    a.bufs = (int)std::max<int64_t>(1, std::min<int64_t>({8, lds / (a.rows_lds * W4_CHUNK * 2), a.chunks}));
+    // LDS: code rings of 2 to 4 units per wave, scales for as many chunks as fit,
+    // and A.  Half of a CU's LDS (two workgroups per CU) where that holds 2 units
+    // ahead, all scales and two chunks of A, or one of a full tile's rows; else
+    // all of it.
+    const int unit = 8 * 2048, a_buf = rows * chunk * 2;
+    auto scales = [&](int64_t seg) {
+        a.seg = (int)seg;
+        a.seg_groups = (int)std::min<int64_t>(groups, seg * chunk / group + 2);
+        a.s_pitch = (int)(cdiv(a.seg_groups * s.one.esize, 16) * 16 + 16);
+        a.z_pitch = Z ? (int)(cdiv(a.seg_groups, 16) * 16 + 16) : 0;
+        return w4_cols(tm) * (a.s_pitch + a.z_pitch);
+    };
+    const int half = 80 * 1024 - 128, whole = 160 * 1024 - 128;
+    int64_t seg = a.chunks;
+    const int a_min = experts ? a_buf : std::min(a.chunks, 2) * a_buf;
+    const int cap = tm == 1 && 2 * unit + scales(seg) + a_min <= half ? half : whole;
+    while (seg > 1 && 2 * unit + scales(seg) + a_buf > cap) seg = cdiv(seg, 2);
+    const int sz = scales(seg);
+    a.depth = 2;
+    while (a.depth < 4 && a.depth < a.chunks && (a.depth + 1) * unit + sz + a_min <= cap) ++a.depth;
+    const int left = (cap - a.depth * unit - sz) / a_buf;
+    a.a_lds = std::max(1, std::min(left, a.chunks)) * a_buf;
+    a.lds_bytes = a.depth * unit + sz + a.a_lds;
+    if (a.lds_bytes > whole) return DG_ERR_OVERFLOW;   // (no size gets here: one chunk's scales are at most 18 KB)
     if (units * a.splits > INT32_MAX) return DG_ERR_OVERFLOW;
     WsLease lease;
     if (a.splits > 1) {

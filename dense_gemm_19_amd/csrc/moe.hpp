@@ -94,20 +94,24 @@ struct W4Args {
     uint32_t g_mul;                        // ceil(2^32 / (G / 32)), 0 for G = 32
     const char *offsets; int64_t o_s; int E;   // offsets null: one group of all M rows
     int slabs;                             // column slabs of w4_cols(tm)
-    int chunks, splits;                    // K in pieces of `chunks` chunks of W4_CHUNK; splits > 1: one matrix only
+    int chunks, splits;                    // K in pieces of `chunks` chunks; splits > 1: one matrix only
     float *ws; int *counters;              // splits > 1: [tiles][splits][16 tm x w4_cols(tm)] sums, a counter per tile (0)
-    int bufs, rows_lds;                    // A's LDS ring: chunks it holds, rows of each
-    int direct;                            // A in whole 16-byte pieces, aligned
-    int s_vec;                             // a window's groups are adjacent in S's and Z's rows
+    int direct, q_direct;                  // A, Q: rows of whole, aligned 16-byte pieces
+    int depth;                             // code units in flight per wave (2 to 4)
+    int a_lds;                             // LDS bytes for A: at least one chunk of 16 tm (or all M) rows
+    int seg, seg_groups;                   // chunks whose scales are in LDS together, groups they touch at most
+    int s_pitch, z_pitch;                  // bytes of a column's scales and zero points in LDS
+    int lds_bytes;
 };
 
-// Columns of a workgroup of 16 tm rows: few rows take narrow slabs, whose
-// registers let two workgroups share a CU.
+// Geometry of the kernel by rows / 16 of a workgroup: columns, K elements of a
+// chunk.  Few rows take narrow slabs, whose LDS
+// lets two workgroups share a CU; more rows take shorter chunks, whose A fits.
+constexpr int W4_MAX_TM = 4;
 constexpr int w4_cols(int tm) { return tm == 1 ? 32 : 64; }
-constexpr int W4_CHUNK = 1024; // K elements that a workgroup's 8 waves take together
+constexpr int w4_chunk(int tm) { return tm == 1 ? 1024 : 512; }
 
-// tm: rows of a workgroup / 16, 1 to w4_max_tm
-int w4_max_tm(int group, int s_kind);
+// tm: rows of a workgroup / 16, 1 to W4_MAX_TM
 hipError_t launch_w4(int in_kind, int tm, const W4Args &a, int64_t units, hipStream_t stream);
 
 }  // namespace dg
