@@ -425,7 +425,7 @@ dg_status w4_entry(const dg_view *A, const dg_view *offsets, const dg_view *Q, c
     const int chunk = w4_chunk(tm);
     const int64_t chunks = cdiv(K, chunk), units = tiles_m * a.slabs;
     int64_t splits = 1;
-    if (!experts && chunks * chunk > 4096 && units < d.cus / 2) {
+    if (!experts && chunks * chunk > 4096 && 2 * units <= d.cus) {
         hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
         if (hipStreamIsCapturing(stream, &cap) != hipSuccess) (void)hipGetLastError();
         else if (cap == hipStreamCaptureStatusNone) splits = std::min<int64_t>(d.cus / units, chunks / 2);

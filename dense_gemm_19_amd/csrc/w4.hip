@@ -28,20 +28,6 @@ constexpr int UNIT_LDS = 2048;   // its 16 rows
 template <int IN>
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) { return dtl::mfma16<IN>(a, b, c); }
 
-// 4 x 4 dwords across the four 16-lane rows of a wave: afterwards dword i of
-// lane row g is what lane row i held in dword g.
-__device__ __forceinline__ u32x4 across_rows(u32x4 d) {
-    u32x2 t = __builtin_amdgcn_permlane32_swap(d[0], d[2], false, false);
-    d[0] = t[0]; d[2] = t[1];
-    t = __builtin_amdgcn_permlane32_swap(d[1], d[3], false, false);
-    d[1] = t[0]; d[3] = t[1];
-    t = __builtin_amdgcn_permlane16_swap(d[0], d[1], false, false);
-    d[0] = t[0]; d[1] = t[1];
-    t = __builtin_amdgcn_permlane16_swap(d[2], d[3], false, false);
-    d[2] = t[0]; d[3] = t[1];
-    return d;
-}
-
 // 8 codes (k in nibble k), a byte each, in the order of k.
 __device__ __forceinline__ u32x2 code_bytes(uint32_t x) {
     const uint32_t lo = x & 0x0f0f0f0fu, hi = (x >> 4) & 0x0f0f0f0fu;
@@ -302,13 +288,15 @@ __global__ void __launch_bounds__(NT, TM == 1 ? 4 : 2) w4_stream(W4Args a) {
     auto group_of = [&](int step) { return min((int)(a.g_mul ? __umulhi((uint32_t)step, a.g_mul) : (uint32_t)step), groups - 1); };
     int seg_g0 = 0;
     auto compute = [&](int c, int slot, int buf) __attribute__((always_inline)) {
-        const char *lq = lds + q_ring + slot * UNIT_LDS + l * 128, *la = lds + a_ring + buf;
+        const char *lq = lds + q_ring + slot * UNIT_LDS + l * 128 + 4 * g, *la = lds + a_ring + buf;
         const char *ls = lds + s_at + (16 * wn + l) * a.s_pitch, *lz = lds + z_at + (16 * wn + l) * a.z_pitch;
         const int k0 = c * CHUNK + wk * UNIT;
 #pragma unroll
         for (int w = 0; w < 2; ++w) {              // 128 elements each
             if (k0 + 128 * w >= nk) break;
-            const u32x4 q = across_rows(*reinterpret_cast<const u32x4 *>(lq + 16 * ((4 * w + g) ^ (l & 7))));
+            uint32_t q[4];                         // lane row g: bytes 4 g .. + 3 of the step's 16
+#pragma unroll
+            for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const uint32_t *>(lq + 16 * ((4 * w + i) ^ (l & 7)));
             u32x4 fa[4][TM];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -326,7 +314,7 @@ __global__ void __launch_bounds__(NT, TM == 1 ? 4 : 2) w4_stream(W4Args a) {
                 }
                 zp[v] = ZP ? (float)*reinterpret_cast<const uint8_t *>(lz + gi) : 8.0f;
             }
-            f32x4 blk[TM], zpt[RAW ? TM : 1];      // a group's sums of a * q (or a * (q - z)) and of a * -z
+            f32x4 blk[TM];                         // a group's sums
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 constexpr int PER = 4 / GV;        // 32-wide steps of a group
@@ -335,14 +323,14 @@ __global__ void __launch_bounds__(NT, TM == 1 ? 4 : 2) w4_stream(W4Args a) {
 #pragma unroll
                 for (int t = 0; t < TM; ++t) {
                     blk[t] = mfma<IN>(fa[i][t], fb, first ? f32x4{0.f, 0.f, 0.f, 0.f} : blk[t]);
-                    if constexpr (RAW) zpt[t] = mfma<IN>(fa[i][t], minus_zero_point(zp[i / PER]), first ? f32x4{0.f, 0.f, 0.f, 0.f} : zpt[t]);
+                    if constexpr (RAW) blk[t] = mfma<IN>(fa[i][t], minus_zero_point(zp[i / PER]), blk[t]);
                 }
                 if (i % PER == PER - 1) {
 #pragma unroll
                     for (int t = 0; t < TM; ++t)
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
-                            acc[t][r] = fmaf(s[i / PER], RAW ? blk[t][r] + zpt[RAW ? t : 0][r] : blk[t][r], acc[t][r]);
+                            acc[t][r] = fmaf(s[i / PER], blk[t][r], acc[t][r]);
                 }
             }
         }
