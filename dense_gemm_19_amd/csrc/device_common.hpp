@@ -11,6 +11,9 @@ namespace dg {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+// the same at any element alignment (gfx950 loads and stores global memory so)
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
 typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 typedef int32_t i32x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -52,8 +55,8 @@ __device__ __forceinline__ void store_out(char *p, int kind, float v) {
     else *reinterpret_cast<uint16_t *>(p) = f32_to_f16_bits(v);
 }
 
-// Four adjacent output elements (p 4-element aligned, in the C dtype), as one
-// vector access.
+// Four adjacent output elements (in the C dtype), as one vector access (loads: p
+// 4-element aligned).
 __device__ __forceinline__ f32x4 load_out4(const char *p, int kind) {
     if (kind == OUT_F32) return *reinterpret_cast<const f32x4 *>(p);
     const u32x2 w = *reinterpret_cast<const u32x2 *>(p);
@@ -68,7 +71,7 @@ __device__ __forceinline__ f32x4 load_out4(const char *p, int kind) {
 
 __device__ __forceinline__ void store_out4(char *p, int kind, const float (&v)[4]) {
     if (kind == OUT_F32) {
-        *reinterpret_cast<f32x4 *>(p) = f32x4{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<f32x4_any *>(p) = f32x4{v[0], v[1], v[2], v[3]};
         return;
     }
     u32x2 w;
@@ -78,7 +81,7 @@ __device__ __forceinline__ void store_out4(char *p, int kind, const float (&v)[4
         const uint32_t hi = kind == OUT_BF16 ? f32_to_bf16_bits(v[2 * h + 1]) : f32_to_f16_bits(v[2 * h + 1]);
         w[h] = lo | (hi << 16);
     }
-    *reinterpret_cast<u32x2 *>(p) = w;
+    *reinterpret_cast<u32x2_any *>(p) = w;
 }
 
 // Sum of S split-K partials, ((p0 + p1) + p2) + ... always in this order, with

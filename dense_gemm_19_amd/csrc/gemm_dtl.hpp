@@ -290,8 +290,10 @@ __device__ __forceinline__ void raster(int t, int tiles_m, int tiles_n, int grou
 // operands' are cleared in LDS before the tile is multiplied (both, since what
 // was read instead may hold infinities or NaN).
 // The workgroup body.  t_direct >= 0: this workgroup computes tile t_direct of
-// p whole (the grouped kernel, which maps its grid itself); otherwise the tile
-// (and K piece) follows from blockIdx.x and gridDim.x as described above.
+// p whole (the grouped kernel, which maps its grid itself), or with SPLIT piece
+// t_direct % S of tile t_direct / S (the experts' kernel; dp_tiles = 0);
+// otherwise the tile (and K piece) follows from blockIdx.x and gridDim.x as
+// described above.
 template <int IN, int BM, int BN, int WGM, int WGN, int NS, int AMODE, int BMODE, bool SPLIT, int NL, bool SA4,
           bool RAGGED = false>
 __device__ __forceinline__ void mfma_dtl_body(const MfmaArgs &p, const int t_direct) {
@@ -333,6 +335,11 @@ __device__ __forceinline__ void mfma_dtl_body(const MfmaArgs &p, const int t_dir
     int t, z = 0, S = 1;
     if (t_direct >= 0) {
         t = t_direct;
+        if constexpr (SPLIT) {
+            S = p.splits;
+            t = t_direct / S;
+            z = t_direct - t * S;
+        }
     } else if (!SPLIT || (int)blockIdx.x < p.dp_tiles) {
         t = xcd_remap(blockIdx.x, SPLIT ? p.dp_tiles : (int)gridDim.x);
     } else {

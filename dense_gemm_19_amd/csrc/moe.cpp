@@ -231,7 +231,9 @@ OpLayout layout(const char *ptr, int64_t rows, int64_t rs, int64_t k, int64_t ks
     return o;
 }
 
-Epilogue plain_epilogue(const Mat &c, int act, bool aligned) {
+// vec4 whatever the alignment: 4 element stores each took 74 us where these take
+// 44 (30 experts of 880 x 1285 BF16).
+Epilogue plain_epilogue(const Mat &c, int act) {
     Epilogue e = {};
     e.C = out_ptr(c);
     e.c_rs = c.rs;
@@ -240,8 +242,7 @@ Epilogue plain_epilogue(const Mat &c, int act, bool aligned) {
     e.alpha = 1.0f;
     e.beta = 0.0f;
     e.act = act;
-    const int64_t v = 4 * c.esize;
-    e.vec4 = aligned && c.cs == c.esize && reinterpret_cast<uintptr_t>(c.ptr) % v == 0 && (c.rows <= 1 || c.rs % v == 0);
+    e.vec4 = c.cs == c.esize;
     return e;
 }
 
@@ -254,6 +255,40 @@ hipError_t launch_product(int in_kind, int load, int tile, int b_mode, bool wgra
 int tile_rows(int load, int tile) { return load == MOE_DTL && tile == T64x128 ? 32 : mfma_tile_bm(tile); }
 int tile_cols(int tile) { return mfma_tile_bn(tile); }
 
+// The pieces of K that each tile is cut into where the tiles leave most of the
+// device idle: `tiles` of them are expected (of at most `most`), with `ktiles` K
+// tiles; a piece keeps at least four.  Few tiles wait for one load after
+// another: 12 rows of 4 experts, 3520 -> 192, took 24.0 us whole, 11.5 us cut.
+// A captured call runs whole: the pieces' workspace may have to be allocated.
+int pieces_of(int load, int tile, int64_t tiles, int64_t ktiles, const Device &d, hipStream_t stream) {
+    if (tile == T256x256 || (load != MOE_DTL && tile == T128x128) || ktiles < 8) return 1;
+    const int64_t s = std::min(d.cus / std::max<int64_t>(tiles, 1), ktiles / 4);
+    if (s < 2) return 1;
+    hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
+    if (hipStreamIsCapturing(stream, &cap) != hipSuccess) {
+        (void)hipGetLastError();
+        return 1;
+    }
+    return cap == hipStreamCaptureStatusNone ? (int)s : 1;
+}
+
+// Launch `units` tiles in a.p.splits pieces each, on the stream's workspace.
+dg_status launch_pieces(int in_kind, int load, int tile, int b_mode, bool wgrad, MoeArgs &a, int64_t units, int64_t bm, int64_t bn,
+                        hipStream_t stream) {
+    if (units > INT32_MAX || units * a.p.splits > INT32_MAX) return DG_ERR_OVERFLOW;
+    WsLease lease;
+    if (a.p.splits > 1) {
+        if (lease_workspace(stream, (size_t)units * a.p.splits * bm * bn * sizeof(float), (size_t)units, &lease) != hipSuccess) {
+            (void)hipGetLastError();
+            return DG_ERR_HIP;
+        }
+        a.p.ws = lease.ws;
+        a.p.counters = lease.counters;
+    }
+    a.units = (int)(units * a.p.splits);
+    return done(launch_product(in_kind, load, tile, b_mode, wgrad, a, units * a.p.splits, stream), stream);
+}
+
 dg_status moe_gemm_entry(const dg_view *A, const dg_view *offsets, const dg_view *W, const dg_view *C, int act,
                          hipStream_t stream) {
     Mat x, off, c;
@@ -265,7 +300,7 @@ dg_status moe_gemm_entry(const dg_view *A, const dg_view *offsets, const dg_view
     if (w.E < 1 || w.one.rows != x.cols || c.rows != x.rows || c.cols != w.one.cols) return DG_ERR_SHAPE_MISMATCH;
     DG_TRY(index_vector(offsets, w.E + 1, &off));
     const int64_t n = x.rows, K = x.cols, N = c.cols;
-    if (n > INT32_MAX || K > INT32_MAX || N > INT32_MAX || w.E > INT32_MAX / 2) return DG_ERR_OVERFLOW;
+    if (n > MOE_MAX_ROWS || K > INT32_MAX || N > INT32_MAX || w.E > INT32_MAX / 2) return DG_ERR_OVERFLOW;
     if (act != DG_ACT_NONE && act != DG_ACT_RELU && act != DG_ACT_GELU_TANH) return DG_ERR_INVALID_ARG;
     if (self_overlaps(c)) return DG_ERR_STRIDE;
     if (spans_overlap(c, x) || spans_overlap(c, w.span) || spans_overlap(c, off)) return DG_ERR_ALIAS;
@@ -281,25 +316,24 @@ dg_status moe_gemm_entry(const dg_view *A, const dg_view *offsets, const dg_view
     const int64_t used = std::min(w.E, n), mean = n / std::max<int64_t>(used, 1);
     int tile = T64x64;
     if (load == MOE_DTL) tile = mean <= 48 ? T64x128 : mean <= 192 ? T128x128 : T256x256;
-    else if (load == MOE_VEC) tile = mean <= 64 ? T64x64 : T128x128;
+    else if (load == MOE_VEC) tile = mean <= 64 || (used + n / 128) * cdiv(N, 128) < d.cus ? T64x64 : T128x128;
     const int bm = tile_rows(load, tile), bn = tile_cols(tile);
 
     MoeArgs a = {};
     a.p.a = Operand{x.ptr, x.rs, x.cs, 1};
     a.p.b = Operand{w.one.ptr, w.one.cs, w.one.rs, 1};
-    a.p.epi = plain_epilogue(c, act, true);
+    a.p.epi = plain_epilogue(c, act);
     a.p.N = (int)N; a.p.K = (int)K;
     a.p.tiles_n = (int)cdiv(N, bn);
     a.p.ktiles = (int)cdiv(K, 64);
-    a.p.splits = 1;
+    a.p.splits = pieces_of(load, tile, (used + n / bm) * a.p.tiles_n, a.p.ktiles, d, stream);
     a.p.group_m = tile == T256x256 ? 4 : 8;
     a.offsets = off.ptr; a.o_s = off.cs;
     a.E = (int)w.E; a.n = (int)n;
     a.e_bs = w.es;
     // every group with rows (the experts and the rows of none) ends in a partial tile at most
     const int64_t units = ((n + std::min(w.E + 1, n) * (bm - 1)) / bm) * a.p.tiles_n;
-    if (units > INT32_MAX) return DG_ERR_OVERFLOW;
-    return done(launch_product(x.dtype == DG_F16 ? IN_F16 : IN_BF16, load, tile, lb.mode, false, a, units, stream), stream);
+    return launch_pieces(x.dtype == DG_F16 ? IN_F16 : IN_BF16, load, tile, lb.mode, false, a, units, bm, bn, stream);
 }
 
 dg_status moe_wgrad_entry(const dg_view *A, const dg_view *D, const dg_view *offsets, const dg_view *dW,
@@ -333,17 +367,17 @@ dg_status moe_wgrad_entry(const dg_view *A, const dg_view *D, const dg_view *off
     MoeArgs a = {};
     a.p.a = Operand{x.ptr, x.cs, x.rs, 1};
     a.p.b = Operand{g.ptr, g.cs, g.rs, 1};
-    a.p.epi = plain_epilogue(w.one, DG_ACT_NONE, w.E == 1 || w.es % (4 * w.one.esize) == 0);
+    a.p.epi = plain_epilogue(w.one, DG_ACT_NONE);
     a.p.M = (int)K; a.p.N = (int)N;
     a.p.tiles_m = (int)cdiv(K, bm); a.p.tiles_n = (int)cdiv(N, bn);
-    a.p.splits = 1;
     a.p.group_m = tile == T256x256 ? 4 : 8;
     a.offsets = off.ptr; a.o_s = off.cs;
     a.E = (int)w.E; a.n = (int)n;
     a.e_cs = w.es;
     const int64_t tiles = (int64_t)a.p.tiles_m * a.p.tiles_n;
     if (tiles > INT32_MAX || tiles * w.E > INT32_MAX) return DG_ERR_OVERFLOW;
-    return done(launch_product(x.dtype == DG_F16 ? IN_F16 : IN_BF16, load, tile, lb.mode, true, a, tiles * w.E, stream), stream);
+    a.p.splits = pieces_of(load, tile, tiles * w.E, cdiv(n / w.E, 64), d, stream);
+    return launch_pieces(x.dtype == DG_F16 ? IN_F16 : IN_BF16, load, tile, lb.mode, true, a, tiles * w.E, bm, bn, stream);
 }
 
 // ---------------------------------------------------------------- 4-bit weights
@@ -373,7 +407,7 @@ dg_status w4_entry(const dg_view *A, const dg_view *offsets, const dg_view *Q, c
     if (q.E < 1 || s.E != q.E || s.one.rows != N || s.one.cols != groups) return DG_ERR_SHAPE_MISMATCH;
     if (Z && (z.E != q.E || z.one.rows != N || z.one.cols != groups)) return DG_ERR_SHAPE_MISMATCH;
     if (experts) DG_TRY(index_vector(offsets, q.E + 1, &off));
-    if (M > INT32_MAX || K > (1 << 20) || N > INT32_MAX || q.E > INT32_MAX / 2) return DG_ERR_OVERFLOW;
+    if (M > (experts ? MOE_MAX_ROWS : INT32_MAX) || K > (1 << 20) || N > INT32_MAX || q.E > INT32_MAX / 2) return DG_ERR_OVERFLOW;
     if (!x.cols_contig() || !q.one.cols_contig()) return DG_ERR_UNSUPPORTED_VIEW;
     // lane offsets within a workgroup's rows and columns are 32-bit
     const int64_t lim = ((int64_t)1 << 31) / 64;
@@ -401,8 +435,12 @@ dg_status w4_entry(const dg_view *A, const dg_view *offsets, const dg_view *Q, c
         return reinterpret_cast<uintptr_t>(m.ptr) % 16 == 0 && es % 16 == 0 && (m.rows <= 1 || m.rs % 16 == 0) &&
                m.cols * m.esize % 16 == 0;
     };
-    a.direct = pieces(x, 0);
-    a.q_direct = pieces(q.one, q.E > 1 ? q.es : 0) && K % 32 == 0 && K > 0;
+    auto words = [](const Mat &m, int64_t es) {    // rows of whole, aligned words
+        return m.cs == m.esize && reinterpret_cast<uintptr_t>(m.ptr) % 4 == 0 && es % 4 == 0 && (m.rows <= 1 || m.rs % 4 == 0) &&
+               m.cols * m.esize % 4 == 0;
+    };
+    const bool usual = K > 0 && K % 32 == 0 && pieces(x, 0) && pieces(q.one, q.E > 1 ? q.es : 0) &&
+                       words(s.one, q.E > 1 ? s.es : 0) && (!Z || words(z.one, q.E > 1 ? z.es : 0));
 
     // Rows of a tile: as few tiles as the largest allows, evenly filled (one
     // matrix), or by the mean count of the experts that can have rows.
@@ -410,7 +448,7 @@ dg_status w4_entry(const dg_view *A, const dg_view *offsets, const dg_view *Q, c
     int tm, rows;
     if (experts) {
         const int64_t mean = M / std::min(q.E, M);
-        tm = mean <= 10 ? 1 : mean <= 24 ? 2 : 4;
+        tm = mean <= 10 ? 1 : mean <= 24 ? 2 : 3;
         tiles_m = (M + std::min(q.E + 1, M) * (16 * tm - 1)) / (16 * tm);
         rows = 16 * tm;
     } else {
@@ -432,30 +470,56 @@ dg_status w4_entry(const dg_view *A, const dg_view *offsets, const dg_view *Q, c
     }
     a.chunks = (int)std::max<int64_t>(cdiv(chunks, splits), 1);
     a.splits = (int)std::max<int64_t>(cdiv(chunks, a.chunks), 1);
-    // LDS: code rings of 2 to 4 units per wave, scales for as many chunks as fit,
-    // and A.  Half of a CU's LDS (two workgroups per CU) where that holds 2 units
-    // ahead, all scales and two chunks of A, or one of a full tile's rows; else
-    // all of it.
-    const int unit = 8 * 2048, a_buf = rows * chunk * 2;
-    auto scales = [&](int64_t seg) {
-        a.seg = (int)seg;
-        a.seg_groups = (int)std::min<int64_t>(groups, seg * chunk / group + 2);
-        a.s_pitch = (int)(cdiv(a.seg_groups * s.one.esize, 16) * 16 + 16);
-        a.z_pitch = Z ? (int)(cdiv(a.seg_groups, 16) * 16 + 16) : 0;
-        return w4_cols(tm) * (a.s_pitch + a.z_pitch);
-    };
-    const int half = 80 * 1024 - 128, whole = 160 * 1024 - 128;
-    int64_t seg = a.chunks;
-    const int a_min = experts ? a_buf : std::min(a.chunks, 2) * a_buf;
-    const int cap = tm == 1 && 2 * unit + scales(seg) + a_min <= half ? half : whole;
-    while (seg > 1 && 2 * unit + scales(seg) + a_buf > cap) seg = cdiv(seg, 2);
-    const int sz = scales(seg);
-    a.depth = 2;
-    while (a.depth < 4 && a.depth < a.chunks && (a.depth + 1) * unit + sz + a_min <= cap) ++a.depth;
-    const int left = (cap - a.depth * unit - sz) / a_buf;
-    a.a_lds = std::max(1, std::min(left, a.chunks)) * a_buf;
-    a.lds_bytes = a.depth * unit + sz + a.a_lds;
-    if (a.lds_bytes > whole) return DG_ERR_OVERFLOW;   // (no size gets here: one chunk's scales are at most 18 KB)
+    // LDS of the usual layout (w4_whole): scales and zero points in words, the pitch
+    // an odd number of them, and rings of 2 to 4 chunks of A and the codes; experts'
+    // rings hold so many of the mean count of rows, and one of a full tile.  Half of
+    // a CU's LDS where 2 chunks of few rows fit and the grid has two workgroups for
+    // a CU, else all.
+    const int half = 80 * 1024 - 128, all = 160 * 1024 - 128;
+    const int unit = 8 * 2048, a_buf = (rows * chunk * 2 + 1023) & ~1023;
+    if (usual) {
+        const int64_t need = std::min<int64_t>(groups, (int64_t)a.chunks * chunk / group + 5);   // from a multiple of 4 on
+        auto pitch = [](int64_t bytes) { return (int)std::max<int64_t>((cdiv(bytes, 4) | 1) * 4, 12); };   // (the reciprocal of one word is 2^32)
+        auto region = [&](int p) { return (w4_cols(tm) * p + 255) & ~255; };
+        a.s_pitch = pitch(need * s.one.esize);
+        a.z_pitch = Z ? pitch(need) : 0;
+        const int sz = region(a.s_pitch) + (Z ? region(a.z_pitch) : 0);
+        const int64_t mean = experts ? std::min<int64_t>(M / std::min(q.E, M) + 1, rows) : rows;
+        const int a_mean = (int)((mean * chunk * 2 + 1023) & ~1023);
+        auto fits = [&](int depth, int bufs, int cap) {
+            a.depth = depth;
+            a.a_lds = (cap - depth * unit - sz) & ~1023;   // (all there is: experts differ in rows)
+            a.lds_bytes = depth * unit + a.a_lds + sz;
+            return a.a_lds >= std::max(a_buf, bufs * a_mean);
+        };
+        const int most = std::min(4, std::max(a.chunks, 2));
+        const bool pairs = tm == 1 && units * a.splits > d.cus;
+        for (int n = most; n > 1 && pairs && !a.whole; --n) a.whole = fits(n, n, half);
+        for (int n = most; n > 1 && !a.whole; --n) a.whole = fits(n, n, all);
+        auto recip = [](int d) { return (uint32_t)((((uint64_t)1 << 32) + d - 1) / d); };
+        a.s_mul = recip(a.s_pitch / 4);
+        a.z_mul = Z ? recip(a.z_pitch / 4) : 0;
+    }
+    // Any other layout (w4_stream): a unit of codes per wave, scales for as many
+    // chunks as fit, and all of A where that fits, else one chunk.
+    if (!a.whole) {
+        auto scales = [&](int64_t seg) {
+            a.seg = (int)seg;
+            a.seg_groups = (int)std::min<int64_t>(groups, seg * chunk / group + 2);
+            a.s_pitch = (int)(cdiv(a.seg_groups * s.one.esize, 16) * 16 + 16);
+            a.z_pitch = Z ? (int)(cdiv(a.seg_groups, 16) * 16 + 16) : 0;
+            return w4_cols(tm) * (a.s_pitch + a.z_pitch);
+        };
+        int64_t seg = a.chunks;
+        const int cap = tm == 1 && unit + scales(seg) + a_buf <= half ? half : all;
+        while (seg > 1 && unit + scales(seg) + a_buf > cap) seg = cdiv(seg, 2);
+        const int sz = scales(seg), left = (cap - unit - sz) / a_buf;
+        a.a_lds = std::max(1, std::min(left, a.chunks)) * a_buf;
+        // (the kernel's end adds the waves' sums in the same LDS: 8 KB each of 16 tm rows x 16 columns)
+        a.lds_bytes = std::max(unit + sz + a.a_lds, tm * 8 * 1024);
+    }
+    if (a.lds_bytes > all) return DG_ERR_OVERFLOW;   // (no size gets here: one chunk's scales are at most 18 KB)
+    a.units = (int)(units * a.splits);
     if (units * a.splits > INT32_MAX) return DG_ERR_OVERFLOW;
     WsLease lease;
     if (a.splits > 1) {

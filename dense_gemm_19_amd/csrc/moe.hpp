@@ -12,6 +12,7 @@ namespace dg {
 // ---------------------------------------------------------------- routing (moe_route.hip)
 
 constexpr int MOE_MAX_EXPERTS = 2048;    // LDS counters of a sort workgroup: 16 waves x E
+constexpr int MOE_MAX_ROWS = 1 << 28;     // of the experts' products: tile counts of 64 experts fit 32 bits
 constexpr int SORT_ONE_MAX = 16384;      // ids sorted by one workgroup; more take three launches
 constexpr int SORT_BLOCK = 4096;         // ids per workgroup of the three-launch sort (at least E fit half of it)
 
@@ -63,6 +64,7 @@ struct MoeArgs {
     MfmaArgs p;
     const char *offsets; int64_t o_s;      // [E + 1] int32
     int E, n;                              // experts, grouped rows
+    int units;                             // forward: workgroups of the grid
     int64_t e_bs, e_cs;                    // bytes per expert of B (forward) and C (wgrad)
 };
 
@@ -96,8 +98,10 @@ struct W4Args {
     int slabs;                             // column slabs of w4_cols(tm)
     int chunks, splits;                    // K in pieces of `chunks` chunks; splits > 1: one matrix only
     float *ws; int *counters;              // splits > 1: [tiles][splits][16 tm x w4_cols(tm)] sums, a counter per tile (0)
-    int direct, q_direct;                  // A, Q: rows of whole, aligned 16-byte pieces
-    int depth;                             // code units in flight per wave (2 to 4)
+    int units;                             // workgroups of the grid
+    int whole;                             // A and Q in aligned 16-byte pieces, scales and zero points in words: w4_whole
+    uint32_t s_mul, z_mul;                 // whole: ceil(2^32 / (pitch / 4)), to divide by it
+    int depth;                             // whole: code units per wave in LDS (2 to 4)
     int a_lds;                             // LDS bytes for A: at least one chunk of 16 tm (or all M) rows
     int seg, seg_groups;                   // chunks whose scales are in LDS together, groups they touch at most
     int s_pitch, z_pitch;                  // bytes of a column's scales and zero points in LDS
@@ -107,11 +111,12 @@ struct W4Args {
 // Geometry of the kernel by rows / 16 of a workgroup: columns, K elements of a
 // chunk.  Few rows take narrow slabs, whose LDS
 // lets two workgroups share a CU; more rows take shorter chunks, whose A fits.
-constexpr int W4_MAX_TM = 4;
+constexpr int W4_MAX_TM = 3;
 constexpr int w4_cols(int tm) { return tm == 1 ? 32 : 64; }
 constexpr int w4_chunk(int tm) { return tm == 1 ? 1024 : 512; }
 
-// tm: rows of a workgroup / 16, 1 to W4_MAX_TM
+// tm: rows of a workgroup / 16, 1 to W4_MAX_TM (4, whose chunk of A leaves LDS
+// no room for a second, took 26 us for 248 x 1452 x 2592 where 3 takes 21.4)
 hipError_t launch_w4(int in_kind, int tm, const W4Args &a, int64_t units, hipStream_t stream);
 
 }  // namespace dg

@@ -25,21 +25,26 @@ namespace moe {
 
 // The product of this workgroup's expert: p's pointers and extents, and the
 // tile.  False: nothing to do.
-template <int BM, bool WGRAD>
+// Split K (a.p.splits pieces a tile): a tile's pieces are units of their own,
+// one after another; p's sums and counters become the expert's.
+template <int BM, int BN, bool WGRAD, bool SPLIT>
 __device__ __forceinline__ bool expert_product(const MoeArgs &a, MfmaArgs &p, int &t) {
     constexpr int KEL = dtl::KB / 2;
     p = a.p;
+    const int S = SPLIT ? a.p.splits : 1;
+    int before;                              // tiles of the experts before
     if constexpr (WGRAD) {
         // The experts in turn, each one's tiles dealt over all XCDs: experts
         // differ in rows, and a run of whole experts per XCD would leave the
         // XCD with the longest ones working alone (8 experts of 500 to 1900
         // rows, 4096 x 4096 FP32: 492 us that way, 310 us this way).
-        const int tiles = a.p.tiles_m * a.p.tiles_n, e = blockIdx.x / tiles;
+        const int tiles = a.p.tiles_m * a.p.tiles_n, e = blockIdx.x / (tiles * S);
         int begin, rows;
         group_rows(a.offsets, a.o_s, a.E, a.n, e, begin, rows);
         begin = __builtin_amdgcn_readfirstlane(begin);
         rows = __builtin_amdgcn_readfirstlane(rows);
-        t = xcd_run(blockIdx.x - e * tiles, tiles);
+        t = xcd_run(blockIdx.x - e * tiles * S, tiles * S);
+        before = e * tiles;
         p.a.ptr += (int64_t)begin * p.a.k_stride;
         p.b.ptr += (int64_t)begin * p.b.k_stride;
         p.epi.C += (int64_t)e * a.e_cs;
@@ -47,7 +52,8 @@ __device__ __forceinline__ bool expert_product(const MoeArgs &a, MfmaArgs &p, in
         p.ktiles = (rows + KEL - 1) / KEL;
     } else {
         Slot s;
-        if (!find_slot<BM>(a.offsets, a.o_s, a.E, a.n, a.p.tiles_n, blockIdx.x, s)) return false;
+        if (!find_slot<BM>(a.offsets, a.o_s, a.E, a.n, a.p.tiles_n * S, a.units, blockIdx.x, s)) return false;
+        before = s.above * a.p.tiles_n;
         p.a.ptr += (int64_t)s.begin * p.a.r_stride;
         p.epi.C += (int64_t)s.begin * p.epi.c_rs;
         p.M = s.rows;
@@ -56,15 +62,20 @@ __device__ __forceinline__ bool expert_product(const MoeArgs &a, MfmaArgs &p, in
         if (s.e < a.E) p.b.ptr += (int64_t)s.e * a.e_bs;
         else p.K = p.ktiles = 0;             // rows of no expert: zero (every activation keeps 0)
     }
+    if constexpr (SPLIT) {
+        p.kt_per_split = (p.ktiles + S - 1) / S;
+        p.ws += (int64_t)before * S * (BM * BN);
+        p.counters += before;
+    }
     return true;
 }
 
-template <int IN, int BM, int BN, int WGM, int WGN, int NS, int AMODE, int BMODE, int NL, bool WGRAD>
+template <int IN, int BM, int BN, int WGM, int WGN, int NS, int AMODE, int BMODE, int NL, bool WGRAD, bool SPLIT>
 __global__ void __launch_bounds__(64 * WGM * WGN) moe_dtl(MoeArgs a) {
     MfmaArgs p;
     int t;
-    if (!expert_product<BM, WGRAD>(a, p, t)) return;
-    dtl::mfma_dtl_body<IN, BM, BN, WGM, WGN, NS, AMODE, BMODE, false, NL, false, true>(p, t);
+    if (!expert_product<BM, BN, WGRAD, SPLIT>(a, p, t)) return;
+    dtl::mfma_dtl_body<IN, BM, BN, WGM, WGN, NS, AMODE, BMODE, SPLIT, NL, false, true>(p, t);
 }
 
 // ------------------------------------------------------------------ register-staged kernel
@@ -140,8 +151,9 @@ struct RegIO {
 };
 
 // B x B tiles, 4 waves (2 x 2), a two-stage LDS ring: the next tile's loads are
-// in flight while the current one is multiplied.
-template <int IN, int B, int AMODE, int BMODE, int LOAD, bool WGRAD>
+// in flight while the current one is multiplied.  SPLIT: a piece of K, whose sums
+// the tile's last piece adds in the order of K, as in the dense kernels.
+template <int IN, int B, int AMODE, int BMODE, int LOAD, bool WGRAD, bool SPLIT>
 __global__ void __launch_bounds__(256) moe_reg(MoeArgs a) {
     constexpr int NT = 256, T = B / 32, STAGE = 2 * B * dtl::KB, KEL = 64;
     using AIO = RegIO<AMODE, B, LOAD, NT>;
@@ -149,7 +161,10 @@ __global__ void __launch_bounds__(256) moe_reg(MoeArgs a) {
     __shared__ __attribute__((aligned(16))) char ring[2 * STAGE];
     MfmaArgs p;
     int t;
-    if (!expert_product<B, WGRAD>(a, p, t)) return;
+    if (!expert_product<B, B, WGRAD, SPLIT>(a, p, t)) return;
+    const int S = SPLIT ? p.splits : 1, piece = t, z = SPLIT ? t % S : 0;
+    t /= S;
+    const int kt0 = SPLIT ? z * p.kt_per_split : 0, kt1 = SPLIT ? min(kt0 + p.kt_per_split, p.ktiles) : p.ktiles;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
     int tm, tn;
     dtl::raster(t, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
@@ -170,13 +185,13 @@ __global__ void __launch_bounds__(256) moe_reg(MoeArgs a) {
         AIO::store(st, ra, tid);
         BIO::store(st + B * dtl::KB, rb, tid);
     };
-    if (p.ktiles > 0) {
-        fetch(0);
-        put(ring, 0);
+    if (kt0 < kt1) {
+        fetch(kt0);
+        put(ring + (kt0 & 1) * STAGE, kt0);
     }
     __syncthreads();
-    for (int kt = 0; kt < p.ktiles; ++kt) {
-        const bool more = kt + 1 < p.ktiles;
+    for (int kt = kt0; kt < kt1; ++kt) {
+        const bool more = kt + 1 < kt1;
         if (more) fetch(kt + 1);
         const char *la = ring + (kt & 1) * STAGE, *lb = la + B * dtl::KB;
 #pragma unroll
@@ -193,6 +208,41 @@ __global__ void __launch_bounds__(256) moe_reg(MoeArgs a) {
         }
         if (more) put(ring + ((kt & 1) ^ 1) * STAGE, kt + 1);
         __syncthreads();
+    }
+    if constexpr (SPLIT) {
+        // [tile][piece][element][thread]: every thread adds its own elements
+        __shared__ int is_last;
+        float *tile = p.ws + (int64_t)(piece - z) * (B * B) + tid;
+        auto at = [&](int q, int i, int j, int e) __attribute__((always_inline)) {
+            return tile + (int64_t)q * (B * B) + ((i * T + j) * 4 + e) * NT;
+        };
+#pragma unroll
+        for (int i = 0; i < T; ++i)
+#pragma unroll
+            for (int j = 0; j < T; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    __hip_atomic_store(at(z, i, j, e), acc[i][j][e], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+        if (tid == 0) is_last = take_last_ticket(p.counters + t, S);
+        __syncthreads();
+        if (!is_last) return;
+#pragma unroll 1
+        for (int q = 0; q < S; ++q) {
+            f32x4 v[T][T];
+#pragma unroll
+            for (int i = 0; i < T; ++i)
+#pragma unroll
+                for (int j = 0; j < T; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[i][j][e] = __hip_atomic_load(at(q, i, j, e), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+            for (int i = 0; i < T; ++i)
+#pragma unroll
+                for (int j = 0; j < T; ++j) acc[i][j] = q == 0 ? v[i][j] : acc[i][j] + v[i][j];
+        }
+        if (tid == 0) __hip_atomic_store(p.counters + t, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     // a lane holds row lane % 16 and 4 adjacent columns of each 16 x 16 block
     const Epilogue &ep = p.epi;
@@ -227,47 +277,56 @@ __global__ void __launch_bounds__(256) moe_reg(MoeArgs a) {
 // operands M/N-contiguous (wgrad).  The tiles are the dense kernel's, plus 32 x
 // 128 for a few rows per expert.
 // The host counts the tiles by the same tile: one that a direction does not
-// have is an error, never another kernel.
-template <int IN>
-hipError_t launch_dtl(int tile, int b_mode, bool wgrad, const MoeArgs &a, int64_t units, hipStream_t s) {
-    if (wgrad) {
-        if (tile == T256x256) DG_MOE_LAUNCH((moe_dtl<IN, 256, 256, 2, 4, 2, MNMAJ, MNMAJ, 4, true>), 512);
-        else if (tile == T128x128) DG_MOE_LAUNCH((moe_dtl<IN, 128, 128, 2, 2, 2, MNMAJ, MNMAJ, 0, true>), 256);
-        else return hipErrorInvalidValue;
-    } else if (b_mode == KMAJ) {
-        if (tile == T256x256) DG_MOE_LAUNCH((moe_dtl<IN, 256, 256, 2, 4, 2, KMAJ, KMAJ, 4, false>), 512);
-        else if (tile == T128x128) DG_MOE_LAUNCH((moe_dtl<IN, 128, 128, 2, 2, 2, KMAJ, KMAJ, 0, false>), 256);
-        else if (tile == T64x128) DG_MOE_LAUNCH((moe_dtl<IN, 32, 128, 1, 4, 7, KMAJ, KMAJ, 0, false>), 256);
-        else return hipErrorInvalidValue;
-    } else {
-        if (tile == T256x256) DG_MOE_LAUNCH((moe_dtl<IN, 256, 256, 2, 4, 2, KMAJ, MNMAJ, 4, false>), 512);
-        else if (tile == T128x128) DG_MOE_LAUNCH((moe_dtl<IN, 128, 128, 2, 2, 2, KMAJ, MNMAJ, 0, false>), 256);
-        else if (tile == T64x128) DG_MOE_LAUNCH((moe_dtl<IN, 32, 128, 1, 4, 7, KMAJ, MNMAJ, 0, false>), 256);
-        else return hipErrorInvalidValue;
+// have (or not split) is an error, never another kernel.
+template <int IN, int BMODE, bool WGRAD, bool SPLIT>
+hipError_t launch_dtl(int tile, const MoeArgs &a, int64_t units, hipStream_t s) {
+    constexpr int AMODE = WGRAD ? MNMAJ : KMAJ;
+    if (tile == T128x128) {
+        DG_MOE_LAUNCH((moe_dtl<IN, 128, 128, 2, 2, 2, AMODE, BMODE, 0, WGRAD, SPLIT>), 256);
+        return hipGetLastError();
     }
+    if constexpr (!WGRAD) {
+        if (tile == T64x128) {
+            DG_MOE_LAUNCH((moe_dtl<IN, 32, 128, 1, 4, 7, AMODE, BMODE, 0, WGRAD, SPLIT>), 256);
+            return hipGetLastError();
+        }
+    }
+    if constexpr (!SPLIT) {
+        if (tile == T256x256) {
+            DG_MOE_LAUNCH((moe_dtl<IN, 256, 256, 2, 4, 2, AMODE, BMODE, 4, WGRAD, SPLIT>), 512);
+            return hipGetLastError();
+        }
+    }
+    return hipErrorInvalidValue;
+}
+
+// any strides (MOE_ELEM): the element loads make every operand K-contiguous in LDS
+template <int IN, int LOAD, int B, bool SPLIT>
+hipError_t launch_reg(int b_mode, bool wgrad, const MoeArgs &a, int64_t units, hipStream_t s) {
+    constexpr int MN = LOAD == MOE_ELEM ? KMAJ : MNMAJ;
+    if (wgrad) DG_MOE_LAUNCH((moe_reg<IN, B, MN, MN, LOAD, true, SPLIT>), 256);
+    else if (LOAD == MOE_ELEM || b_mode == KMAJ) DG_MOE_LAUNCH((moe_reg<IN, B, KMAJ, KMAJ, LOAD, false, SPLIT>), 256);
+    else DG_MOE_LAUNCH((moe_reg<IN, B, KMAJ, MN, LOAD, false, SPLIT>), 256);
     return hipGetLastError();
 }
 
-template <int IN, int LOAD, int B>
-hipError_t launch_reg(int b_mode, bool wgrad, const MoeArgs &a, int64_t units, hipStream_t s) {
-    if constexpr (LOAD == MOE_ELEM) {   // any strides: the element loads make every operand K-contiguous in LDS
-        if (wgrad) DG_MOE_LAUNCH((moe_reg<IN, B, KMAJ, KMAJ, LOAD, true>), 256);
-        else DG_MOE_LAUNCH((moe_reg<IN, B, KMAJ, KMAJ, LOAD, false>), 256);
-    } else {
-        if (wgrad) DG_MOE_LAUNCH((moe_reg<IN, B, MNMAJ, MNMAJ, LOAD, true>), 256);
-        else if (b_mode == KMAJ) DG_MOE_LAUNCH((moe_reg<IN, B, KMAJ, KMAJ, LOAD, false>), 256);
-        else DG_MOE_LAUNCH((moe_reg<IN, B, KMAJ, MNMAJ, LOAD, false>), 256);
+template <int IN, bool SPLIT>
+hipError_t launch_s(int load, int tile, int b_mode, bool wgrad, const MoeArgs &a, int64_t units, hipStream_t s) {
+    if (load == MOE_DTL && wgrad) return launch_dtl<IN, MNMAJ, true, SPLIT>(tile, a, units, s);
+    if (load == MOE_DTL && b_mode == KMAJ) return launch_dtl<IN, KMAJ, false, SPLIT>(tile, a, units, s);
+    if (load == MOE_DTL) return launch_dtl<IN, MNMAJ, false, SPLIT>(tile, a, units, s);
+    if constexpr (!SPLIT) {
+        if (load == MOE_VEC && tile == T128x128) return launch_reg<IN, MOE_VEC, 128, SPLIT>(b_mode, wgrad, a, units, s);
     }
-    return hipGetLastError();
+    if (load == MOE_VEC && tile == T64x64) return launch_reg<IN, MOE_VEC, 64, SPLIT>(b_mode, wgrad, a, units, s);
+    if (load == MOE_ELEM && tile == T64x64) return launch_reg<IN, MOE_ELEM, 64, SPLIT>(b_mode, wgrad, a, units, s);
+    return hipErrorInvalidValue;
 }
 
 template <int IN>
 hipError_t launch(int load, int tile, int b_mode, bool wgrad, const MoeArgs &a, int64_t units, hipStream_t s) {
-    if (load == MOE_DTL) return launch_dtl<IN>(tile, b_mode, wgrad, a, units, s);
-    if (load == MOE_VEC && tile == T128x128) return launch_reg<IN, MOE_VEC, 128>(b_mode, wgrad, a, units, s);
-    if (load == MOE_VEC && tile == T64x64) return launch_reg<IN, MOE_VEC, 64>(b_mode, wgrad, a, units, s);
-    if (load == MOE_ELEM && tile == T64x64) return launch_reg<IN, MOE_ELEM, 64>(b_mode, wgrad, a, units, s);
-    return hipErrorInvalidValue;
+    return a.p.splits > 1 ? launch_s<IN, true>(load, tile, b_mode, wgrad, a, units, s)
+                          : launch_s<IN, false>(load, tile, b_mode, wgrad, a, units, s);
 }
 #undef DG_MOE_LAUNCH
 

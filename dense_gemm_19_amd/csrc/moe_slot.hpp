@@ -24,8 +24,9 @@ __device__ __forceinline__ int lane_sum(int v, int lane) {
 }
 
 // One expert's rows and this workgroup's unit within its tiles (wave-uniform).
-// e == E: the rows that belong to no expert (from offsets[E] on).
-struct Slot { int e, begin, rows, unit; };
+// e == E: the rows that belong to no expert (from offsets[E] on).  above: rows
+// of tiles of the groups before it.
+struct Slot { int e, begin, rows, unit, above; };
 
 // Rows [begin, end) of group e (e == E: the rest up to n).  Offsets are clamped
 // into [0, n], so that no value of theirs reaches outside the operands.
@@ -37,22 +38,26 @@ __device__ __forceinline__ void group_rows(const char *off, int64_t o_s, int E, 
 }
 
 // The slot of workgroup b: groups in order, each with ceil(rows / BM) * tiles_n
-// units.  False: b is past the last unit.  Every wave does this by itself.
+// units (tiles_n: units per row of tiles).  False: b is past the last unit, or
+// the offsets name more than the grid's `units`, which only overlapping groups
+// can (n is at most 2^28, so that 64 groups' tile rows fit 32 bits).  Every wave
+// does this by itself.
 template <int BM>
-__device__ __forceinline__ bool find_slot(const char *off, int64_t o_s, int E, int n, int tiles_n, int b, Slot &s) {
+__device__ __forceinline__ bool find_slot(const char *off, int64_t o_s, int E, int n, int tiles_n, int units, int b, Slot &s) {
     const int lane = threadIdx.x & 63;
     int begin, rows;
     group_rows(off, o_s, E, n, lane, begin, rows);
     int mine = lane <= E ? (rows + BM - 1) / BM : 0;
     int upto = lane_sum(mine, lane);
-    int total = __builtin_amdgcn_readlane(upto, 63);
+    int64_t total = __builtin_amdgcn_readlane(upto, 63);
     for (int e0 = 64; e0 <= E; e0 += 64) {   // more than 63 experts: the tiles of the rest
         int bb, rr;
         group_rows(off, o_s, E, n, e0 + lane, bb, rr);
         total += __builtin_amdgcn_readlane(lane_sum(e0 + lane <= E ? (rr + BM - 1) / BM : 0, lane), 63);
     }
-    if (b >= total * tiles_n) return false;
-    const int u = xcd_run(b, total * tiles_n);
+    total *= tiles_n;
+    if (b >= total || total > units) return false;
+    const int u = xcd_run(b, (int)total);
     const int want = u / tiles_n;            // tile row among all groups'
     int base = 0, e0 = 0;
     while (true) {
@@ -62,7 +67,8 @@ __device__ __forceinline__ bool find_slot(const char *off, int64_t o_s, int E, i
             s.e = e0 + l;
             s.begin = __builtin_amdgcn_readlane(begin, l);
             s.rows = __builtin_amdgcn_readlane(rows, l);
-            s.unit = u - (base + __builtin_amdgcn_readlane(upto - mine, l)) * tiles_n;
+            s.above = base + __builtin_amdgcn_readlane(upto - mine, l);
+            s.unit = u - s.above * tiles_n;
             return true;
         }
         base += __builtin_amdgcn_readlane(upto, 63);

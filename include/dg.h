@@ -397,10 +397,11 @@ dg_status dg_quant_fp8(const dg_view *X, const dg_view *Q, const dg_view *S, dg_
  * memory: a dropped choice.  Conventions as for the GEMM entry points
  * (asynchronous on `stream`, outputs untouched on error, no atomics on
  * floating-point values: results are bitwise reproducible).  Every one may be
- * captured in a HIP graph.  None needs scratch memory but dg_gemm_w4, which
- * splits K over workgroups where N is small, on the stream's split-K workspace
- * (a captured call does not split, so its last bits may differ).  Views of index vectors are [len] or
- * [1][len].
+ * captured in a HIP graph.  Where a product's tiles leave most of the device idle
+ * and K is long, dg_gemm_w4, dg_moe_gemm and dg_moe_gemm_wgrad cut K into pieces on
+ * the stream's split-K workspace; a captured call does not (so its last bits may
+ * differ), and the other entry points need no scratch memory.  Views of index
+ * vectors are [len] or [1][len].
  */
 
 /* Sort the router's choices by expert, stably (equal experts keep the order of
@@ -453,7 +454,7 @@ dg_status dg_moe_combine_grad(const dg_view *dY, const dg_view *Ys, const dg_vie
  *   act: a dg_act value.
  * Errors: DG_ERR_NDIM (W not 3-D), DG_ERR_INVALID_ARG (act), DG_ERR_DTYPE,
  * DG_ERR_SHAPE_MISMATCH, DG_ERR_STRIDE, DG_ERR_ALIAS, DG_ERR_OVERFLOW (more than
- * 2^31 - 1 tiles), view errors. */
+ * 2^28 rows or 2^31 - 1 tiles), view errors. */
 dg_status dg_moe_gemm(const dg_view *A, const dg_view *offsets, const dg_view *W, const dg_view *C, dg_act act,
                       hipStream_t stream);
 
