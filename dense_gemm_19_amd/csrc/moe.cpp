@@ -92,6 +92,14 @@ dg_status done(hipError_t e, hipStream_t stream) {
     return DG_SUCCESS;
 }
 
+// The stream is being captured (or cannot be asked): no workspace is allocated.
+bool capturing(hipStream_t stream) {
+    hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
+    if (hipStreamIsCapturing(stream, &cap) == hipSuccess) return cap != hipStreamCaptureStatusNone;
+    (void)hipGetLastError();
+    return true;
+}
+
 char *out_ptr(const Mat &m) { return const_cast<char *>(m.ptr); }
 
 // ---------------------------------------------------------------- routing
@@ -128,6 +136,15 @@ dg_status sort_entry(const dg_view *ids, int32_t E, const dg_view *offsets, cons
     a.order = reinterpret_cast<int *>(out_ptr(ord));
     a.pos = reinterpret_cast<int *>(out_ptr(p));
     a.blocks = (int)cdiv(n, SORT_BLOCK);
+    a.table = nullptr;
+    WsLease lease;
+    if (n >= SORT_TABLE_MIN && (int64_t)a.blocks * E <= SORT_TABLE_MAX && !capturing(stream)) {
+        if (lease_workspace(stream, (size_t)a.blocks * E * sizeof(int), 0, &lease) != hipSuccess) {
+            (void)hipGetLastError();
+            return DG_ERR_HIP;
+        }
+        a.table = reinterpret_cast<int *>(lease.ws);
+    }
     return done(launch_moe_sort(a, stream), stream);
 }
 
@@ -252,8 +269,8 @@ hipError_t launch_product(int in_kind, int load, int tile, int b_mode, bool wgra
                              : launch_moe_gemm_bf16(load, tile, b_mode, wgrad, a, units, s);
 }
 
-int tile_rows(int load, int tile) { return load == MOE_DTL && tile == T64x128 ? 32 : mfma_tile_bm(tile); }
-int tile_cols(int tile) { return mfma_tile_bn(tile); }
+int tile_rows(int load, int tile) { return tile == MOE_T192 ? 192 : load == MOE_DTL && tile == T64x128 ? 32 : mfma_tile_bm(tile); }
+int tile_cols(int tile) { return tile == MOE_T192 ? 256 : mfma_tile_bn(tile); }
 
 // The pieces of K that each tile is cut into where the tiles leave most of the
 // device idle: `tiles` of them are expected (of at most `most`), with `ktiles` K
@@ -261,15 +278,10 @@ int tile_cols(int tile) { return mfma_tile_bn(tile); }
 // another: 12 rows of 4 experts, 3520 -> 192, took 24.0 us whole, 11.5 us cut.
 // A captured call runs whole: the pieces' workspace may have to be allocated.
 int pieces_of(int load, int tile, int64_t tiles, int64_t ktiles, const Device &d, hipStream_t stream) {
-    if (tile == T256x256 || (load != MOE_DTL && tile == T128x128) || ktiles < 8) return 1;
+    if (tile == T256x256 || tile == MOE_T192 || (load != MOE_DTL && tile == T128x128) || ktiles < 8) return 1;
     const int64_t s = std::min(d.cus / std::max<int64_t>(tiles, 1), ktiles / 4);
     if (s < 2) return 1;
-    hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
-    if (hipStreamIsCapturing(stream, &cap) != hipSuccess) {
-        (void)hipGetLastError();
-        return 1;
-    }
-    return cap == hipStreamCaptureStatusNone ? (int)s : 1;
+    return capturing(stream) ? 1 : (int)s;
 }
 
 // Launch `units` tiles in a.p.splits pieces each, on the stream's workspace.
@@ -315,7 +327,13 @@ dg_status moe_gemm_entry(const dg_view *A, const dg_view *offsets, const dg_view
     // Tile rows by the mean count of the experts that can have rows.
     const int64_t used = std::min(w.E, n), mean = n / std::max<int64_t>(used, 1);
     int tile = T64x64;
-    if (load == MOE_DTL) tile = mean <= 48 ? T64x128 : mean <= 192 ? T128x128 : T256x256;
+    if (load == MOE_DTL) {
+        tile = mean <= 48 ? T64x128 : mean <= 192 ? T128x128 : T256x256;
+        // 192 rows where that leaves a whole round of the device less (64 experts of
+        // 234 rows, 4096 -> 512 FP16: 127 us with 256 rows on 181 CUs, 120.5).
+        auto rounds = [&](int64_t rows) { return cdiv((used / 2 + cdiv(n, rows)) * cdiv(N, 256), d.cus) * rows; };
+        if (tile == T256x256 && rounds(192) * 10 < rounds(256) * 9) tile = MOE_T192;
+    }
     else if (load == MOE_VEC) tile = mean <= 64 || (used + n / 128) * cdiv(N, 128) < d.cus ? T64x64 : T128x128;
     const int bm = tile_rows(load, tile), bn = tile_cols(tile);
 
@@ -327,7 +345,7 @@ dg_status moe_gemm_entry(const dg_view *A, const dg_view *offsets, const dg_view
     a.p.tiles_n = (int)cdiv(N, bn);
     a.p.ktiles = (int)cdiv(K, 64);
     a.p.splits = pieces_of(load, tile, (used + n / bm) * a.p.tiles_n, a.p.ktiles, d, stream);
-    a.p.group_m = tile == T256x256 ? 4 : 8;
+    a.p.group_m = tile == T256x256 || tile == MOE_T192 ? 4 : 8;
     a.offsets = off.ptr; a.o_s = off.cs;
     a.E = (int)w.E; a.n = (int)n;
     a.e_bs = w.es;
@@ -463,11 +481,8 @@ dg_status w4_entry(const dg_view *A, const dg_view *offsets, const dg_view *Q, c
     const int chunk = w4_chunk(tm);
     const int64_t chunks = cdiv(K, chunk), units = tiles_m * a.slabs;
     int64_t splits = 1;
-    if (!experts && chunks * chunk > 4096 && 2 * units <= d.cus) {
-        hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
-        if (hipStreamIsCapturing(stream, &cap) != hipSuccess) (void)hipGetLastError();
-        else if (cap == hipStreamCaptureStatusNone) splits = std::min<int64_t>(d.cus / units, chunks / 2);
-    }
+    if (!experts && chunks * chunk > 4096 && 2 * units <= d.cus && !capturing(stream))
+        splits = std::min<int64_t>(d.cus / units, chunks / 2);
     a.chunks = (int)std::max<int64_t>(cdiv(chunks, splits), 1);
     a.splits = (int)std::max<int64_t>(cdiv(chunks, a.chunks), 1);
     // LDS of the usual layout (w4_whole): scales and zero points in words, the pitch

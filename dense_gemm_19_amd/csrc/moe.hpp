@@ -14,7 +14,9 @@ namespace dg {
 constexpr int MOE_MAX_EXPERTS = 2048;    // LDS counters of a sort workgroup: 16 waves x E
 constexpr int MOE_MAX_ROWS = 1 << 28;     // of the experts' products: tile counts of 64 experts fit 32 bits
 constexpr int SORT_ONE_MAX = 16384;      // ids sorted by one workgroup; more take three launches
-constexpr int SORT_BLOCK = 4096;         // ids per workgroup of the three-launch sort (at least E fit half of it)
+constexpr int SORT_BLOCK = 4096;         // ids per workgroup of the two- and three-launch sorts (at least E fit half of it)
+constexpr int SORT_TABLE_MIN = 8192;     // ids from which two launches are quicker than one workgroup
+constexpr int SORT_TABLE_MAX = 1 << 15;  // counts that every workgroup of the two-launch sort reads at most
 
 struct SortArgs {
     const char *ids; int64_t i_rs, i_cs;   // [T][k]
@@ -22,7 +24,8 @@ struct SortArgs {
     int k, n;                              // n = T * k
     int E, bits;                           // E < 2^bits + 1: every expert id fits `bits` bits
     int *offsets, *order, *pos;            // contiguous: [E + 1], [n], [T][k]
-    int blocks;                            // workgroups of the three-launch sort
+    int blocks;                            // workgroups of the two- and three-launch sorts
+    int *table;                            // two launches: [blocks][E] counts, or null
 };
 
 struct GatherArgs {
@@ -74,8 +77,9 @@ struct MoeArgs {
 //            contiguous along one of their dims, at least 8 long.
 //  MOE_ELEM: element loads, any strides.
 enum MoeLoad : int { MOE_DTL = 0, MOE_VEC = 1, MOE_ELEM = 2 };
+constexpr int MOE_T192 = NUM_MFMA_TILES;   // MOE_DTL, forward: 192 x 256
 
-// tile: MfmaTile (T64x128 here stands for the 32 x 128 tile of MOE_DTL).
+// tile: MfmaTile or MOE_T192 (T64x128 here stands for the 32 x 128 tile of MOE_DTL).
 // units: an upper bound of the work units (forward) or their number (wgrad).
 hipError_t launch_moe_gemm_f16(int load, int tile, int b_mode, bool wgrad, const MoeArgs &a, int64_t units,
                                hipStream_t stream);

@@ -400,8 +400,9 @@ dg_status dg_quant_fp8(const dg_view *X, const dg_view *Q, const dg_view *S, dg_
  * captured in a HIP graph.  Where a product's tiles leave most of the device idle
  * and K is long, dg_gemm_w4, dg_moe_gemm and dg_moe_gemm_wgrad cut K into pieces on
  * the stream's split-K workspace; a captured call does not (so its last bits may
- * differ), and the other entry points need no scratch memory.  Views of index
- * vectors are [len] or [1][len].
+ * differ).  dg_moe_sort of many ids keeps its counts there (a captured call does
+ * without); the other entry points need no scratch memory.  Views of index vectors
+ * are [len] or [1][len].
  */
 
 /* Sort the router's choices by expert, stably (equal experts keep the order of
