@@ -276,9 +276,11 @@ int tile_cols(int tile) { return tile == MOE_T192 ? 256 : mfma_tile_bn(tile); }
 // device idle: `tiles` of them are expected (of at most `most`), with `ktiles` K
 // tiles; a piece keeps at least four.  Few tiles wait for one load after
 // another: 12 rows of 4 experts, 3520 -> 192, took 24.0 us whole, 11.5 us cut.
+// Adding the pieces takes about 3 us, what 8 K tiles of the 32 x 128 tile do (12 of
+// them, 4 experts of 6 rows: 8.1 us whole, 9.6 cut).
 // A captured call runs whole: the pieces' workspace may have to be allocated.
 int pieces_of(int load, int tile, int64_t tiles, int64_t ktiles, const Device &d, hipStream_t stream) {
-    if (tile == T256x256 || tile == MOE_T192 || (load != MOE_DTL && tile == T128x128) || ktiles < 8) return 1;
+    if (tile == T256x256 || tile == MOE_T192 || (load != MOE_DTL && tile == T128x128) || ktiles < (tile == T64x128 ? 16 : 8)) return 1;
     const int64_t s = std::min(d.cus / std::max<int64_t>(tiles, 1), ktiles / 4);
     if (s < 2) return 1;
     return capturing(stream) ? 1 : (int)s;
@@ -324,17 +326,34 @@ dg_status moe_gemm_entry(const dg_view *A, const dg_view *offsets, const dg_view
     const OpLayout lb = layout(w.one.ptr, N, w.one.cs, K, w.one.rs, w.es % 16 == 0 || w.E == 1);
     int load = MOE_ELEM;
     if (la.mode == KMAJ && la.vec && lb.vec) load = la.dtl && lb.dtl ? MOE_DTL : MOE_VEC;
-    // Tile rows by the mean count of the experts that can have rows.
-    const int64_t used = std::min(w.E, n), mean = n / std::max<int64_t>(used, 1);
+    // The tile: by the mean row count of the experts that can have rows; of the
+    // larger direct ones the quickest by what a K tile takes in each (us, measured
+    // on long K; two 128 x 128 workgroups share a CU) and the rounds that the
+    // expected tiles make: 64 experts of 234 rows, 4096 -> 512 FP16, take 127 us as
+    // 256 x 256 tiles, 120.5 as 192 x 256; 13 experts of 366 rows, 1088 -> 192, 25
+    // us as 256 x 256, 16.6 as pieces of 128 x 128.
+    const int64_t used = std::min(w.E, n), mean = n / std::max<int64_t>(used, 1), ktiles = cdiv(K, 64);
+    auto expected = [&](int t) {
+        const int64_t rows = tile_rows(load, t);
+        return std::max(used, used / 2 + cdiv(n, rows)) * cdiv(N, tile_cols(t));
+    };
     int tile = T64x64;
-    if (load == MOE_DTL) {
-        tile = mean <= 48 ? T64x128 : mean <= 192 ? T128x128 : T256x256;
-        // 192 rows where that leaves a whole round of the device less (64 experts of
-        // 234 rows, 4096 -> 512 FP16: 127 us with 256 rows on 181 CUs, 120.5).
-        auto rounds = [&](int64_t rows) { return cdiv((used / 2 + cdiv(n, rows)) * cdiv(N, 256), d.cus) * rows; };
-        if (tile == T256x256 && rounds(192) * 10 < rounds(256) * 9) tile = MOE_T192;
+    if (load == MOE_DTL && mean <= 48) {
+        tile = T64x128;
+    } else if (load == MOE_DTL) {
+        double best = 0.0;
+        for (int t : {(int)T256x256, MOE_T192, (int)T128x128}) {
+            const int64_t tiles = expected(t), S = pieces_of(load, t, tiles, ktiles, d, stream);
+            const double k_us = t == T256x256 ? 1.78 : t == MOE_T192 ? 1.65 : tiles * S <= d.cus ? 0.8 : 1.3;
+            const double us = k_us * cdiv(tiles * S, t == T128x128 ? 2 * d.cus : d.cus) * cdiv(ktiles, S) + (S > 1 ? 3.0 : 0.0);
+            if (best == 0.0 || us < best) {
+                best = us;
+                tile = t;
+            }
+        }
+    } else if (load == MOE_VEC) {
+        tile = mean <= 64 || expected(T128x128) < d.cus ? T64x64 : T128x128;
     }
-    else if (load == MOE_VEC) tile = mean <= 64 || (used + n / 128) * cdiv(N, 128) < d.cus ? T64x64 : T128x128;
     const int bm = tile_rows(load, tile), bn = tile_cols(tile);
 
     MoeArgs a = {};
@@ -343,8 +362,8 @@ dg_status moe_gemm_entry(const dg_view *A, const dg_view *offsets, const dg_view
     a.p.epi = plain_epilogue(c, act);
     a.p.N = (int)N; a.p.K = (int)K;
     a.p.tiles_n = (int)cdiv(N, bn);
-    a.p.ktiles = (int)cdiv(K, 64);
-    a.p.splits = pieces_of(load, tile, (used + n / bm) * a.p.tiles_n, a.p.ktiles, d, stream);
+    a.p.ktiles = (int)ktiles;
+    a.p.splits = pieces_of(load, tile, expected(tile), ktiles, d, stream);
     a.p.group_m = tile == T256x256 || tile == MOE_T192 ? 4 : 8;
     a.offsets = off.ptr; a.o_s = off.cs;
     a.E = (int)w.E; a.n = (int)n;
