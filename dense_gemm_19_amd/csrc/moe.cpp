@@ -3,6 +3,7 @@
 #include <hip/hip_runtime_api.h>
 
 #include <algorithm>
+#include <cmath>
 #include <initializer_list>
 
 #include "dg.h"
@@ -138,7 +139,9 @@ dg_status sort_entry(const dg_view *ids, int32_t E, const dg_view *offsets, cons
     a.blocks = (int)cdiv(n, SORT_BLOCK);
     a.table = nullptr;
     WsLease lease;
-    if (n >= SORT_TABLE_MIN && (int64_t)a.blocks * E <= SORT_TABLE_MAX && !capturing(stream)) {
+    const int64_t table_blocks = cdiv(n, sort_table_block(n));
+    if (n >= SORT_TABLE_MIN && table_blocks * E <= SORT_TABLE_MAX && !capturing(stream)) {
+        a.blocks = (int)table_blocks;
         if (lease_workspace(stream, (size_t)a.blocks * E * sizeof(int), 0, &lease) != hipSuccess) {
             (void)hipGetLastError();
             return DG_ERR_HIP;
@@ -168,6 +171,11 @@ dg_status gather_entry(const dg_view *X, const dg_view *order, int32_t k, const 
     a.order = o.ptr; a.o_s = o.cs;
     a.T = (int)x.rows; a.k = k; a.n = (int)y.rows; a.H = (int)y.cols; a.esize = y.esize;
     a.vec = x.cols_contig() && y.cols_contig();
+    // An output above 96 MB goes past the caches: 16384 rows of 4096 BF16 39.5 us
+    // instead of 45.8.  A product that then reads them and is bound by memory takes
+    // that back (with 4096 -> 1024: 163 us for both instead of 160), one as large as
+    // such row counts mostly meet does not (4096 -> 14336: 1.7 ms).
+    a.stream = y.rows * y.cols * y.esize > (int64_t)96 << 20;
     return done(launch_moe_gather(a, stream), stream);
 }
 
@@ -345,7 +353,12 @@ dg_status moe_gemm_entry(const dg_view *A, const dg_view *offsets, const dg_view
         for (int t : {(int)T256x256, MOE_T192, (int)T128x128}) {
             const int64_t tiles = expected(t), S = pieces_of(load, t, tiles, ktiles, d, stream);
             const double k_us = t == T256x256 ? 1.78 : t == MOE_T192 ? 1.65 : tiles * S <= d.cus ? 0.8 : 1.3;
-            const double us = k_us * cdiv(tiles * S, t == T128x128 ? 2 * d.cus : d.cus) * cdiv(ktiles, S) + (S > 1 ? 3.0 : 0.0);
+            // rounds: between their fraction and the next whole number, the expected
+            // count being one of many (8 experts of exactly 2048 rows make one round
+            // of 256 x 256 tiles where 1.06 are expected)
+            const double r = (double)(tiles * S) / (t == T128x128 ? 2 * d.cus : d.cus);
+            const double rounds = r <= 1.0 ? 1.0 : 0.5 * (r + std::ceil(r));
+            const double us = k_us * rounds * cdiv(ktiles, S) + (S > 1 ? 3.0 : 0.0);
             if (best == 0.0 || us < best) {
                 best = us;
                 tile = t;

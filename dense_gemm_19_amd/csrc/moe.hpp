@@ -14,7 +14,10 @@ namespace dg {
 constexpr int MOE_MAX_EXPERTS = 2048;    // LDS counters of a sort workgroup: 16 waves x E
 constexpr int MOE_MAX_ROWS = 1 << 28;     // of the experts' products: tile counts of 64 experts fit 32 bits
 constexpr int SORT_ONE_MAX = 16384;      // ids sorted by one workgroup; more take three launches
-constexpr int SORT_BLOCK = 4096;         // ids per workgroup of the two- and three-launch sorts (at least E fit half of it)
+constexpr int SORT_BLOCK = 4096;         // ids per workgroup of the three-launch sort (at least E fit half of it)
+// ids per workgroup of the two-launch sort: few ids want more workgroups (30208: 10.5
+// us, 11.9 with 4096), many a smaller table (262144 over 256 experts: 14.7, 15.1 with 2048)
+constexpr int sort_table_block(int64_t n) { return n <= 1 << 17 ? 2048 : 4096; }
 constexpr int SORT_TABLE_MIN = 8192;     // ids from which two launches are quicker than one workgroup
 constexpr int SORT_TABLE_MAX = 1 << 15;  // counts that every workgroup of the two-launch sort reads at most
 
@@ -34,6 +37,7 @@ struct GatherArgs {
     const char *order; int64_t o_s;        // [n] int32
     int T, k, n, H, esize;
     int vec;                               // both operands' rows are contiguous
+    int stream;                            // stores past the caches
 };
 
 // combine (Y = sum of w * Ys) and its gradient (dYs = w * dY, dw = <dY, Ys>)

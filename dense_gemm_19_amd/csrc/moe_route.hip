@@ -258,25 +258,27 @@ __global__ void __launch_bounds__(SORT_T) moe_sort_place(SortArgs a) {
 // columns of the table itself, whole (the experts' totals) and up to its own
 // part, instead of waiting for one workgroup that does it for all.  Bound by the
 // latencies of two launches (262144 ids over 256 experts: 14.7 us, three launches
-// 17.6 us; 30208 over 8: 11.9 and 16.3 us).
+// 17.6 us; 30208 over 8: 10.5 and 16.3 us).
+template <int BLOCK>
 __global__ void __launch_bounds__(SORT_T) moe_sort_table(SortArgs a) {
     extern __shared__ int lds[];
     const int i0 = block_start(a, blockIdx.x), i1 = block_start(a, blockIdx.x + 1);
-    int key[SORT_BLOCK / SORT_T];
+    int key[BLOCK / SORT_T];
 #pragma unroll
-    for (int s = 0; s < SORT_BLOCK / SORT_T; ++s) {
+    for (int s = 0; s < BLOCK / SORT_T; ++s) {
         const int i = i0 + s * SORT_T + threadIdx.x;
         key[s] = i < i1 ? sort_key(a, i) : -1;
     }
     for (int e = threadIdx.x; e < a.E; e += SORT_T) lds[e] = 0;
     __syncthreads();
 #pragma unroll
-    for (int s = 0; s < SORT_BLOCK / SORT_T; ++s)
+    for (int s = 0; s < BLOCK / SORT_T; ++s)
         if (key[s] >= 0) atomicAdd(lds + key[s], 1);
     __syncthreads();
     for (int e = threadIdx.x; e < a.E; e += SORT_T) a.table[(int64_t)blockIdx.x * a.E + e] = lds[e];
 }
 
+template <int BLOCK>
 __global__ void __launch_bounds__(SORT_T) moe_sort_place_table(SortArgs a) {
     extern __shared__ int lds[];              // cnt[SORT_W][E], all[parts][E], before[parts][E]
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, me = blockIdx.x;
@@ -285,7 +287,7 @@ __global__ void __launch_bounds__(SORT_T) moe_sort_place_table(SortArgs a) {
     const int cols = min(a.E, SORT_T), parts = SORT_T / cols;
     int *all = lds + SORT_W * a.E, *before = all + parts * a.E;
     __shared__ int kept;
-    Run<SORT_BLOCK / SORT_T> r;
+    Run<BLOCK / SORT_T> r;
     r.load(a, min(b0 + wave * run, b1), min(b0 + wave * run + run, b1), lane);
     // the table's columns, SCAN_U counts in flight per thread
     const int part = tid / cols, per = (a.blocks + parts - 1) / parts;
@@ -370,10 +372,13 @@ template <int EB> struct Chunk {
                 if (e < left) get(e, p + e * cs);
         }
     }
+    // STREAM: past the caches
+    template <bool STREAM = false>
     __device__ void store(char *p, int64_t cs, int c, int left, int vec) const {
         p += (int64_t)c * N * cs;
         if (vec && left >= N) {
-            *reinterpret_cast<u32x4_any *>(p) = v;
+            if (STREAM) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any *>(p));
+            else *reinterpret_cast<u32x4_any *>(p) = v;
         } else {
 #pragma unroll
             for (int e = 0; e < N; ++e)
@@ -408,9 +413,9 @@ constexpr int GATHER_U = 4;   // chunks of a row that a lane holds at once
 // ------------------------------------------------------------------ gather
 
 // Xs[r] = X[order[r] / k].  A copy, bound by the bytes (16384 rows of 4096 BF16:
-// 45.6 us, 4.4 TB/s; a plain copy of 1 GiB reaches 5.15 TB/s): `lanes` lanes walk one
+// 39.5 us, 5.1 TB/s, what a plain copy of 1 GiB reaches; a.stream): `lanes` lanes walk one
 // piece (GATHER_U * lanes chunks) of a row, all of its loads before its stores.
-template <int EB>
+template <int EB, bool STREAM>
 __global__ void __launch_bounds__(NT) moe_gather_rows(GatherArgs a, int lanes, int pieces) {
     constexpr int CN = Chunk<EB>::N;
     const int64_t u = ((int64_t)blockIdx.x * NT + threadIdx.x) / lanes;
@@ -432,7 +437,7 @@ __global__ void __launch_bounds__(NT) moe_gather_rows(GatherArgs a, int lanes, i
 #pragma unroll
     for (int q = 0; q < GATHER_U; ++q) {
         const int c = c0 + q * lanes;
-        if (c * CN < a.H) v[q].store(dst, a.y_cs, c, a.H - c * CN, a.vec);
+        if (c * CN < a.H) v[q].template store<STREAM>(dst, a.y_cs, c, a.H - c * CN, a.vec);
     }
 }
 
@@ -642,9 +647,12 @@ hipError_t launch_moe_sort(const SortArgs &a, hipStream_t s) {
     if (a.table) {
         const int cols = a.E < SORT_T ? a.E : SORT_T, parts = SORT_T / cols;
         const size_t lds = (size_t)(SORT_W + 2 * parts) * a.E * sizeof(int);
-        if ((e = allow_lds(moe_sort_place_table, lds)) != hipSuccess) return e;
-        hipLaunchKernelGGL(moe_sort_table, dim3(a.blocks), dim3(SORT_T), a.E * sizeof(int), s, a);
-        hipLaunchKernelGGL(moe_sort_place_table, dim3(a.blocks), dim3(SORT_T), lds, s, a);
+        const bool small = sort_table_block(a.n) == 2048;
+        const auto count = small ? moe_sort_table<2048> : moe_sort_table<4096>;
+        const auto place = small ? moe_sort_place_table<2048> : moe_sort_place_table<4096>;
+        if ((e = allow_lds(place, lds)) != hipSuccess) return e;
+        hipLaunchKernelGGL(count, dim3(a.blocks), dim3(SORT_T), a.E * sizeof(int), s, a);
+        hipLaunchKernelGGL(place, dim3(a.blocks), dim3(SORT_T), lds, s, a);
         return hipGetLastError();
     }
     if (a.n <= SORT_ONE_MAX) {
@@ -669,9 +677,9 @@ hipError_t launch_moe_gather(const GatherArgs &a, hipStream_t s) {
     const int64_t g = blocks((int64_t)a.n * pieces * lanes);
     if (g > INT32_MAX) return hipErrorInvalidValue;
     switch (a.esize) {
-    case 1: hipLaunchKernelGGL(moe_gather_rows<1>, dim3(g), dim3(NT), 0, s, a, lanes, pieces); break;
-    case 2: hipLaunchKernelGGL(moe_gather_rows<2>, dim3(g), dim3(NT), 0, s, a, lanes, pieces); break;
-    default: hipLaunchKernelGGL(moe_gather_rows<4>, dim3(g), dim3(NT), 0, s, a, lanes, pieces); break;
+    case 1: hipLaunchKernelGGL((a.stream ? moe_gather_rows<1, true> : moe_gather_rows<1, false>), dim3(g), dim3(NT), 0, s, a, lanes, pieces); break;
+    case 2: hipLaunchKernelGGL((a.stream ? moe_gather_rows<2, true> : moe_gather_rows<2, false>), dim3(g), dim3(NT), 0, s, a, lanes, pieces); break;
+    default: hipLaunchKernelGGL((a.stream ? moe_gather_rows<4, true> : moe_gather_rows<4, false>), dim3(g), dim3(NT), 0, s, a, lanes, pieces); break;
     }
     return hipGetLastError();
 }

@@ -140,3 +140,15 @@ def test_overlapping_offsets_stay_inside(dg):
     C = nan(n, N)
     dg.moe_gemm(A, torch.tensor([0] * 9 + [n], dtype=torch.int32, device=DEV), W, C)
     om.check(C, om.experts(A.cpu(), torch.tensor([0] * 9 + [n]), W.cpu(), 0, F32), "after")
+
+
+def test_gather_of_a_large_batch(dg):
+    # an output large enough to be stored past the caches, with rows whose last chunk is partial
+    g = torch.Generator().manual_seed(2)
+    T, k, H = 12000, 2, 2101
+    order = torch.randperm(T * k, generator=g).int()
+    order[::97] = -1
+    X = normal(g, T, H)
+    Xs = dg.moe_gather(X.to(DEV), order.to(DEV), k, torch.full((T * k, H), float("nan"), dtype=BF16, device=DEV))
+    want = torch.where((order >= 0)[:, None], X[order.clamp(min=0).long() // k], torch.zeros(1, dtype=BF16))
+    assert torch.equal(Xs.cpu(), want)
