@@ -485,12 +485,12 @@ dg_status w4_entry(const dg_view *A, const dg_view *offsets, const dg_view *Q, c
         return reinterpret_cast<uintptr_t>(m.ptr) % 16 == 0 && es % 16 == 0 && (m.rows <= 1 || m.rs % 16 == 0) &&
                m.cols * m.esize % 16 == 0;
     };
-    auto words = [](const Mat &m, int64_t es) {    // rows of whole, aligned words
-        return m.cs == m.esize && reinterpret_cast<uintptr_t>(m.ptr) % 4 == 0 && es % 4 == 0 && (m.rows <= 1 || m.rs % 4 == 0) &&
-               m.cols * m.esize % 4 == 0;
+    // the words that hold any of them lie between the first and the last one
+    auto words = [](const Stack &t) {
+        return t.one.cs == t.one.esize && t.span.lo % 4 == 0 && t.span.hi % 4 == 0;
     };
     const bool usual = K > 0 && K % 32 == 0 && pieces(x, 0) && pieces(q.one, q.E > 1 ? q.es : 0) &&
-                       words(s.one, q.E > 1 ? s.es : 0) && (!Z || words(z.one, q.E > 1 ? z.es : 0));
+                       words(s) && (!Z || words(z));
 
     // Rows of a tile: as few tiles as the largest allows, evenly filled (one
     // matrix), or by the mean count of the experts that can have rows.
@@ -528,8 +528,9 @@ dg_status w4_entry(const dg_view *A, const dg_view *offsets, const dg_view *Q, c
         const int64_t need = std::min<int64_t>(groups, (int64_t)a.chunks * chunk / group + 5);   // from a multiple of 4 on
         auto pitch = [](int64_t bytes) { return (int)std::max<int64_t>((cdiv(bytes, 4) | 1) * 4, 12); };   // (the reciprocal of one word is 2^32)
         auto region = [&](int p) { return (w4_cols(tm) * p + 255) & ~255; };
-        a.s_pitch = pitch(need * s.one.esize);
-        a.z_pitch = Z ? pitch(need) : 0;
+        a.seg_groups = (int)need;
+        a.s_pitch = pitch(need * s.one.esize + 3);
+        a.z_pitch = Z ? pitch(need + 3) : 0;
         const int sz = region(a.s_pitch) + (Z ? region(a.z_pitch) : 0);
         const int64_t mean = experts ? std::min<int64_t>(M / std::min(q.E, M) + 1, rows) : rows;
         const int a_mean = (int)((mean * chunk * 2 + 1023) & ~1023);

@@ -107,7 +107,7 @@ struct W4Args {
     int chunks, splits;                    // K in pieces of `chunks` chunks; splits > 1: one matrix only
     float *ws; int *counters;              // splits > 1: [tiles][splits][16 tm x w4_cols(tm)] sums, a counter per tile (0)
     int units;                             // workgroups of the grid
-    int whole;                             // A and Q in aligned 16-byte pieces, scales and zero points in words: w4_whole
+    int whole;                             // A and Q in aligned 16-byte pieces, scales and zero points in words that hold nothing else: w4_whole
     uint32_t s_mul, z_mul;                 // whole: ceil(2^32 / (pitch / 4)), to divide by it
     int depth;                             // whole: code units per wave in LDS (2 to 4)
     int a_lds;                             // LDS bytes for A: at least one chunk of 16 tm (or all M) rows

@@ -292,7 +292,8 @@ __device__ __forceinline__ void finish(const Part &p, const f32x4 (&acc)[TM], ch
 }
 
 // The usual layout (W4Args::whole): rows of A and of the codes in whole, aligned
-// 16-byte pieces, scales and zero points in aligned words that LDS holds at once.
+// 16-byte pieces, scales and zero points one run of whole aligned words that LDS holds
+// at once.
 // A workgroup computes 16 * TM rows x 16 * WN columns over its chunks of K.  Its
 // 8 waves are WK x WN: wave (wk, wn) takes 16 columns and unit wk of every chunk.
 //  - Everything goes to LDS by load-to-LDS instructions, which cost no registers
@@ -338,24 +339,30 @@ __global__ void __launch_bounds__(NT, TM == 1 ? 4 : 2) w4_whole(W4Args a) {
     const int q_ring = wave * (a.depth * UNIT_LDS), a_ring = WAVES * a.depth * UNIT_LDS;
     const int s_at = a_ring + a.a_lds, z_at = s_at + ((w4_cols(TM) * a.s_pitch + 255) & ~255);
 
-    // Scales (and zero points) of this piece's groups from g0 on: word d of column
-    // r at r * pitch + 4 d, the pitch an odd number of words.
+    // Scales (and zero points) of this piece's groups from g0 on: the aligned words
+    // that hold column r's, word d at r * pitch + 4 d, the pitch an odd number of
+    // words.  The first byte is the (r * rs + from)'th of them, modulo 4.
     // group of 32-element step `step` of K: see w4_stream
     auto group_of = [&](int step) { return min((int)(a.g_mul ? __umulhi((uint32_t)step, a.g_mul) : (uint32_t)step), a.groups - 1); };
     const int g0 = __builtin_amdgcn_readfirstlane(group_of(c0 * (CHUNK / 32)) & ~3);
     auto words = [&](const char *base, int64_t rs, int pitch, uint32_t mul, int at, int bytes) __attribute__((always_inline)) {
         const int per = pitch / 4, total = w4_cols(TM) * per;
+        const uint32_t from = (uint32_t)(uintptr_t)base & 3u;
+        base -= from;
 #pragma unroll 1
         for (int j = wave; j * 64 < total; j += WAVES) {
             const int i = j * 64 + lane, r = (int)__umulhi((uint32_t)i, mul), d = i - r * per;
-            dtl::lds_load4(base, (uint32_t)min(r, p.cols - 1) * (uint32_t)rs + (uint32_t)min(4 * d, bytes - 4),
+            const uint32_t row = (uint32_t)min(r, p.cols - 1) * (uint32_t)rs + from;
+            dtl::lds_load4(base, (row & ~3u) + min(4u * (uint32_t)d, ((row & 3u) + (uint32_t)bytes - 1u) & ~3u),
                            __builtin_amdgcn_readfirstlane(lds0 + at + j * 256));
         }
     };
+    const char *s_base = a.S + uniform((int64_t)p.e * a.s_es + (int64_t)p.n0 * a.s_rs + (int64_t)g0 * SB);
+    const char *z_base = ZP ? a.Z + uniform((int64_t)p.e * a.z_es + (int64_t)p.n0 * a.z_rs + g0) : nullptr;
     if (c0 < c1) {
-        const int n = a.groups - g0;
-        words(a.S + uniform((int64_t)p.e * a.s_es + (int64_t)p.n0 * a.s_rs + (int64_t)g0 * SB), a.s_rs, a.s_pitch, a.s_mul, s_at, n * SB);
-        if (ZP) words(a.Z + uniform((int64_t)p.e * a.z_es + (int64_t)p.n0 * a.z_rs + g0), a.z_rs, a.z_pitch, a.z_mul, z_at, n);
+        const int n = min(a.groups - g0, a.seg_groups);
+        words(s_base, a.s_rs, a.s_pitch, a.s_mul, s_at, n * SB);
+        if (ZP) words(z_base, a.z_rs, a.z_pitch, a.z_mul, z_at, n);
     }
 
     // Chunk c into slot `slot` of both rings.  Codes: piece i of row r of a unit at
@@ -409,7 +416,9 @@ __global__ void __launch_bounds__(NT, TM == 1 ? 4 : 2) w4_whole(W4Args a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) fa_at[i][t] = a_ring + wk * 512 + row * ROW + 16 * ((4 * i + g) ^ (row & 15));
     }
-    const char *ls = lds + s_at + (16 * wn + l) * a.s_pitch, *lz = lds + z_at + (16 * wn + l) * a.z_pitch;
+    const uint32_t col = (uint32_t)min(16 * wn + l, p.cols - 1);
+    const char *ls = lds + s_at + (16 * wn + l) * a.s_pitch + ((col * (uint32_t)a.s_rs + (uint32_t)(uintptr_t)s_base) & 3u);
+    const char *lz = lds + z_at + (16 * wn + l) * a.z_pitch + ((col * (uint32_t)a.z_rs + (uint32_t)(uintptr_t)z_base) & 3u);
     auto compute = [&](int c, int slot) __attribute__((always_inline)) {
         const int k0 = c * CHUNK + wk * UNIT, qs = q_lane + slot * UNIT_LDS, as = slot * a_bytes;
         uint32_t qw[8];                            // lane row g: bytes 4 g .. + 3 of the 16 of a 32-element step

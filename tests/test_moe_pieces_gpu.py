@@ -152,3 +152,26 @@ def test_gather_of_a_large_batch(dg):
     Xs = dg.moe_gather(X.to(DEV), order.to(DEV), k, torch.full((T * k, H), float("nan"), dtype=BF16, device=DEV))
     want = torch.where((order >= 0)[:, None], X[order.clamp(min=0).long() // k], torch.zeros(1, dtype=BF16))
     assert torch.equal(Xs.cpu(), want)
+
+
+@pytest.mark.parametrize("M", [1, 16, 30, 90])
+@pytest.mark.parametrize("N,K,G", [(68, 2080, 32), (36, 4640, 32), (44, 5920, 128), (20, 1312, 96)])
+@pytest.mark.parametrize("st", [F32, F16, BF16])
+def test_w4_rows_of_scales_off_words(dg, M, N, K, G, st):
+    # odd counts of groups: rows of scales and zero points begin anywhere in a word, the whole run does not
+    g = torch.Generator().manual_seed(M + N + K)
+    A = normal(g, M, K)
+    Q, S, Z = weights(g, N, K, G, True, st)
+    for z in (Z, None):
+        C = nan(M, N)
+        dg.gemm_w4(A.to(DEV), Q.to(DEV), S.to(DEV), C, group=G, Z=None if z is None else z.to(DEV))
+        om.check(C, om.w4(A, Q, S, z, G, 0, F32), f"{M}x{N}x{K}")
+    E, n = 3, 3 * M + 1
+    off = offsets([M, 0, 2 * M])
+    A = normal(g, n, K)
+    Q, S, Z = weights(g, N, K, G, True, st, (E,))
+    C = nan(n, N)
+    dg.moe_gemm_w4(A.to(DEV), off.to(DEV), Q.to(DEV), S.to(DEV), C, group=G, Z=Z.to(DEV))
+    v, b = om.w4_experts(A, off, Q, S, Z, G, 0, F32)
+    v[n - 1:], b[n - 1:] = 0, 0
+    om.check(C, (v, b), "experts")
