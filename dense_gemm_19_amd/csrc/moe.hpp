@@ -124,7 +124,7 @@ constexpr int w4_cols(int tm) { return tm == 1 ? 32 : 64; }
 constexpr int w4_chunk(int tm) { return tm == 1 ? 1024 : 512; }
 
 // tm: rows of a workgroup / 16, 1 to W4_MAX_TM (4, whose chunk of A leaves LDS
-// no room for a second, took 26 us for 248 x 1452 x 2592 where 3 takes 21.4)
+// no room for a second, took 26 us for 248 x 1452 x 2592 where 3 takes 14.2 to 21)
 hipError_t launch_w4(int in_kind, int tm, const W4Args &a, int64_t units, hipStream_t stream);
 
 }  // namespace dg
