@@ -281,8 +281,7 @@ int tile_rows(int load, int tile) { return tile == MOE_T192 ? 192 : load == MOE_
 int tile_cols(int tile) { return tile == MOE_T192 ? 256 : mfma_tile_bn(tile); }
 
 // The pieces of K that each tile is cut into where the tiles leave most of the
-// device idle: `tiles` of them are expected (of at most `most`), with `ktiles` K
-// tiles; a piece keeps at least four.  Few tiles wait for one load after
+// device idle: `tiles` of them are expected, with `ktiles` K tiles; a piece keeps at least four.  Few tiles wait for one load after
 // another: 12 rows of 4 experts, 3520 -> 192, took 24.0 us whole, 11.5 us cut.
 // Adding the pieces takes about 3 us, what 8 K tiles of the 32 x 128 tile do (12 of
 // them, 4 experts of 6 rows: 8.1 us whole, 9.6 cut).
