@@ -159,7 +159,7 @@ dg_status gather_entry(const dg_view *X, const dg_view *order, int32_t k, const 
     if (!(is_float(x.dtype) || x.dtype == DG_F8E4M3) || y.dtype != x.dtype) return DG_ERR_DTYPE;
     if (y.cols != x.cols) return DG_ERR_SHAPE_MISMATCH;
     DG_TRY(index_vector(order, y.rows, &o));
-    if (x.rows > INT32_MAX || x.cols > INT32_MAX || y.rows > INT32_MAX) return DG_ERR_OVERFLOW;
+    if (x.rows > INT32_MAX || x.cols > MOE_MAX_EXTENT || y.rows > INT32_MAX) return DG_ERR_OVERFLOW;
     if (self_overlaps(y)) return DG_ERR_STRIDE;
     if (spans_overlap(y, x) || spans_overlap(y, o)) return DG_ERR_ALIAS;
     if (y.empty()) return DG_SUCCESS;
@@ -199,7 +199,7 @@ dg_status combine_entry(const dg_view *Ys, const dg_view *pos, const dg_view *w,
     if (w && (wt.rows != p.rows || wt.cols != p.cols)) return DG_ERR_SHAPE_MISMATCH;
     if (grad && (ds.rows != s.rows || ds.cols != s.cols)) return DG_ERR_SHAPE_MISMATCH;
     if (dw && (dv.rows != p.rows || dv.cols != p.cols)) return DG_ERR_SHAPE_MISMATCH;
-    if (s.rows > INT32_MAX || y.rows > INT32_MAX || y.cols > INT32_MAX || p.cols > INT32_MAX) return DG_ERR_OVERFLOW;
+    if (s.rows > INT32_MAX || y.rows > INT32_MAX || y.cols > MOE_MAX_EXTENT || p.cols > MOE_MAX_EXTENT) return DG_ERR_OVERFLOW;
     // what is written overlaps neither itself nor any other view
     if (!grad) {
         if (self_overlaps(y)) return DG_ERR_STRIDE;
@@ -321,7 +321,7 @@ dg_status moe_gemm_entry(const dg_view *A, const dg_view *offsets, const dg_view
     if (w.E < 1 || w.one.rows != x.cols || c.rows != x.rows || c.cols != w.one.cols) return DG_ERR_SHAPE_MISMATCH;
     DG_TRY(index_vector(offsets, w.E + 1, &off));
     const int64_t n = x.rows, K = x.cols, N = c.cols;
-    if (n > MOE_MAX_ROWS || K > INT32_MAX || N > INT32_MAX || w.E > INT32_MAX / 2) return DG_ERR_OVERFLOW;
+    if (n > MOE_MAX_ROWS || K > MOE_MAX_EXTENT || N > MOE_MAX_EXTENT || w.E > INT32_MAX / 2) return DG_ERR_OVERFLOW;
     if (act != DG_ACT_NONE && act != DG_ACT_RELU && act != DG_ACT_GELU_TANH) return DG_ERR_INVALID_ARG;
     if (self_overlaps(c)) return DG_ERR_STRIDE;
     if (spans_overlap(c, x) || spans_overlap(c, w.span) || spans_overlap(c, off)) return DG_ERR_ALIAS;
@@ -396,7 +396,7 @@ dg_status moe_wgrad_entry(const dg_view *A, const dg_view *D, const dg_view *off
     if (w.E < 1 || g.rows != x.rows || w.one.rows != x.cols || w.one.cols != g.cols) return DG_ERR_SHAPE_MISMATCH;
     DG_TRY(index_vector(offsets, w.E + 1, &off));
     const int64_t n = x.rows, K = x.cols, N = g.cols;
-    if (n > INT32_MAX || K > INT32_MAX || N > INT32_MAX || w.E > INT32_MAX / 2) return DG_ERR_OVERFLOW;
+    if (n > MOE_MAX_EXTENT || K > MOE_MAX_EXTENT || N > MOE_MAX_EXTENT || w.E > INT32_MAX / 2) return DG_ERR_OVERFLOW;
     if (stack_overlaps(w)) return DG_ERR_STRIDE;
     if (spans_overlap(w.span, x) || spans_overlap(w.span, g) || spans_overlap(w.span, off)) return DG_ERR_ALIAS;
     if (w.one.empty()) return DG_SUCCESS;
@@ -456,7 +456,7 @@ dg_status w4_entry(const dg_view *A, const dg_view *offsets, const dg_view *Q, c
     if (q.E < 1 || s.E != q.E || s.one.rows != N || s.one.cols != groups) return DG_ERR_SHAPE_MISMATCH;
     if (Z && (z.E != q.E || z.one.rows != N || z.one.cols != groups)) return DG_ERR_SHAPE_MISMATCH;
     if (experts) DG_TRY(index_vector(offsets, q.E + 1, &off));
-    if (M > (experts ? MOE_MAX_ROWS : INT32_MAX) || K > (1 << 20) || N > INT32_MAX || q.E > INT32_MAX / 2) return DG_ERR_OVERFLOW;
+    if (M > (experts ? MOE_MAX_ROWS : MOE_MAX_EXTENT) || K > (1 << 20) || N > MOE_MAX_EXTENT || q.E > INT32_MAX / 2) return DG_ERR_OVERFLOW;
     if (!x.cols_contig() || !q.one.cols_contig()) return DG_ERR_UNSUPPORTED_VIEW;
     // lane offsets within a workgroup's rows and columns are 32-bit
     const int64_t lim = ((int64_t)1 << 31) / 64;

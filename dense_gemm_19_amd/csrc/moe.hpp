@@ -9,6 +9,10 @@
 
 namespace dg {
 
+// The kernels walk an extent in 32 bits and may step past its end by less than a
+// tile or a wave's chunks: 256 columns, 64 chunks of 16 elements.
+constexpr int64_t MOE_MAX_EXTENT = INT32_MAX - 4095;
+
 // ---------------------------------------------------------------- routing (moe_route.hip)
 
 constexpr int MOE_MAX_EXPERTS = 2048;    // LDS counters of a sort workgroup: 16 waves x E

@@ -402,7 +402,9 @@ dg_status dg_quant_fp8(const dg_view *X, const dg_view *Q, const dg_view *S, dg_
  * the stream's split-K workspace; a captured call does not (so its last bits may
  * differ).  dg_moe_sort of many ids keeps its counts there (a captured call does
  * without); the other entry points need no scratch memory.  Views of index vectors
- * are [len] or [1][len].
+ * are [len] or [1][len].  Counts of rows are at most 2^31 - 1, the extents H, K and N
+ * and the choices k at most 2^31 - 4096 (dg_moe_sort's k: whatever n allows), where no
+ * tighter limit is given: DG_ERR_OVERFLOW above.
  */
 
 /* Sort the router's choices by expert, stably (equal experts keep the order of
@@ -461,7 +463,7 @@ dg_status dg_moe_gemm(const dg_view *A, const dg_view *offsets, const dg_view *W
 
 /* dW[e] <- sum over expert e's rows of A[r]^T * D[r] (zero for an expert without rows).
  *   A [n][K] and D [n][N]: both DG_F16 or both DG_BF16; dW [E][K][N] DG_F32, DG_F16
- *   or DG_BF16.  Otherwise as dg_moe_gemm. */
+ *   or DG_BF16.  Otherwise as dg_moe_gemm, but for the rows: up to 2^31 - 4096. */
 dg_status dg_moe_gemm_wgrad(const dg_view *A, const dg_view *D, const dg_view *offsets, const dg_view *dW,
                             hipStream_t stream);
 

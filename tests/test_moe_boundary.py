@@ -183,3 +183,32 @@ def test_nothing_to_do():
     dg.moe_gather(z(T, H), z(0, dt=I32), 2, z(0, H), stream=0)
     dg.moe_combine(z(0, H), z(0, K, dt=I32), z(0, H), stream=0)
     dg.moe_gemm_wgrad(z(R, 0), z(R, N), z(E + 1, dt=I32), z(E, 0, N), stream=0)
+
+
+# An extent that a kernel's 32-bit walk could step past 2^31 is refused; the next smaller one is not (an
+# output of one repeated element is then refused for that).
+LIMIT = 2 ** 31 - 4096
+
+
+def one(*shape, dt=BF16):
+    return z(1, dt=dt).expand(*shape)
+
+
+@pytest.mark.parametrize("size,status", [(LIMIT, "STRIDE"), (LIMIT + 1, "OVERFLOW"), (2 ** 31 - 1, "OVERFLOW")])
+def test_extents_next_to_32_bits(size, status):
+    i32 = lambda *s: z(*s, dt=I32)   # noqa: E731
+    for dt in (F32, BF16):
+        refused(status, dg.moe_gather, one(2, size, dt=dt), i32(2), 1, one(2, size, dt=dt))
+        refused(status, dg.moe_combine, one(2, size, dt=dt), i32(2, 1), one(2, size, dt=dt))
+        refused(status, dg.moe_combine_grad, one(2, size, dt=dt), one(2, size, dt=dt), i32(2, 1), z(2, 1, dt=F32),
+                one(2, size, dt=dt), z(2, 1, dt=F32))
+    many = one(2, size, dt=I32)
+    refused(status, dg.moe_combine, z(2, H), many, one(2, H))
+    refused(status, dg.moe_combine_grad, z(2, H), z(2, H), many, one(2, size, dt=F32), z(2, H), one(2, size, dt=F32))
+    refused(status, dg.moe_gemm, one(2, size), i32(2), one(1, size, 8), one(2, 8))
+    refused(status, dg.moe_gemm, one(2, 8), i32(2), one(1, 8, size), one(2, size))
+    refused(status, dg.moe_gemm_wgrad, one(size, 8), one(size, 8), i32(2), one(1, 8, 8))
+    refused(status, dg.moe_gemm_wgrad, one(2, size), one(2, 8), i32(2), one(1, size, 8))
+    refused(status, dg.moe_gemm_wgrad, one(2, 8), one(2, size), i32(2), one(1, 8, size))
+    refused(status, dg.gemm_w4, z(2, 32), z(1, 16, dt=U8).expand(size, 16), one(size, 1), one(2, size), 32)
+    refused(status, dg.gemm_w4, z(1, 32).expand(size, 32), z(8, 16, dt=U8), z(8, 1), one(size, 8), 32)
