@@ -34,20 +34,21 @@ __device__ __forceinline__ uint64_t same_key(int key, int bits) {
     return m;
 }
 
-// A wave's run of ids [i0, i1): at most STEPS steps of 64, whose keys stay in
-// registers from the count to the placing (every load is issued before any use).
+// A wave's run of ids: at most STEPS steps of 64, whose keys stay in registers
+// from the count to the placing (every load is issued before any use).  Its end is
+// kept as a length: the last id may be number 2^31 - 2, and numbers past it wrap.
 template <int STEPS>
 struct Run {
     int key[STEPS];
-    int i0, i1;
+    int i0, len;
 
-    __device__ void load(const SortArgs &a, int b, int e, int lane) {
-        i0 = b; i1 = e;
+    // ids [at, at + each) of a workgroup's ids [b, e), as far as there are any
+    __device__ void load(const SortArgs &a, int b, int e, int at, int each, int lane) {
+        at = min(at, e - b);
+        i0 = b + at;
+        len = min(each, e - i0);
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-            const int i = i0 + 64 * s + lane;
-            key[s] = i < i1 ? sort_key(a, i) : -1;
-        }
+        for (int s = 0; s < STEPS; ++s) key[s] = 64 * s + lane < len ? sort_key(a, i0 + 64 * s + lane) : -1;
     }
     // cnt[key] += 1 per id (integer counts: the order does not matter)
     __device__ void count(int *cnt) const {
@@ -61,8 +62,7 @@ struct Run {
     __device__ void place(const SortArgs &a, int *next, int lane) const {
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
-            if (i0 + 64 * s >= i1) break;
-            const int i = i0 + 64 * s + lane;
+            if (64 * s >= len) break;
             const uint64_t m = same_key(key[s], a.bits);
             const int rank = __popcll(m & ((1ull << lane) - 1));
             int at = -1;
@@ -71,7 +71,8 @@ struct Run {
             if (key[s] >= 0 && (m >> lane) == 1)
                 __hip_atomic_store(next + key[s], at + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
             __builtin_amdgcn_wave_barrier();
-            if (i < i1) {
+            if (64 * s + lane < len) {
+                const int i = i0 + 64 * s + lane;
                 a.pos[i] = at;
                 if (at >= 0) a.order[at] = i;
             }
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(SORT_T) moe_sort_one(SortArgs a) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int run = ((a.n + SORT_T - 1) / SORT_T) * 64;   // ids per wave, whole steps
     Run<STEPS> r;
-    r.load(a, min(wave * run, a.n), min(wave * run + run, a.n), lane);
+    r.load(a, 0, a.n, wave * run, run, lane);
     for (int i = tid; i < SORT_W * a.E; i += SORT_T) lds[i] = 0;
     __syncthreads();
     r.count(lds + wave * a.E);
@@ -233,7 +234,7 @@ __global__ void __launch_bounds__(SORT_T) moe_sort_place(SortArgs a) {
     const int b0 = block_start(a, blockIdx.x), b1 = block_start(a, blockIdx.x + 1);
     const int run = (b1 - b0 + SORT_T - 1) / SORT_T * 64;
     Run<SORT_BLOCK / SORT_T> r;
-    r.load(a, min(b0 + wave * run, b1), min(b0 + wave * run + run, b1), lane);
+    r.load(a, b0, b1, wave * run, run, lane);
     const int kept = a.offsets[a.E];
     for (int i = tid; i < SORT_W * a.E; i += SORT_T) lds[i] = 0;
     __syncthreads();
@@ -288,7 +289,7 @@ __global__ void __launch_bounds__(SORT_T) moe_sort_place_table(SortArgs a) {
     int *all = lds + SORT_W * a.E, *before = all + parts * a.E;
     __shared__ int kept;
     Run<BLOCK / SORT_T> r;
-    r.load(a, min(b0 + wave * run, b1), min(b0 + wave * run + run, b1), lane);
+    r.load(a, b0, b1, wave * run, run, lane);
     // the table's columns, SCAN_U counts in flight per thread
     const int part = tid / cols, per = (a.blocks + parts - 1) / parts;
     const int t0 = min(part * per, a.blocks), t1 = part < parts ? min(t0 + per, a.blocks) : t0;
