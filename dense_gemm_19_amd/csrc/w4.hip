@@ -444,6 +444,13 @@ __global__ void __launch_bounds__(NT, TM == 1 ? 4 : 2) w4_whole(W4Args a) {
                 }
                 zp[v] = ZP ? (float)*reinterpret_cast<const uint8_t *>(lz + gi) : 8.0f;
             }
+            // groups past K (these elements hold its end): their sums are zero, but
+            // zero times an infinite last scale would be NaN
+            if (GV > 1 && k0 + 128 * (w + 1) > nk) {
+#pragma unroll
+                for (int v = 1; v < GV; ++v)
+                    if (k0 + 128 * w + v * (128 / GV) >= nk) s[v] = 0.0f;
+            }
             f32x4 blk[TM];                         // a group's sums
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -631,6 +638,13 @@ __global__ void __launch_bounds__(NT, TM == 1 ? 4 : 2) w4_stream(W4Args a) {
                     s[v] = a.s_kind == OUT_BF16 ? bf16_bits_to_f32(h) : f16_bits_to_f32(h);
                 }
                 zp[v] = ZP ? (float)*reinterpret_cast<const uint8_t *>(lz + gi) : 8.0f;
+            }
+            // groups past K (these elements hold its end): their sums are zero, but
+            // zero times an infinite last scale would be NaN
+            if (GV > 1 && k0 + 128 * (w + 1) > nk) {
+#pragma unroll
+                for (int v = 1; v < GV; ++v)
+                    if (k0 + 128 * w + v * (128 / GV) >= nk) s[v] = 0.0f;
             }
             f32x4 blk[TM];                         // a group's sums
 #pragma unroll

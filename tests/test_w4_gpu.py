@@ -177,3 +177,29 @@ def test_w4_in_a_graph(dg):
         dg.gemm_w4(A, Q, S, C, group=G)
         torch.cuda.synchronize()
         assert torch.equal(C, got), rep
+
+
+@pytest.mark.parametrize("K,G", [(160, 32), (320, 64), (288, 96), (333, 32), (2080, 32), (1096, 64)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_infinite_scale_of_the_last_group(dg, K, G, dtype, zeros):
+    # the last 128 elements of K hold less than their groups: what lies past K adds nothing, not Inf times 0
+    g = torch.Generator().manual_seed(K + G)
+    N = 40
+    Q, S, Z = weights(g, N, K, G, zeros, F32)
+    Q = (Q | 0x99)                                               # q - z is not 0, and above it
+    if zeros:
+        Z = Z % 9
+    S[::3, -1], S[1::3, -1] = float("inf"), float("-inf")
+    S[0, 0] = float("inf")
+    for M in (3, 20, 40):
+        A = (0.5 + torch.rand(M, K, generator=g)).to(dtype)
+        a1 = torch.zeros(M * K + 1, dtype=dtype, device=DEV)[1:].view(M, K).copy_(A)   # any other layout
+        want = om.w4(A, Q, S, Z, G, 0, F32)
+        for a in (A.to(DEV), a1):
+            C = dg.gemm_w4(a, *dev(Q, S), torch.empty(M, N, device=DEV), group=G, Z=dev(Z)[0])
+            om.check(C, want, f"{M}x{N}x{K} G {G}")
+    off = torch.tensor([0, 15, 40], dtype=torch.int32)
+    Q, S, Z = (None if t is None else torch.stack([t, t]) for t in (Q, S, Z))
+    C = dg.moe_gemm_w4(*dev(A, off, Q, S), torch.empty(40, N, device=DEV), group=G, Z=dev(Z)[0])
+    om.check(C, want, "experts")
