@@ -35,48 +35,34 @@ __device__ __forceinline__ u32x2 code_bytes(uint32_t x) {
     return u32x2{__builtin_amdgcn_perm(hi, lo, 0x05010400u), __builtin_amdgcn_perm(hi, lo, 0x07030602u)};
 }
 
-// 8 codes minus z as FP16 or BF16.  A byte q under 0x64 is the FP16 number 1024
-// + q, so one packed add gives two differences, exactly.  BF16 has no packed
-// arithmetic here: mixed FP16 -> FP32 multiply-adds, then the upper halves of two
-// (a difference has at most 8 significant bits).
+// 8 codes minus z as FP16 or BF16, exactly (a difference has at most 8 significant
+// bits).  A byte q under 0x64 is the FP16 number 1024 + q, so one packed add gives
+// two differences.  BF16 has no packed arithmetic here: a code under a zero byte is
+// the FP16 number q * 2^-24, a mixed FP16 -> FP32 multiply-add makes it q - z, and
+// the upper halves of two are the pair (19 instructions for 8 codes).
 template <int IN>
 __device__ __forceinline__ u32x4 decode(uint32_t x, float z) {
-    const u32x2 e = code_bytes(x);
     u32x4 out;
-    float unit = 1.0f;
-    asm("" : "+s"(unit));   // keeps the multiply, so that conversion and add are one instruction
+    if (IN == IN_F16) {
+        const u32x2 e = code_bytes(x);
+        const _Float16 c = (_Float16)(-1024.0f - z);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const f16x2 v = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, e[j / 2], j & 1 ? 0x04030402u : 0x04010400u));
-        if (IN == IN_F16) {
-            const _Float16 c = (_Float16)(-1024.0f - z);
-            out[j] = __builtin_bit_cast(uint32_t, v + f16x2{c, c});
-        } else {
-            const float p = fmaf((float)v[0], unit, -1024.0f - z), q = fmaf((float)v[1], unit, -1024.0f - z);
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t v = __builtin_amdgcn_perm(0x64646464u, e[j / 2], j & 1 ? 0x04030402u : 0x04010400u);
+            out[j] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, v) + f16x2{c, c});
+        }
+    } else {
+        const uint32_t lo = x & 0x0f0f0f0fu, hi = (x >> 4) & 0x0f0f0f0fu;
+        float unit = 0x1p24f;
+        asm("" : "+s"(unit));   // keeps the multiply, so that conversion and add are one instruction
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const f16x2 v = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(hi, lo, 0x0c040c00u + 0x00010001u * j));
+            const float p = fmaf((float)v[0], unit, -z), q = fmaf((float)v[1], unit, -z);
             out[j] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, q), __builtin_bit_cast(uint32_t, p), 0x07060302u);
         }
     }
     return out;
-}
-
-// 8 codes as BF16 numbers, z not yet subtracted.  As E4M3 a byte 0 .. 15 is that
-// many times 2^-9 (its subnormals and first normals lie evenly), so one
-// conversion with a scale of 2^9 gives two of them, exactly: 9 instructions where
-// decode takes 21.
-__device__ __forceinline__ u32x4 decode_codes(uint32_t x) {
-    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-    const u32x2 e = code_bytes(x);
-    const bf16x2 v[4] = {__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(e[0], 512.0f, false),
-                         __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(e[0], 512.0f, true),
-                         __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(e[1], 512.0f, false),
-                         __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(e[1], 512.0f, true)};
-    return u32x4{__builtin_bit_cast(uint32_t, v[0]), __builtin_bit_cast(uint32_t, v[1]),
-                 __builtin_bit_cast(uint32_t, v[2]), __builtin_bit_cast(uint32_t, v[3])};
-}
-// -z for every element of a fragment (z <= 255: exact in BF16)
-__device__ __forceinline__ u32x4 minus_zero_point(float z) {
-    const uint32_t b = __builtin_bit_cast(uint32_t, -z), p = __builtin_amdgcn_perm(b, b, 0x07060302u);
-    return u32x4{p, p, p, p};
 }
 
 // 16 bytes from p on: elements of BYTES bytes `stride` apart, of which only the
@@ -115,25 +101,6 @@ __device__ __forceinline__ u32x4 down_bytes(u32x4 v, int by) {
         hi >>= 8 * by;
     }
     return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
-}
-
-// C[m][n] before the activation, by the definition, one element after another
-// (for sums that came out infinite or NaN).
-__device__ __forceinline__ float whole_sum(const W4Args &a, int e, int m, int n, int nk) {
-    const char *q = a.Q + (int64_t)e * a.q_es + (int64_t)n * a.q_rs, *x = a.A + (int64_t)m * a.a_rs;
-    float sum = 0.0f;
-    for (int k0 = 0; k0 < nk; k0 += a.G) {
-        const int gi = k0 / a.G;
-        const float s = load_out(a.S + (int64_t)e * a.s_es + (int64_t)n * a.s_rs + (int64_t)gi * a.s_cs, a.s_kind);
-        const int z = a.Z ? *reinterpret_cast<const uint8_t *>(a.Z + (int64_t)e * a.z_es + (int64_t)n * a.z_rs + (int64_t)gi * a.z_cs) : 8;
-        float part = 0.0f;
-        for (int k = k0; k < min(k0 + a.G, nk); ++k) {
-            const int code = *reinterpret_cast<const uint8_t *>(q + k / 2) >> (4 * (k & 1)) & 15;
-            part = fmaf(bf16_bits_to_f32(*reinterpret_cast<const uint16_t *>(x + 2 * (int64_t)k)), (float)(code - z), part);
-        }
-        sum = fmaf(s, part, sum);
-    }
-    return sum;
 }
 
 // An offset that every lane shares, in scalar registers.
@@ -213,7 +180,7 @@ __device__ __forceinline__ bool find_part(const W4Args &a, Part &p) {
 
 // The waves' sums added, the pieces' too, activated and stored.
 // Register (t, r) of lane (l, g) of wave (wk, wn) is C[16 t + 4 g + r][16 wn + l].
-template <int IN, int TM>
+template <int TM>
 __device__ __forceinline__ void finish(const Part &p, const f32x4 (&acc)[TM], char *lds, int *is_last, int tid, int wk, int wn) {
     constexpr int WN = w4_cols(TM) / 16, WK = WAVES / WN, REGS = TM * WN * 256, PER = REGS / NT;
     const int lane = tid & 63;
@@ -262,8 +229,6 @@ __device__ __forceinline__ void finish(const Part &p, const f32x4 (&acc)[TM], ch
     if constexpr (PER == 1) {
         const int t = (tid >> 8) % TM, m = p.m0 + 16 * t + 4 * ((lane >> 4) & 3) + ((tid >> 6) & 3), n = p.n0 + 16 * ((tid >> 8) / TM) + (lane & 15);
         if (m >= p.rows || n >= o.N) return;
-        // an infinite activation times q and times -z may cancel to NaN
-        if (IN == IN_BF16 && TM == 1 && !(fabsf(v[0]) < __builtin_inff())) v[0] = whole_sum(o, p.e, p.begin + m, n, p.nk);
         store_out(o.C + (int64_t)(p.begin + m) * o.c_rs + (int64_t)n * o.c_cs, o.out_kind, activate(o.act, v[0]));
         return;
     }
@@ -317,9 +282,6 @@ __global__ void __launch_bounds__(NT, TM == 1 ? 4 : 2) w4_whole(W4Args a) {
     __shared__ int is_last;
     constexpr int WN = w4_cols(TM) / 16, WK = WAVES / WN, CHUNK = w4_chunk(TM), ROW = CHUNK * 2, PR = ROW / 16;
     static_assert(WK * UNIT == CHUNK, "a unit per wave");
-    // Few BF16 rows are bound by the decoding: the codes go to the matrix cores as
-    // they are and the zero points as a second product of the same rows.
-    constexpr bool RAW = IN == IN_BF16 && TM == 1;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wk = wave % WK, wn = wave / WK;
     const int l = lane & 15, g = lane >> 4;
@@ -456,12 +418,9 @@ __global__ void __launch_bounds__(NT, TM == 1 ? 4 : 2) w4_whole(W4Args a) {
             for (int i = 0; i < 4; ++i) {
                 constexpr int PER = 4 / GV;        // 32-wide steps of a group
                 const bool first = i % PER == 0;
-                const u32x4 fb = RAW ? decode_codes(q[i]) : decode<IN>(q[i], zp[i / PER]);
+                const u32x4 fb = decode<IN>(q[i], zp[i / PER]);
 #pragma unroll
-                for (int t = 0; t < TM; ++t) {
-                    blk[t] = mfma<IN>(fa[i][t], fb, first ? f32x4{0.f, 0.f, 0.f, 0.f} : blk[t]);
-                    if constexpr (RAW) blk[t] = mfma<IN>(fa[i][t], minus_zero_point(zp[i / PER]), blk[t]);
-                }
+                for (int t = 0; t < TM; ++t) blk[t] = mfma<IN>(fa[i][t], fb, first ? f32x4{0.f, 0.f, 0.f, 0.f} : blk[t]);
                 if (i % PER == PER - 1) {
 #pragma unroll
                     for (int t = 0; t < TM; ++t)
@@ -500,7 +459,7 @@ __global__ void __launch_bounds__(NT, TM == 1 ? 4 : 2) w4_whole(W4Args a) {
         slot = slot + 1 == slots ? 0 : slot + 1;
     }
     wait_barrier();                                // every wave has read its last chunk
-    finish<IN, TM>(p, acc, lds, &is_last, tid, wk, wn);
+    finish<TM>(p, acc, lds, &is_last, tid, wk, wn);
 }
 
 // Any other layout: the same split of the work, everything through registers, at
@@ -514,7 +473,6 @@ __global__ void __launch_bounds__(NT, TM == 1 ? 4 : 2) w4_stream(W4Args a) {
     __shared__ int is_last;
     constexpr int WN = w4_cols(TM) / 16, WK = WAVES / WN, CHUNK = w4_chunk(TM), ROW = CHUNK * 2, PR = ROW / 16;
     constexpr int PIECES = 16 * TM * PR / NT;      // of a chunk of a full tile, per thread
-    constexpr bool RAW = IN == IN_BF16 && TM == 1;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wk = wave % WK, wn = wave / WK;
     const int l = lane & 15, g = lane >> 4;
@@ -650,12 +608,11 @@ __global__ void __launch_bounds__(NT, TM == 1 ? 4 : 2) w4_stream(W4Args a) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 constexpr int PER = 4 / GV;        // 32-wide steps of a group
-                const u32x4 fb = RAW ? decode_codes(q[i]) : decode<IN>(q[i], zp[i / PER]);
+                const u32x4 fb = decode<IN>(q[i], zp[i / PER]);
 #pragma unroll
                 for (int t = 0; t < TM; ++t) {
                     const u32x4 fa = *reinterpret_cast<const u32x4 *>(buf + arow[t] * ROW + 16 * ((wk * 32 + 16 * w + 4 * i + g) ^ (arow[t] & 15)));
                     blk[t] = mfma<IN>(fa, fb, i % PER == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : blk[t]);
-                    if constexpr (RAW) blk[t] = mfma<IN>(fa, minus_zero_point(zp[i / PER]), blk[t]);
                 }
                 if (i % PER == PER - 1) {
 #pragma unroll
@@ -697,7 +654,7 @@ __global__ void __launch_bounds__(NT, TM == 1 ? 4 : 2) w4_stream(W4Args a) {
         }
     }
     __syncthreads();                               // every wave has read its last chunk
-    finish<IN, TM>(p, acc, lds, &is_last, tid, wk, wn);
+    finish<TM>(p, acc, lds, &is_last, tid, wk, wn);
 }
 
 template <int IN, int TM, int GV, int SB>

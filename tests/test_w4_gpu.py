@@ -203,3 +203,24 @@ def test_infinite_scale_of_the_last_group(dg, K, G, dtype, zeros):
     Q, S, Z = (None if t is None else torch.stack([t, t]) for t in (Q, S, Z))
     C = dg.moe_gemm_w4(*dev(A, off, Q, S), torch.empty(40, N, device=DEV), group=G, Z=dev(Z)[0])
     om.check(C, want, "experts")
+
+
+@pytest.mark.parametrize("M", [1, 5, 20])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_zero_weights_meet_large_activations(dg, M, dtype, zeros):
+    # most codes equal their zero point, a few activations are a thousand times the others: the sum's bound is
+    # that of the weights that are not zero
+    g = torch.Generator().manual_seed(M)
+    N, K, G = 70, 2048, 64
+    A = torch.randn(M, K, generator=g) * torch.where(torch.rand(K, generator=g) < 0.02, 1000.0, 1.0)
+    _, S, Z = weights(g, N, K, G, zeros, F32)
+    z = torch.full((N, K), 8) if Z is None else (Z % 16).repeat_interleave(G, 1).long()
+    q = torch.where(torch.rand(N, K, generator=g) < 0.97, z, torch.randint(0, 16, (N, K), generator=g))
+    q[7] = z[7]                                                  # nothing but zeros
+    Q = (q[:, 0::2] | q[:, 1::2] << 4).to(torch.uint8)
+    Z = None if Z is None else Z % 16
+    A = A.to(dtype)
+    C = dg.gemm_w4(*dev(A, Q, S), torch.empty(M, N, device=DEV), group=G, Z=dev(Z)[0])
+    om.check(C, om.w4(A, Q, S, Z, G, 0, F32), f"{M}")
+    assert (C[:, 7] == 0).all()
