@@ -101,6 +101,9 @@ bool capturing(hipStream_t stream) {
     return true;
 }
 
+// A launch holds fewer than 2^32 threads.
+bool fits_a_launch(int64_t workgroups, int64_t threads) { return workgroups < ((int64_t)1 << 32) / threads; }
+
 char *out_ptr(const Mat &m) { return const_cast<char *>(m.ptr); }
 
 // ---------------------------------------------------------------- routing
@@ -296,7 +299,7 @@ int pieces_of(int load, int tile, int64_t tiles, int64_t ktiles, const Device &d
 // Launch `units` tiles in a.p.splits pieces each, on the stream's workspace.
 dg_status launch_pieces(int in_kind, int load, int tile, int b_mode, bool wgrad, MoeArgs &a, int64_t units, int64_t bm, int64_t bn,
                         hipStream_t stream) {
-    if (units > INT32_MAX || units * a.p.splits > INT32_MAX) return DG_ERR_OVERFLOW;
+    if (units > INT32_MAX || !fits_a_launch(units * a.p.splits, tile == T256x256 || tile == MOE_T192 ? 512 : 256)) return DG_ERR_OVERFLOW;
     WsLease lease;
     if (a.p.splits > 1) {
         if (lease_workspace(stream, (size_t)units * a.p.splits * bm * bn * sizeof(float), (size_t)units, &lease) != hipSuccess) {
@@ -566,8 +569,8 @@ dg_status w4_entry(const dg_view *A, const dg_view *offsets, const dg_view *Q, c
         a.lds_bytes = std::max(unit + sz + a.a_lds, tm * 8 * 1024);
     }
     if (a.lds_bytes > all) return DG_ERR_OVERFLOW;   // (no size gets here: one chunk's scales are at most 18 KB)
+    if (!fits_a_launch(units * a.splits, 512)) return DG_ERR_OVERFLOW;
     a.units = (int)(units * a.splits);
-    if (units * a.splits > INT32_MAX) return DG_ERR_OVERFLOW;
     WsLease lease;
     if (a.splits > 1) {
         if (lease_workspace(stream, (size_t)units * a.splits * 16 * tm * w4_cols(tm) * sizeof(float), (size_t)units, &lease) != hipSuccess) {

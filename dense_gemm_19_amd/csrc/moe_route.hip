@@ -672,47 +672,84 @@ hipError_t launch_moe_sort(const SortArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
-hipError_t launch_moe_gather(const GatherArgs &a, hipStream_t s) {
-    const int cn = 16 / a.esize, chunks = (a.H + cn - 1) / cn, lanes = lanes_of(chunks);
-    const int pieces = (chunks + GATHER_U * lanes - 1) / (GATHER_U * lanes);
-    const int64_t g = blocks((int64_t)a.n * pieces * lanes);
-    if (g > INT32_MAX) return hipErrorInvalidValue;
-    switch (a.esize) {
-    case 1: hipLaunchKernelGGL((a.stream ? moe_gather_rows<1, true> : moe_gather_rows<1, false>), dim3(g), dim3(NT), 0, s, a, lanes, pieces); break;
-    case 2: hipLaunchKernelGGL((a.stream ? moe_gather_rows<2, true> : moe_gather_rows<2, false>), dim3(g), dim3(NT), 0, s, a, lanes, pieces); break;
-    default: hipLaunchKernelGGL((a.stream ? moe_gather_rows<4, true> : moe_gather_rows<4, false>), dim3(g), dim3(NT), 0, s, a, lanes, pieces); break;
+// A launch holds fewer than 2^32 threads: rows of `per_row` threads go out in runs
+// of at most 2^31, launch(first row, rows) each.
+template <class Launch>
+static hipError_t in_runs(int64_t rows, int64_t per_row, Launch launch) {
+    const int64_t most = std::max<int64_t>(((int64_t)1 << 31) / per_row, 1);
+    for (int64_t r = 0; r < rows; r += most) {
+        launch(r, std::min(most, rows - r));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
     }
-    return hipGetLastError();
+    return hipSuccess;
 }
 
-hipError_t launch_moe_combine(int kind, const CombineArgs &a, hipStream_t s) {
-    const int cn = kind == OUT_F32 ? 4 : 8, chunks = (a.H + cn - 1) / cn, lanes = lanes_of(chunks);
+hipError_t launch_moe_gather(const GatherArgs &all, hipStream_t s) {
+    const int cn = 16 / all.esize, chunks = (all.H + cn - 1) / cn, lanes = lanes_of(chunks);
+    const int pieces = (chunks + GATHER_U * lanes - 1) / (GATHER_U * lanes);
+    return in_runs(all.n, (int64_t)pieces * lanes, [&](int64_t r, int64_t rows) {
+        GatherArgs a = all;
+        a.Y += r * a.y_rs;
+        a.order += r * a.o_s;
+        a.n = (int)rows;
+        const dim3 g((unsigned)blocks(rows * pieces * lanes));
+        switch (a.esize) {
+        case 1: hipLaunchKernelGGL((a.stream ? moe_gather_rows<1, true> : moe_gather_rows<1, false>), g, dim3(NT), 0, s, a, lanes, pieces); break;
+        case 2: hipLaunchKernelGGL((a.stream ? moe_gather_rows<2, true> : moe_gather_rows<2, false>), g, dim3(NT), 0, s, a, lanes, pieces); break;
+        default: hipLaunchKernelGGL((a.stream ? moe_gather_rows<4, true> : moe_gather_rows<4, false>), g, dim3(NT), 0, s, a, lanes, pieces); break;
+        }
+    });
+}
+
+// Tokens from t on, `tokens` of them.
+static CombineArgs tokens_from(CombineArgs a, int64_t t, int64_t tokens) {
+    a.Y += t * a.y_rs;
+    a.pos += t * a.p_rs;
+    if (a.w) a.w += t * a.w_rs;
+    if (a.dw) a.dw += t * a.g_rs;
+    a.T = (int)tokens;
+    return a;
+}
+
+hipError_t launch_moe_combine(int kind, const CombineArgs &all, hipStream_t s) {
+    const int cn = kind == OUT_F32 ? 4 : 8, chunks = (all.H + cn - 1) / cn, lanes = lanes_of(chunks);
     const int pieces = (chunks + lanes - 1) / lanes;
-    const int64_t g = blocks((int64_t)a.T * pieces * lanes);
-    if (g > INT32_MAX) return hipErrorInvalidValue;
-    switch (kind) {
-    case OUT_F32: hipLaunchKernelGGL(moe_combine_rows<OUT_F32>, dim3(g), dim3(NT), 0, s, a, lanes, pieces); break;
-    case OUT_F16: hipLaunchKernelGGL(moe_combine_rows<OUT_F16>, dim3(g), dim3(NT), 0, s, a, lanes, pieces); break;
-    default: hipLaunchKernelGGL(moe_combine_rows<OUT_BF16>, dim3(g), dim3(NT), 0, s, a, lanes, pieces); break;
-    }
-    return hipGetLastError();
+    return in_runs(all.T, (int64_t)pieces * lanes, [&](int64_t t, int64_t tokens) {
+        const CombineArgs a = tokens_from(all, t, tokens);
+        const dim3 g((unsigned)blocks(tokens * pieces * lanes));
+        switch (kind) {
+        case OUT_F32: hipLaunchKernelGGL(moe_combine_rows<OUT_F32>, g, dim3(NT), 0, s, a, lanes, pieces); break;
+        case OUT_F16: hipLaunchKernelGGL(moe_combine_rows<OUT_F16>, g, dim3(NT), 0, s, a, lanes, pieces); break;
+        default: hipLaunchKernelGGL(moe_combine_rows<OUT_BF16>, g, dim3(NT), 0, s, a, lanes, pieces); break;
+        }
+    });
 }
 
 namespace {
 template <int KIND>
-hipError_t grad_kind(CombineArgs a, hipStream_t s) {
-    const int chunks = (a.H + Vals<KIND>::N - 1) / Vals<KIND>::N, lanes = lanes_of(chunks);
+hipError_t grad_kind(CombineArgs all, hipStream_t s) {
+    const int chunks = (all.H + Vals<KIND>::N - 1) / Vals<KIND>::N, lanes = lanes_of(chunks);
     // clearing workgroups: 32, more where their rows would not fit the bit map
-    a.zero_rows = (int)std::min<int64_t>(ZERO_ROWS_MAX, ((int64_t)a.R + 31) / 32);
-    a.zero_blocks = a.zero_rows ? (int)(((int64_t)a.R + a.zero_rows - 1) / a.zero_rows) : 0;
+    all.zero_rows = (int)std::min<int64_t>(ZERO_ROWS_MAX, ((int64_t)all.R + 31) / 32);
+    const int zero_blocks = all.zero_rows ? (int)(((int64_t)all.R + all.zero_rows - 1) / all.zero_rows) : 0;
     // a row of at least 128 chunks gives each of a workgroup's 4 waves 32 lanes of work
     const bool wide = chunks >= 128;
-    const int64_t g = a.zero_blocks + (wide ? (int64_t)a.T : blocks((int64_t)a.T * lanes));
-    if (g > INT32_MAX) return hipErrorInvalidValue;
-    if (g == 0) return hipSuccess;
-    if (wide) hipLaunchKernelGGL((moe_combine_grad_rows<KIND, NT / 64>), dim3(g), dim3(NT), 0, s, a, lanes);
-    else hipLaunchKernelGGL((moe_combine_grad_rows<KIND, 1>), dim3(g), dim3(NT), 0, s, a, lanes);
-    return hipGetLastError();
+    const int64_t per_token = wide ? NT : lanes;
+    auto launch = [&](CombineArgs a, int zeros, int64_t tokens) {
+        a.zero_blocks = zeros;
+        const dim3 g((unsigned)(zeros + blocks(tokens * per_token)));
+        if (wide) hipLaunchKernelGGL((moe_combine_grad_rows<KIND, NT / 64>), g, dim3(NT), 0, s, a, lanes);
+        else hipLaunchKernelGGL((moe_combine_grad_rows<KIND, 1>), g, dim3(NT), 0, s, a, lanes);
+    };
+    if (all.T * per_token <= (int64_t)1 << 31) {
+        if (zero_blocks == 0 && all.T == 0) return hipSuccess;
+        launch(all, zero_blocks, all.T);
+        return hipGetLastError();
+    }
+    // (the clearing workgroups read the places of every token)
+    if (zero_blocks) launch(all, zero_blocks, 0);
+    return in_runs(all.T, per_token, [&](int64_t t, int64_t tokens) { launch(tokens_from(all, t, tokens), 0, tokens); });
 }
 }  // namespace
 

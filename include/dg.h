@@ -457,7 +457,8 @@ dg_status dg_moe_combine_grad(const dg_view *dY, const dg_view *Ys, const dg_vie
  *   act: a dg_act value.
  * Errors: DG_ERR_NDIM (W not 3-D), DG_ERR_INVALID_ARG (act), DG_ERR_DTYPE,
  * DG_ERR_SHAPE_MISMATCH, DG_ERR_STRIDE, DG_ERR_ALIAS, DG_ERR_OVERFLOW (more than
- * 2^28 rows or 2^31 - 1 tiles), view errors. */
+ * 2^28 rows, or a launch of 2^32 threads: 2^24 tiles, 2^23 of the 256-wide ones),
+ * view errors. */
 dg_status dg_moe_gemm(const dg_view *A, const dg_view *offsets, const dg_view *W, const dg_view *C, dg_act act,
                       hipStream_t stream);
 
@@ -479,8 +480,8 @@ dg_status dg_moe_gemm_wgrad(const dg_view *A, const dg_view *D, const dg_view *o
  * group's sum is formed in FP32 and then multiplied by its scale.
  * Errors: DG_ERR_INVALID_ARG (group, act), DG_ERR_DTYPE, DG_ERR_SHAPE_MISMATCH,
  * DG_ERR_UNSUPPORTED_VIEW (A's or Q's rows not contiguous), DG_ERR_STRIDE,
- * DG_ERR_ALIAS, DG_ERR_OVERFLOW (K above 2^20, row strides of 32 MiB or more),
- * view errors. */
+ * DG_ERR_ALIAS, DG_ERR_OVERFLOW (K above 2^20, row strides of 32 MiB or more, 2^23
+ * tiles or more), view errors. */
 dg_status dg_gemm_w4(const dg_view *A, const dg_view *Q, const dg_view *S, const dg_view *Z, const dg_view *C,
                      int32_t group, dg_act act, hipStream_t stream);
 
