@@ -111,6 +111,11 @@ def lib() -> ctypes.CDLL:
             getattr(L, f).restype = ctypes.c_int
         L.dg_quant_fp8.argtypes = [P, P, P, ctypes.c_int, ctypes.c_void_p]
         L.dg_quant_fp8.restype = ctypes.c_int
+        I, B, Z = ctypes.c_int32, ctypes.c_char_p, ctypes.c_size_t
+        for name, args in (("moe_sort", [P, I, P, P, P]), ("moe_gemm", [P] * 4), ("moe_gemm_wgrad", [P] * 4),
+                           ("gemm_w4", [P] * 5 + [I]), ("moe_gemm_w4", [P] * 6 + [I])):
+            f = getattr(L, f"dg_{name}_plan")
+            f.argtypes, f.restype = args + [B, Z], ctypes.c_int
         D = ctypes.POINTER(ctypes.c_double)
         L.dg_calib_mfma.argtypes = [ctypes.c_int, D, ctypes.c_void_p]
         L.dg_calib_read.argtypes = [ctypes.c_void_p, ctypes.c_size_t, D, ctypes.c_void_p]
@@ -405,6 +410,40 @@ def moe_gemm_w4(A: torch.Tensor, offsets: torch.Tensor, Q: torch.Tensor, S: torc
     """gemm_w4 for the rows of every expert (Q, S and Z with a leading expert dim); returns C."""
     _check(_bind().moe_gemm_w4(A, offsets, Q, S, Z, C, group, act, _raw(stream)), "dg_moe_gemm_w4")
     return C
+
+
+def _plan_text(name, *args) -> str:
+    """What dg_<name>_plan writes; tensors become views, None a null one."""
+    views = [view_of(a) if isinstance(a, torch.Tensor) else a for a in args]
+    refs = [ctypes.byref(v) if isinstance(v, View) else v for v in views]
+    buf = ctypes.create_string_buffer(256)
+    _check(getattr(lib(), f"dg_{name}_plan")(*refs, buf, len(buf)), f"dg_{name}_plan")
+    return buf.value.decode()
+
+
+def moe_sort_plan(ids, E: int, offsets, order, pos) -> str:
+    """Describe the launches moe_sort would make for these tensors (nothing runs; needs no GPU)."""
+    return _plan_text("moe_sort", ids, E, offsets, order, pos)
+
+
+def moe_gemm_plan(A, offsets, W, C) -> str:
+    """Describe the kernel moe_gemm would run: its loads, tile, pieces of K and grid."""
+    return _plan_text("moe_gemm", A, offsets, W, C)
+
+
+def moe_gemm_wgrad_plan(A, D, offsets, dW) -> str:
+    """Describe the kernel moe_gemm_wgrad would run."""
+    return _plan_text("moe_gemm_wgrad", A, D, offsets, dW)
+
+
+def gemm_w4_plan(A, Q, S, C, group: int, Z=None) -> str:
+    """Describe the kernel gemm_w4 would run."""
+    return _plan_text("gemm_w4", A, Q, S, Z, C, group)
+
+
+def moe_gemm_w4_plan(A, offsets, Q, S, C, group: int, Z=None) -> str:
+    """Describe the kernel moe_gemm_w4 would run."""
+    return _plan_text("moe_gemm_w4", A, offsets, Q, S, Z, C, group)
 
 
 # ---- measured roofline denominators (include/dg_calib.h)

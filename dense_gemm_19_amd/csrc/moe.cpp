@@ -4,6 +4,8 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdarg>
+#include <cstdio>
 #include <initializer_list>
 
 #include "dg.h"
@@ -74,8 +76,26 @@ bool stack_overlaps(const Stack &s) {
     return self_overlaps(s.one) || (s.E > 1 && s.es < (int64_t)(s.one.hi - s.one.lo));
 }
 
-dg_status ready(std::initializer_list<const Mat *> ms, Device *d) {
-    DG_TRY(current_device(d, true));
+// Where a call's plan is written instead of running it.
+struct Report {
+    char *buf;
+    size_t len;
+    __attribute__((format(printf, 2, 3))) dg_status say(const char *format, ...) {
+        va_list args;
+        va_start(args, format);
+        if (len) std::vsnprintf(buf, len, format, args);
+        va_end(args);
+        return DG_SUCCESS;
+    }
+};
+
+// Nothing to launch.
+dg_status nothing(Report *r) { return r ? r->say("nothing to do") : DG_SUCCESS; }
+
+// The current device (a plan needs none).
+dg_status ready(std::initializer_list<const Mat *> ms, Device *d, const Report *r) {
+    DG_TRY(current_device(d, !r));
+    if (r) return DG_SUCCESS;
     if (!d->gfx950) return DG_ERR_ARCH;
     if (env_on("DG_CHECK_POINTERS"))
         for (const Mat *m : ms)
@@ -94,7 +114,9 @@ dg_status done(hipError_t e, hipStream_t stream) {
 }
 
 // The stream is being captured (or cannot be asked): no workspace is allocated.
-bool capturing(hipStream_t stream) {
+// (A plan is that of a call that is not captured.)
+bool capturing(hipStream_t stream, const Report *r) {
+    if (r) return false;
     hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
     if (hipStreamIsCapturing(stream, &cap) == hipSuccess) return cap != hipStreamCaptureStatusNone;
     (void)hipGetLastError();
@@ -109,7 +131,7 @@ char *out_ptr(const Mat &m) { return const_cast<char *>(m.ptr); }
 // ---------------------------------------------------------------- routing
 
 dg_status sort_entry(const dg_view *ids, int32_t E, const dg_view *offsets, const dg_view *order, const dg_view *pos,
-                     hipStream_t stream) {
+                     hipStream_t stream, Report *r) {
     Mat i, off, ord, p;
     if (E < 1 || E > MOE_MAX_EXPERTS) return DG_ERR_INVALID_ARG;
     DG_TRY(canonicalize(ids, &i));
@@ -126,7 +148,7 @@ dg_status sort_entry(const dg_view *ids, int32_t E, const dg_view *offsets, cons
         spans_overlap(off, p) || spans_overlap(ord, p))
         return DG_ERR_ALIAS;
     Device d;
-    DG_TRY(ready({&i, &off, &ord, &p}, &d));
+    DG_TRY(ready({&i, &off, &ord, &p}, &d, r));
     SortArgs a;
     a.ids = i.ptr; a.i_rs = i.rs; a.i_cs = i.cs;
     a.wide = i.dtype == DG_I64;
@@ -143,14 +165,17 @@ dg_status sort_entry(const dg_view *ids, int32_t E, const dg_view *offsets, cons
     a.table = nullptr;
     WsLease lease;
     const int64_t table_blocks = cdiv(n, sort_table_block(n));
-    if (n >= SORT_TABLE_MIN && table_blocks * E <= SORT_TABLE_MAX && !capturing(stream)) {
+    if (n >= SORT_TABLE_MIN && table_blocks * E <= SORT_TABLE_MAX && !capturing(stream, r)) {
         a.blocks = (int)table_blocks;
+        if (r) return r->say("two launches of %d workgroups, %d ids each", a.blocks, sort_table_block(n));
         if (lease_workspace(stream, (size_t)a.blocks * E * sizeof(int), 0, &lease) != hipSuccess) {
             (void)hipGetLastError();
             return DG_ERR_HIP;
         }
         a.table = reinterpret_cast<int *>(lease.ws);
     }
+    if (r && n <= SORT_ONE_MAX) return r->say("one workgroup, up to %d ids a thread", sort_steps(a.n));
+    if (r) return r->say("three launches of %d workgroups", a.blocks);
     return done(launch_moe_sort(a, stream), stream);
 }
 
@@ -167,7 +192,7 @@ dg_status gather_entry(const dg_view *X, const dg_view *order, int32_t k, const 
     if (spans_overlap(y, x) || spans_overlap(y, o)) return DG_ERR_ALIAS;
     if (y.empty()) return DG_SUCCESS;
     Device d;
-    DG_TRY(ready({&x, &o, &y}, &d));
+    DG_TRY(ready({&x, &o, &y}, &d, nullptr));
     GatherArgs a;
     a.X = x.ptr; a.x_rs = x.rs; a.x_cs = x.cs;
     a.Y = out_ptr(y); a.y_rs = y.rs; a.y_cs = y.cs;
@@ -217,7 +242,7 @@ dg_status combine_entry(const dg_view *Ys, const dg_view *pos, const dg_view *w,
         if (ds.empty() && dv.empty()) return DG_SUCCESS;
     }
     Device d;
-    DG_TRY(ready({&s, &p, &wt, &y, &ds, &dv}, &d));
+    DG_TRY(ready({&s, &p, &wt, &y, &ds, &dv}, &d, nullptr));
     CombineArgs a = {};
     a.Ys = s.ptr; a.s_rs = s.rs; a.s_cs = s.cs;
     a.Y = out_ptr(y); a.y_rs = y.rs; a.y_cs = y.cs;
@@ -289,17 +314,20 @@ int tile_cols(int tile) { return tile == MOE_T192 ? 256 : mfma_tile_bn(tile); }
 // Adding the pieces takes about 3 us, what 8 K tiles of the 32 x 128 tile do (12 of
 // them, 4 experts of 6 rows: 8.1 us whole, 9.6 cut).
 // A captured call runs whole: the pieces' workspace may have to be allocated.
-int pieces_of(int load, int tile, int64_t tiles, int64_t ktiles, const Device &d, hipStream_t stream) {
+int pieces_of(int load, int tile, int64_t tiles, int64_t ktiles, const Device &d, hipStream_t stream, const Report *r) {
     if (tile == T256x256 || tile == MOE_T192 || (load != MOE_DTL && tile == T128x128) || ktiles < (tile == T64x128 ? 16 : 8)) return 1;
     const int64_t s = std::min(d.cus / std::max<int64_t>(tiles, 1), ktiles / 4);
     if (s < 2) return 1;
-    return capturing(stream) ? 1 : (int)s;
+    return capturing(stream, r) ? 1 : (int)s;
 }
 
 // Launch `units` tiles in a.p.splits pieces each, on the stream's workspace.
 dg_status launch_pieces(int in_kind, int load, int tile, int b_mode, bool wgrad, MoeArgs &a, int64_t units, int64_t bm, int64_t bn,
-                        hipStream_t stream) {
+                        hipStream_t stream, Report *r) {
     if (units > INT32_MAX || !fits_a_launch(units * a.p.splits, tile == T256x256 || tile == MOE_T192 ? 512 : 256)) return DG_ERR_OVERFLOW;
+    if (r)
+        return r->say("%s loads, %dx%d tiles, K in %d pieces, %lld workgroups", load == MOE_DTL ? "direct" : load == MOE_VEC ? "vector" : "element",
+                      (int)bm, (int)bn, a.p.splits, (long long)(units * a.p.splits));
     WsLease lease;
     if (a.p.splits > 1) {
         if (lease_workspace(stream, (size_t)units * a.p.splits * bm * bn * sizeof(float), (size_t)units, &lease) != hipSuccess) {
@@ -314,7 +342,7 @@ dg_status launch_pieces(int in_kind, int load, int tile, int b_mode, bool wgrad,
 }
 
 dg_status moe_gemm_entry(const dg_view *A, const dg_view *offsets, const dg_view *W, const dg_view *C, int act,
-                         hipStream_t stream) {
+                         hipStream_t stream, Report *r) {
     Mat x, off, c;
     Stack w;
     DG_TRY(canonicalize(A, &x));
@@ -328,9 +356,9 @@ dg_status moe_gemm_entry(const dg_view *A, const dg_view *offsets, const dg_view
     if (act != DG_ACT_NONE && act != DG_ACT_RELU && act != DG_ACT_GELU_TANH) return DG_ERR_INVALID_ARG;
     if (self_overlaps(c)) return DG_ERR_STRIDE;
     if (spans_overlap(c, x) || spans_overlap(c, w.span) || spans_overlap(c, off)) return DG_ERR_ALIAS;
-    if (c.empty()) return DG_SUCCESS;
+    if (c.empty()) return nothing(r);
     Device d;
-    DG_TRY(ready({&x, &off, &w.span, &c}, &d));
+    DG_TRY(ready({&x, &off, &w.span, &c}, &d, r));
 
     const OpLayout la = layout(x.ptr, n, x.rs, K, x.cs, true);
     const OpLayout lb = layout(w.one.ptr, N, w.one.cs, K, w.one.rs, w.es % 16 == 0 || w.E == 1);
@@ -353,7 +381,7 @@ dg_status moe_gemm_entry(const dg_view *A, const dg_view *offsets, const dg_view
     } else if (load == MOE_DTL) {
         double best = 0.0;
         for (int t : {(int)T256x256, MOE_T192, (int)T128x128}) {
-            const int64_t tiles = expected(t), S = pieces_of(load, t, tiles, ktiles, d, stream);
+            const int64_t tiles = expected(t), S = pieces_of(load, t, tiles, ktiles, d, stream, r);
             const double k_us = t == T256x256 ? 1.78 : t == MOE_T192 ? 1.65 : tiles * S <= d.cus ? 0.8 : 1.3;
             // rounds: between their fraction and the next whole number, the expected
             // count being one of many (8 experts of exactly 2048 rows make one round
@@ -378,18 +406,18 @@ dg_status moe_gemm_entry(const dg_view *A, const dg_view *offsets, const dg_view
     a.p.N = (int)N; a.p.K = (int)K;
     a.p.tiles_n = (int)cdiv(N, bn);
     a.p.ktiles = (int)ktiles;
-    a.p.splits = pieces_of(load, tile, expected(tile), ktiles, d, stream);
+    a.p.splits = pieces_of(load, tile, expected(tile), ktiles, d, stream, r);
     a.p.group_m = tile == T256x256 || tile == MOE_T192 ? 4 : 8;
     a.offsets = off.ptr; a.o_s = off.cs;
     a.E = (int)w.E; a.n = (int)n;
     a.e_bs = w.es;
     // every group with rows (the experts and the rows of none) ends in a partial tile at most
     const int64_t units = ((n + std::min(w.E + 1, n) * (bm - 1)) / bm) * a.p.tiles_n;
-    return launch_pieces(x.dtype == DG_F16 ? IN_F16 : IN_BF16, load, tile, lb.mode, false, a, units, bm, bn, stream);
+    return launch_pieces(x.dtype == DG_F16 ? IN_F16 : IN_BF16, load, tile, lb.mode, false, a, units, bm, bn, stream, r);
 }
 
 dg_status moe_wgrad_entry(const dg_view *A, const dg_view *D, const dg_view *offsets, const dg_view *dW,
-                          hipStream_t stream) {
+                          hipStream_t stream, Report *r) {
     Mat x, g, off;
     Stack w;
     DG_TRY(canonicalize(A, &x));
@@ -402,9 +430,9 @@ dg_status moe_wgrad_entry(const dg_view *A, const dg_view *D, const dg_view *off
     if (n > MOE_MAX_EXTENT || K > MOE_MAX_EXTENT || N > MOE_MAX_EXTENT || w.E > INT32_MAX / 2) return DG_ERR_OVERFLOW;
     if (stack_overlaps(w)) return DG_ERR_STRIDE;
     if (spans_overlap(w.span, x) || spans_overlap(w.span, g) || spans_overlap(w.span, off)) return DG_ERR_ALIAS;
-    if (w.one.empty()) return DG_SUCCESS;
+    if (w.one.empty()) return nothing(r);
     Device d;
-    DG_TRY(ready({&x, &g, &off, &w.span}, &d));
+    DG_TRY(ready({&x, &g, &off, &w.span}, &d, r));
 
     // dW[e] is a product summed over rows: A's columns are its rows
     const OpLayout la = layout(x.ptr, K, x.cs, n, x.rs, true), lb = layout(g.ptr, N, g.cs, n, g.rs, true);
@@ -428,14 +456,14 @@ dg_status moe_wgrad_entry(const dg_view *A, const dg_view *D, const dg_view *off
     a.e_cs = w.es;
     const int64_t tiles = (int64_t)a.p.tiles_m * a.p.tiles_n;
     if (tiles > INT32_MAX || tiles * w.E > INT32_MAX) return DG_ERR_OVERFLOW;
-    a.p.splits = pieces_of(load, tile, tiles * w.E, cdiv(n / w.E, 64), d, stream);
-    return launch_pieces(x.dtype == DG_F16 ? IN_F16 : IN_BF16, load, tile, lb.mode, true, a, tiles * w.E, bm, bn, stream);
+    a.p.splits = pieces_of(load, tile, tiles * w.E, cdiv(n / w.E, 64), d, stream, r);
+    return launch_pieces(x.dtype == DG_F16 ? IN_F16 : IN_BF16, load, tile, lb.mode, true, a, tiles * w.E, bm, bn, stream, r);
 }
 
 // ---------------------------------------------------------------- 4-bit weights
 
 dg_status w4_entry(const dg_view *A, const dg_view *offsets, const dg_view *Q, const dg_view *S, const dg_view *Z,
-                   const dg_view *C, int32_t group, int act, bool experts, hipStream_t stream) {
+                   const dg_view *C, int32_t group, int act, bool experts, hipStream_t stream, Report *r) {
     Mat x, c, off;
     Stack q, s, z;
     DG_TRY(canonicalize(A, &x));
@@ -467,9 +495,9 @@ dg_status w4_entry(const dg_view *A, const dg_view *offsets, const dg_view *Q, c
     if (self_overlaps(c)) return DG_ERR_STRIDE;
     for (const Mat *m : {&x, &q.span, &s.span, &z.span, &off})
         if (spans_overlap(c, *m)) return DG_ERR_ALIAS;
-    if (c.empty()) return DG_SUCCESS;
+    if (c.empty()) return nothing(r);
     Device d;
-    DG_TRY(ready({&x, &off, &q.span, &s.span, &z.span, &c}, &d));
+    DG_TRY(ready({&x, &off, &q.span, &s.span, &z.span, &c}, &d, r));
 
     W4Args a = {};
     a.A = x.ptr; a.a_rs = x.rs;
@@ -515,7 +543,7 @@ dg_status w4_entry(const dg_view *A, const dg_view *offsets, const dg_view *Q, c
     const int chunk = w4_chunk(tm);
     const int64_t chunks = cdiv(K, chunk), units = tiles_m * a.slabs;
     int64_t splits = 1;
-    if (!experts && chunks * chunk > 4096 && 2 * units <= d.cus && !capturing(stream))
+    if (!experts && chunks * chunk > 4096 && 2 * units <= d.cus && !capturing(stream, r))
         splits = std::min<int64_t>(d.cus / units, chunks / 2);
     a.chunks = (int)std::max<int64_t>(cdiv(chunks, splits), 1);
     a.splits = (int)std::max<int64_t>(cdiv(chunks, a.chunks), 1);
@@ -570,6 +598,9 @@ dg_status w4_entry(const dg_view *A, const dg_view *offsets, const dg_view *Q, c
     }
     if (a.lds_bytes > all) return DG_ERR_OVERFLOW;   // (no size gets here: one chunk's scales are at most 18 KB)
     if (!fits_a_launch(units * a.splits, 512)) return DG_ERR_OVERFLOW;
+    if (r)
+        return r->say("%s, %dx%d tiles, K in %d pieces, %lld workgroups of %d LDS bytes", a.whole ? "aligned words" : "any layout", 16 * tm,
+                      w4_cols(tm), a.splits, (long long)(units * a.splits), a.lds_bytes);
     a.units = (int)(units * a.splits);
     WsLease lease;
     if (a.splits > 1) {
@@ -590,7 +621,7 @@ extern "C" {
 
 dg_status dg_moe_sort(const dg_view *ids, int32_t E, const dg_view *offsets, const dg_view *order, const dg_view *pos,
                       hipStream_t stream) {
-    return dg::sort_entry(ids, E, offsets, order, pos, stream);
+    return dg::sort_entry(ids, E, offsets, order, pos, stream, nullptr);
 }
 
 dg_status dg_moe_gather(const dg_view *X, const dg_view *order, int32_t k, const dg_view *Xs, hipStream_t stream) {
@@ -608,22 +639,55 @@ dg_status dg_moe_combine_grad(const dg_view *dY, const dg_view *Ys, const dg_vie
 
 dg_status dg_moe_gemm(const dg_view *A, const dg_view *offsets, const dg_view *W, const dg_view *C, dg_act act,
                       hipStream_t stream) {
-    return dg::moe_gemm_entry(A, offsets, W, C, (int)act, stream);
+    return dg::moe_gemm_entry(A, offsets, W, C, (int)act, stream, nullptr);
 }
 
 dg_status dg_moe_gemm_wgrad(const dg_view *A, const dg_view *D, const dg_view *offsets, const dg_view *dW,
                             hipStream_t stream) {
-    return dg::moe_wgrad_entry(A, D, offsets, dW, stream);
+    return dg::moe_wgrad_entry(A, D, offsets, dW, stream, nullptr);
 }
 
 dg_status dg_gemm_w4(const dg_view *A, const dg_view *Q, const dg_view *S, const dg_view *Z, const dg_view *C,
                      int32_t group, dg_act act, hipStream_t stream) {
-    return dg::w4_entry(A, nullptr, Q, S, Z, C, group, (int)act, false, stream);
+    return dg::w4_entry(A, nullptr, Q, S, Z, C, group, (int)act, false, stream, nullptr);
 }
 
 dg_status dg_moe_gemm_w4(const dg_view *A, const dg_view *offsets, const dg_view *Q, const dg_view *S,
                          const dg_view *Z, const dg_view *C, int32_t group, dg_act act, hipStream_t stream) {
-    return dg::w4_entry(A, offsets, Q, S, Z, C, group, (int)act, true, stream);
+    return dg::w4_entry(A, offsets, Q, S, Z, C, group, (int)act, true, stream, nullptr);
+}
+
+dg_status dg_moe_sort_plan(const dg_view *ids, int32_t E, const dg_view *offsets, const dg_view *order, const dg_view *pos,
+                           char *buf, size_t len) {
+    if (!buf && len) return DG_ERR_INVALID_ARG;
+    dg::Report r = {buf, len};
+    return dg::sort_entry(ids, E, offsets, order, pos, nullptr, &r);
+}
+
+dg_status dg_moe_gemm_plan(const dg_view *A, const dg_view *offsets, const dg_view *W, const dg_view *C, char *buf, size_t len) {
+    if (!buf && len) return DG_ERR_INVALID_ARG;
+    dg::Report r = {buf, len};
+    return dg::moe_gemm_entry(A, offsets, W, C, DG_ACT_NONE, nullptr, &r);
+}
+
+dg_status dg_moe_gemm_wgrad_plan(const dg_view *A, const dg_view *D, const dg_view *offsets, const dg_view *dW, char *buf, size_t len) {
+    if (!buf && len) return DG_ERR_INVALID_ARG;
+    dg::Report r = {buf, len};
+    return dg::moe_wgrad_entry(A, D, offsets, dW, nullptr, &r);
+}
+
+dg_status dg_gemm_w4_plan(const dg_view *A, const dg_view *Q, const dg_view *S, const dg_view *Z, const dg_view *C,
+                          int32_t group, char *buf, size_t len) {
+    if (!buf && len) return DG_ERR_INVALID_ARG;
+    dg::Report r = {buf, len};
+    return dg::w4_entry(A, nullptr, Q, S, Z, C, group, DG_ACT_NONE, false, nullptr, &r);
+}
+
+dg_status dg_moe_gemm_w4_plan(const dg_view *A, const dg_view *offsets, const dg_view *Q, const dg_view *S,
+                              const dg_view *Z, const dg_view *C, int32_t group, char *buf, size_t len) {
+    if (!buf && len) return DG_ERR_INVALID_ARG;
+    dg::Report r = {buf, len};
+    return dg::w4_entry(A, offsets, Q, S, Z, C, group, DG_ACT_NONE, true, nullptr, &r);
 }
 
 }  // extern "C"

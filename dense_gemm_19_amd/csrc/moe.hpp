@@ -17,7 +17,11 @@ constexpr int64_t MOE_MAX_EXTENT = INT32_MAX - 4095;
 
 constexpr int MOE_MAX_EXPERTS = 2048;    // LDS counters of a sort workgroup: 16 waves x E
 constexpr int MOE_MAX_ROWS = 1 << 28;     // of the experts' products: tile counts of 64 experts fit 32 bits
-constexpr int SORT_ONE_MAX = 16384;      // ids sorted by one workgroup; more take three launches
+constexpr int SORT_T = 1024;             // threads of a sort workgroup
+constexpr int SORT_ONE_MAX = 16384;      // ids sorted by one workgroup; more take two launches or three
+// Ids a thread of that workgroup holds at most: few where few ids allow it, for
+// fewer registers and instructions to fetch.
+constexpr int sort_steps(int n) { return n <= SORT_T ? 1 : n <= 4 * SORT_T ? 4 : SORT_ONE_MAX / SORT_T; }
 constexpr int SORT_BLOCK = 4096;         // ids per workgroup of the three-launch sort (at least E fit half of it)
 // ids per workgroup of the two-launch sort: few ids want more workgroups (30208: 10.5
 // us, 11.9 with 4096), many a smaller table (262144 over 256 experts: 14.7, 15.1 with 2048)

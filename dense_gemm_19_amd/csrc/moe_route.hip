@@ -15,7 +15,7 @@ typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
 
 // ------------------------------------------------------------------ sort
 
-constexpr int SORT_T = 1024, SORT_W = SORT_T / 64;
+constexpr int SORT_W = SORT_T / 64;
 
 // The key of id i: its expert, or -1 (dropped).
 __device__ __forceinline__ int sort_key(const SortArgs &a, int i) {
@@ -658,8 +658,8 @@ hipError_t launch_moe_sort(const SortArgs &a, hipStream_t s) {
     }
     if (a.n <= SORT_ONE_MAX) {
         const size_t lds = (SORT_W + 1) * a.E * sizeof(int);
-        // few steps per wave where few ids allow it: fewer registers and instructions to fetch
-        const auto k = a.n <= SORT_T ? moe_sort_one<1> : a.n <= 4 * SORT_T ? moe_sort_one<4> : moe_sort_one<SORT_ONE_MAX / SORT_T>;
+        const int steps = sort_steps(a.n);
+        const auto k = steps == 1 ? moe_sort_one<1> : steps == 4 ? moe_sort_one<4> : moe_sort_one<SORT_ONE_MAX / SORT_T>;
         if ((e = allow_lds(k, lds)) != hipSuccess) return e;
         hipLaunchKernelGGL(k, dim3(1), dim3(SORT_T), lds, s, a);
         return hipGetLastError();

@@ -490,6 +490,22 @@ dg_status dg_gemm_w4(const dg_view *A, const dg_view *Q, const dg_view *S, const
 dg_status dg_moe_gemm_w4(const dg_view *A, const dg_view *offsets, const dg_view *Q, const dg_view *S,
                          const dg_view *Z, const dg_view *C, int32_t group, dg_act act, hipStream_t stream);
 
+/* Validate the arguments as the call without _plan does and write a one-line,
+ * NUL-terminated description of what it would run into buf[0..len-1] (the loads,
+ * tile, pieces of K and grid of a product, the launches of a sort), without
+ * launching anything.  Needs no GPU: with no device visible it plans for a 256-CU
+ * gfx950; the plan is that of a call that is not captured.  buf may be NULL only if
+ * len == 0 (DG_ERR_INVALID_ARG). */
+dg_status dg_moe_sort_plan(const dg_view *ids, int32_t E, const dg_view *offsets, const dg_view *order, const dg_view *pos,
+                           char *buf, size_t len);
+dg_status dg_moe_gemm_plan(const dg_view *A, const dg_view *offsets, const dg_view *W, const dg_view *C, char *buf, size_t len);
+dg_status dg_moe_gemm_wgrad_plan(const dg_view *A, const dg_view *D, const dg_view *offsets, const dg_view *dW, char *buf,
+                                 size_t len);
+dg_status dg_gemm_w4_plan(const dg_view *A, const dg_view *Q, const dg_view *S, const dg_view *Z, const dg_view *C,
+                          int32_t group, char *buf, size_t len);
+dg_status dg_moe_gemm_w4_plan(const dg_view *A, const dg_view *offsets, const dg_view *Q, const dg_view *S,
+                              const dg_view *Z, const dg_view *C, int32_t group, char *buf, size_t len);
+
 /* Helper (no page passage): static, human-readable name of a status code
  * ("DG_ERR_ALIAS", ...); "DG_ERR_UNKNOWN" for a value outside dg_status. */
 const char *dg_status_str(dg_status s);

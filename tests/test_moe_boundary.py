@@ -212,3 +212,28 @@ def test_extents_next_to_32_bits(size, status):
     refused(status, dg.moe_gemm_wgrad, one(2, 8), one(2, size), i32(2), one(1, 8, size))
     refused(status, dg.gemm_w4, z(2, 32), z(1, 16, dt=U8).expand(size, 16), one(size, 1), one(2, size), 32)
     refused(status, dg.gemm_w4, z(1, 32).expand(size, 32), z(8, 16, dt=U8), z(8, 1), one(size, 8), 32)
+
+
+def test_plans_refuse_what_the_calls_refuse():
+    i32 = lambda *s: z(*s, dt=I32)   # noqa: E731
+    with pytest.raises(dg.DGError, match="INVALID_ARG"):
+        dg.moe_sort_plan(i32(T, K), 0, i32(1), i32(R), i32(T, K))
+    with pytest.raises(dg.DGError, match="SHAPE_MISMATCH"):
+        dg.moe_gemm_plan(z(R, H), i32(E), z(E, H, N), z(R, N))
+    with pytest.raises(dg.DGError, match="STRIDE"):
+        dg.moe_gemm_wgrad_plan(z(R, H), z(R, N), i32(E + 1), z(1, H, N).expand(E, H, N))
+    with pytest.raises(dg.DGError, match="DTYPE"):
+        dg.gemm_w4_plan(z(R, 64), z(N, 32), z(N, 2), z(R, N), 32)
+    with pytest.raises(dg.DGError, match="NDIM"):
+        dg.moe_gemm_w4_plan(z(R, 64), i32(E + 1), z(N, 32, dt=U8), z(E, N, 2), z(R, N), 32)
+    # a grid of 2^32 threads and the largest below it
+    for experts, ok in ((2 ** 24, False), (2 ** 24 - 1, True)):
+        args = (one(16, 8), one(16, 8), torch.empty(experts + 1, dtype=I32), torch.empty(experts, 8, 8, dtype=BF16))
+        if ok:
+            assert dg.moe_gemm_wgrad_plan(*args).endswith(f"{experts} workgroups")
+        else:
+            with pytest.raises(dg.DGError, match="OVERFLOW"):
+                dg.moe_gemm_wgrad_plan(*args)
+    assert dg.moe_gemm_plan(z(0, H), i32(E + 1), z(E, H, N), z(0, N)) == "nothing to do"
+    assert dg.STATUS[dg.lib().dg_gemm_w4_plan(None, None, None, None, None, 32, None, 8)] == "DG_ERR_INVALID_ARG"
+    assert dg.STATUS[dg.lib().dg_gemm_w4_plan(None, None, None, None, None, 32, None, 0)] == "DG_ERR_NULL"
