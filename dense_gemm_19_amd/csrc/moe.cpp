@@ -199,11 +199,14 @@ dg_status gather_entry(const dg_view *X, const dg_view *order, int32_t k, const 
     a.order = o.ptr; a.o_s = o.cs;
     a.T = (int)x.rows; a.k = k; a.n = (int)y.rows; a.H = (int)y.cols; a.esize = y.esize;
     a.vec = x.cols_contig() && y.cols_contig();
-    // An output above 96 MB goes past the caches: 16384 rows of 4096 BF16 39.5 us
-    // instead of 45.8.  A product that then reads them and is bound by memory takes
-    // that back (with 4096 -> 1024: 163 us for both instead of 160), one as large as
-    // such row counts mostly meet does not (4096 -> 14336: 1.7 ms).
-    a.stream = y.rows * y.cols * y.esize > (int64_t)96 << 20;
+    // An output above 160 MB goes past the caches.  Alone a gather gains by that from
+    // 96 MB on (16384 rows of 4096 BF16, 128 MB: 39.6 us instead of 45.0), but the
+    // product that reads its output next gives it back while the last-level cache
+    // still holds a good part of it.  Gather and product, 8 experts, 4096 -> 1024 and
+    // -> 4096, past the caches and through them: 101 MB 153 and 449 us, 150 and 437;
+    // 128 MB 239 and 565, 237 and 560; 187 MB 270 and 744, 283 and 747; 256 MB 394
+    // and 1033, 405 and 1043.
+    a.stream = y.rows * y.cols * y.esize > (int64_t)160 << 20;
     return done(launch_moe_gather(a, stream), stream);
 }
 

@@ -88,6 +88,23 @@ def test_sort_by_one_workgroup_in_a_graph():
             assert torch.equal(a.cpu(), b)
 
 
+# ---------------------------------------------------------------- gather past the caches
+
+@gpu
+@pytest.mark.parametrize("H,dtype", [(2101, BF16), (4202, torch.float8_e4m3fn), (1050, F32)])
+def test_gather_of_outputs_above_160_mb(H, dtype):
+    g = torch.Generator().manual_seed(2)
+    T, k = 20500, 2
+    order = torch.randperm(T * k, generator=g).int()
+    order[::97] = -1
+    assert T * k * H * dtype.itemsize > 160 << 20
+    X = torch.randint(0, 120, (T, H * dtype.itemsize), generator=g, dtype=U8).view(dtype)   # finite in every type
+    out = torch.full((T * k, H * dtype.itemsize), 0x7f, dtype=U8, device=DEV).view(dtype)
+    dg.moe_gather(X.to(DEV), order.to(DEV), k, out)
+    want = torch.where((order >= 0)[:, None], X.view(U8)[order.clamp(min=0).long() // k], 0)
+    assert torch.equal(out.cpu().view(U8), want)
+
+
 # ---------------------------------------------------------------- experts' products
 
 # rows of each expert, K, N, what runs; K and the rows are no whole tiles
