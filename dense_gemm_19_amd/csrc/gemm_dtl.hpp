@@ -688,8 +688,8 @@ __device__ __forceinline__ void mfma_dtl_body(const MfmaArgs &p, const int t_dir
         // loaded value placed after a store would wait for that store too (the
         // counter that tracks loads counts stores), and each element would pay
         // a memory round trip; so would a load inside a per-element branch.
-        // Where C's rows are contiguous and 4-element aligned (ep.vec4), each
-        // lane's 4 adjacent columns go in one vector load or store.
+        // Where C's rows are contiguous (ep.vec4), each lane's 4 adjacent columns go
+        // in one vector load or store.
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
             const int m = mr + 16 * i;

@@ -42,8 +42,10 @@ struct Epilogue {
     int64_t bias_s;     // bytes between consecutive bias elements (0: one value for every column)
     int bias_kind;      // OutKind numbering: OUT_F32 / OUT_F16 / OUT_BF16
     int act;            // Act
-    int vec4;           // C's rows are contiguous and 4-element aligned (c_cs == element size,
-                        // C and c_rs multiples of 4 elements): 4 adjacent columns in one access
+    int vec4;           // C's rows are contiguous (c_cs == element size): 4 adjacent columns in one
+                        // access.  Loads (beta != 0) need C and c_rs to be multiples of 4 elements,
+                        // which dg_gemm* ask for; stores go to any element's address, and the
+                        // experts' products, which never read C, set it for every such C.
     constexpr bool plain() const { return bias == nullptr && act == ACT_NONE; }
 };
 

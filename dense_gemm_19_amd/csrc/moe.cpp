@@ -556,7 +556,7 @@ dg_status w4_entry(const dg_view *A, const dg_view *offsets, const dg_view *Q, c
     // a CU's LDS where 2 chunks of few rows fit and the grid has two workgroups for
     // a CU, else all.
     const int half = 80 * 1024 - 128, all = 160 * 1024 - 128;
-    const int unit = 8 * 2048, a_buf = (rows * chunk * 2 + 1023) & ~1023;
+    const int unit = 8 * 2048, a_buf = rows * chunk * 2;
     if (usual) {
         const int64_t need = std::min<int64_t>(groups, (int64_t)a.chunks * chunk / group + 5);   // from a multiple of 4 on
         auto pitch = [](int64_t bytes) { return (int)std::max<int64_t>((cdiv(bytes, 4) | 1) * 4, 12); };   // (the reciprocal of one word is 2^32)
@@ -566,7 +566,7 @@ dg_status w4_entry(const dg_view *A, const dg_view *offsets, const dg_view *Q, c
         a.z_pitch = Z ? pitch(need + 3) : 0;
         const int sz = region(a.s_pitch) + (Z ? region(a.z_pitch) : 0);
         const int64_t mean = experts ? std::min<int64_t>(M / std::min(q.E, M) + 1, rows) : rows;
-        const int a_mean = (int)((mean * chunk * 2 + 1023) & ~1023);
+        const int a_mean = (int)(mean * chunk * 2);
         auto fits = [&](int depth, int bufs, int cap) {
             a.depth = depth;
             a.a_lds = (cap - depth * unit - sz) & ~1023;   // (all there is: experts differ in rows)

@@ -11,7 +11,7 @@
 // count and the workgroups past the real count leave at once.  Weight gradient:
 // the tiles are known (E matrices of K x N), only the summed rows vary.
 //
-// Three kernels share this mapping.  The direct-to-LDS kernel is the library's
+// Two kernels share this mapping.  The direct-to-LDS kernel is the library's
 // dense one (gemm_dtl.hpp) on the expert's part of the operands.  The
 // register-staged kernel below serves rows at any alignment (16-byte loads) and
 // any strides (element loads).

@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(NT, TM == 1 ? 4 : 2) w4_whole(W4Args a) {
 
     const char *qb = a.Q + uniform((int64_t)p.e * a.q_es + (int64_t)p.n0 * a.q_rs);
     const char *ab = a.A + uniform((int64_t)(p.begin + p.m0) * a.a_rs);
-    const int a_bytes = (here * ROW + 1023) & ~1023;   // a chunk of the rows there are, in whole loads of a wave
+    const int a_bytes = here * ROW;                // a chunk of the rows there are
     // Chunks in LDS at a time: a.depth units, as far as A's part holds the rows; all
     // of them are issued before the first is computed where that is all there are,
     // else one less, since a slot is refilled while the next one is computed.
@@ -334,8 +334,8 @@ __global__ void __launch_bounds__(NT, TM == 1 ? 4 : 2) w4_whole(W4Args a) {
     const uint32_t q_off[2] = {(uint32_t)min(16 * wn + q_row, p.cols - 1) * (uint32_t)a.q_rs,
                                (uint32_t)min(16 * wn + q_row + 8, p.cols - 1) * (uint32_t)a.q_rs};
     const int q_bytes = nk / 2;
-    constexpr int RPL = PR >= 64 ? 1 : 64 / PR;    // rows of A that one load touches
-    const int a_row = PR >= 64 ? 0 : lane / PR, a_piece = 16 * ((lane % PR) ^ a_row);
+    constexpr int LPR = PR / 64;                   // loads of a wave in a row of A
+    static_assert(PR % 64 == 0, "no load crosses a row");
     const int a_loads = (a_bytes / 1024 - wave + WAVES - 1) / WAVES;   // of a chunk, by this wave
     auto issue = [&](int c, int slot) __attribute__((always_inline)) {
         const int last = nk * 2 - c * ROW - 16;    // A's pieces past K read the last one (cleared below)
@@ -343,10 +343,9 @@ __global__ void __launch_bounds__(NT, TM == 1 ? 4 : 2) w4_whole(W4Args a) {
         uint32_t dst = lds0 + a_ring + slot * a_bytes + wave * 1024;
 #pragma unroll 1
         for (int j = wave; j * 1024 < a_bytes; j += WAVES) {
-            const int r = PR >= 64 ? j / (PR / 64) : j * RPL, half = PR > 64 ? (j % (PR / 64)) * 1024 : 0;
-            const uint32_t piece = (uint32_t)min((a_piece ^ (16 * (r & 15))) + half, last);
-            const uint32_t rows = RPL > 1 ? (uint32_t)min(a_row, here - 1 - r) * (uint32_t)a.a_rs : 0u;
-            dtl::lds_load16(ac + (int64_t)r * a.a_rs, piece + rows, __builtin_amdgcn_readfirstlane(dst));
+            const int r = j / LPR;
+            const uint32_t piece = (uint32_t)min(16 * (lane ^ (r & 15)) + j % LPR * 1024, last);
+            dtl::lds_load16(ac + (int64_t)r * a.a_rs, piece, __builtin_amdgcn_readfirstlane(dst));
             dst += WAVES * 1024;
         }
         const int at = c * (CHUNK / 2) + wk * (UNIT / 2);
