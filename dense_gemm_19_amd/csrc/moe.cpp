@@ -367,12 +367,16 @@ dg_status moe_gemm_entry(const dg_view *A, const dg_view *offsets, const dg_view
     const OpLayout lb = layout(w.one.ptr, N, w.one.cs, K, w.one.rs, w.es % 16 == 0 || w.E == 1);
     int load = MOE_ELEM;
     if (la.mode == KMAJ && la.vec && lb.vec) load = la.dtl && lb.dtl ? MOE_DTL : MOE_VEC;
-    // The tile: by the mean row count of the experts that can have rows; of the
-    // larger direct ones the quickest by what a K tile takes in each (us, measured
-    // on long K; two 128 x 128 workgroups share a CU) and the rounds that the
-    // expected tiles make: 64 experts of 234 rows, 4096 -> 512 FP16, take 127 us as
-    // 256 x 256 tiles, 120.5 as 192 x 256; 13 experts of 366 rows, 1088 -> 192, 25
-    // us as 256 x 256, 16.6 as pieces of 128 x 128.
+    // The tile: by the mean row count of the experts that can have rows.  Direct, 32
+    // x 128 up to a mean of 48 (8 experts, 4096 -> 14336: 16 rows each 178 us, 128 x
+    // 128 178; 64 rows 243 and 188; between, whole 32-row tiles are as quick at 32
+    // rows, 184 and 176, and behind at 40, 228 and 178: a bound of 24 would serve
+    // even counts better).  Of the larger ones the quickest by what a K tile takes
+    // in each (us, measured on long K; two 128 x 128 workgroups share a CU) and the
+    // rounds that the expected tiles make: 64 experts of 234 rows, 4096 -> 512 FP16,
+    // take 127 us as 256 x 256 tiles, 120.5 as 192 x 256; 13 experts of 366 rows,
+    // 1088 -> 192, 25 us as 256 x 256, 16.6 as pieces of 128 x 128.
+    // Expected tiles: an expert's last one is half full on average.
     const int64_t used = std::min(w.E, n), mean = n / std::max<int64_t>(used, 1), ktiles = cdiv(K, 64);
     auto expected = [&](int t) {
         const int64_t rows = tile_rows(load, t);
@@ -398,6 +402,8 @@ dg_status moe_gemm_entry(const dg_view *A, const dg_view *offsets, const dg_view
             }
         }
     } else if (load == MOE_VEC) {
+        // 8 experts of 512 rows, 1001 -> 2047: 41 us, 55 as 64 x 64; of 128 rows, whose
+        // 128 x 128 tiles leave CUs idle, 18 us, 29 as 128 x 128
         tile = mean <= 64 || expected(T128x128) < d.cus ? T64x64 : T128x128;
     }
     const int bm = tile_rows(load, tile), bn = tile_cols(tile);
@@ -442,6 +448,10 @@ dg_status moe_wgrad_entry(const dg_view *A, const dg_view *D, const dg_view *off
     int load = MOE_ELEM;
     if (x.cs == 2 && g.cs == 2 && K >= 8 && N >= 8)
         load = la.mode == MNMAJ && lb.mode == MNMAJ && la.dtl && lb.dtl ? MOE_DTL : MOE_VEC;
+    // The largest tile that gives every CU one: 8 experts of 1024 rows, 2048 x 2048,
+    // 82 us as 256 x 256 tiles, 103 as 128 x 128; 1024 x 1024 34 and 29.  Loads at any
+    // alignment: 1001 x 1023 55 us as 64 x 64, 39 as 128 x 128; 513 x 511 of 256 rows
+    // 10.4 and 13.9.
     int tile = load == MOE_ELEM ? T64x64 : T128x128;
     if (load == MOE_DTL && w.E * cdiv(K, 256) * cdiv(N, 256) >= d.cus) tile = T256x256;
     if (load == MOE_VEC && w.E * cdiv(K, 128) * cdiv(N, 128) < d.cus) tile = T64x64;
@@ -526,7 +536,10 @@ dg_status w4_entry(const dg_view *A, const dg_view *offsets, const dg_view *Q, c
                        words(s) && (!Z || words(z));
 
     // Rows of a tile: as few tiles as the largest allows, evenly filled (one
-    // matrix), or by the mean count of the experts that can have rows.
+    // matrix), or by the mean count of the experts that can have rows (16 experts of
+    // 0.5 to 1.5 times the mean, 4096 -> 7168, G 128: mean 8 83 us as 16 rows x 32
+    // columns, 102 as 32 x 64; 12 126 and 104; 16 107 as 32 x 64, 116 as 48 x 64; 28
+    // 145 and 123).
     int64_t tiles_m;
     int tm, rows;
     if (experts) {
@@ -540,9 +553,11 @@ dg_status w4_entry(const dg_view *A, const dg_view *offsets, const dg_view *Q, c
         rows = (int)std::min<int64_t>(M, 16 * tm);
     }
     a.slabs = (int)cdiv(N, w4_cols(tm));
-    // K in pieces where one matrix has too few slabs to fill the device and
-    // several chunks: each piece keeps two.  A captured call runs whole: the
-    // pieces' workspace may have to be allocated.
+    // K in pieces where one matrix has too few slabs to fill the device and K is
+    // above 4096: each piece keeps two chunks.  (The bound is a high one: cut from 4
+    // chunks on, 1 x 1024 x 4096 takes 6.9 us instead of 7.9, 33 x 2048 x 4096 9.6
+    // instead of 16.3.)  Experts' K is never cut: their tiles vary with the rows.  A
+    // captured call runs whole: the pieces' workspace may have to be allocated.
     const int chunk = w4_chunk(tm);
     const int64_t chunks = cdiv(K, chunk), units = tiles_m * a.slabs;
     int64_t splits = 1;

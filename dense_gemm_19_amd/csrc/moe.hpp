@@ -20,14 +20,19 @@ constexpr int MOE_MAX_ROWS = 1 << 28;     // of the experts' products: tile coun
 constexpr int SORT_T = 1024;             // threads of a sort workgroup
 constexpr int SORT_ONE_MAX = 16384;      // ids sorted by one workgroup; more take two launches or three
 // Ids a thread of that workgroup holds at most: few where few ids allow it, for
-// fewer registers and instructions to fetch.
+// fewer registers and instructions to fetch (512 ids: 3.4 us, 3.9 with 16).
 constexpr int sort_steps(int n) { return n <= SORT_T ? 1 : n <= 4 * SORT_T ? 4 : SORT_ONE_MAX / SORT_T; }
 constexpr int SORT_BLOCK = 4096;         // ids per workgroup of the three-launch sort (at least E fit half of it)
 // ids per workgroup of the two-launch sort: few ids want more workgroups (30208: 10.5
 // us, 11.9 with 4096), many a smaller table (262144 over 256 experts: 14.7, 15.1 with 2048)
 constexpr int sort_table_block(int64_t n) { return n <= 1 << 17 ? 2048 : 4096; }
-constexpr int SORT_TABLE_MIN = 8192;     // ids from which two launches are quicker than one workgroup
-constexpr int SORT_TABLE_MAX = 1 << 15;  // counts that every workgroup of the two-launch sort reads at most
+// ids from which two launches are mostly quicker than one workgroup (64 experts: 6000
+// ids 8.0 us, one workgroup 7.8; 8192 7.9 and 9.2; 16384 8.3 and 15.3; 8 experts: 8192
+// 9.7 and 8.5)
+constexpr int SORT_TABLE_MIN = 8192;
+// counts that every workgroup of the two-launch sort reads at most (32768 of them:
+// 16.3 us, three launches 21.7; 65536 would still be quicker, 22.8 and 30.4)
+constexpr int SORT_TABLE_MAX = 1 << 15;
 
 struct SortArgs {
     const char *ids; int64_t i_rs, i_cs;   // [T][k]

@@ -4,9 +4,9 @@
 //   C[m][n] = act(sum over k of A[m][k] * s[n][k/G] * (q[n][k] - z[n][k/G]))
 //
 // Codes and zero points are whole numbers of at most 255, exact in FP16 and
-// BF16, so they go to the matrix cores as they are; each scale group's sum is
-// formed in FP32 there and then enters the FP32 accumulator times its scale,
-// once.  No weight is rounded.
+// BF16, and so are their differences, which go to the matrix cores; each scale
+// group's sum is formed in FP32 there and then enters the FP32 accumulator times its
+// scale, once.  No weight is rounded.
 //
 // Bound by the bytes of the codes where few rows meet many weights (half a byte
 // per weight), by the latency of the loads and the instructions fetched for small
@@ -273,9 +273,10 @@ __device__ __forceinline__ void finish(const Part &p, const f32x4 (&acc)[TM], ch
 // Pieces of 16 bytes are XOR-swizzled by their row in LDS (fetched so from memory)
 // and rows of scales are an odd number of words apart, so that the 16 rows of a
 // read fall on distinct banks.
-// Measured: 1 x 14336 x 4096 BF16 10.8 us (12.0 us with scales and part of the
-// bookkeeping through registers), 33 x 4096 x 14336 FP16 19.0 us (25.1), 16 rows
-// over 16 experts of 7168 x 4096 46 to 58 us, the codes at 4.8 to 6.0 TB/s.
+// Measured: 1 x 14336 x 4096 BF16 12.0 us (zero points as a second product of the
+// same rows, which needs 9 instructions for 8 codes, takes 10.6 but rounds at the size
+// of |A|(q + z): sums of zero weights were not zero), 33 x 4096 x 14336 FP16 19.1 us,
+// 16 rows over 16 experts of 7168 x 4096 50 to 60 us, the codes at 4.6 to 5.6 TB/s.
 template <int IN, int TM, int GV, int SB, bool ZP>
 __global__ void __launch_bounds__(NT, TM == 1 ? 4 : 2) w4_whole(W4Args a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];   // codes, A, scales, zero points; then the waves' sums

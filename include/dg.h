@@ -476,8 +476,12 @@ dg_status dg_moe_gemm_wgrad(const dg_view *A, const dg_view *D, const dg_view *o
  *   S [N][ceil(K / group)] DG_F32, DG_F16 or DG_BF16; Z the same shape, DG_U8 (any
  *     value 0 .. 255), or NULL: 8.
  *   group: a positive multiple of 32.  C [M][N] DG_F32, DG_F16 or DG_BF16.
- * No weight is rounded: codes and zero points enter the products exactly, each
+ * No weight is rounded: the differences q - z enter the products exactly, each
  * group's sum is formed in FP32 and then multiplied by its scale.
+ * Quickest where K is a multiple of 32, rows of A and Q begin at multiples of 16
+ * bytes, the groups of S and Z are adjacent, and each of S and Z begins and ends at
+ * a multiple of 4 bytes (dg_gemm_w4_plan: "aligned words"); any other layout takes
+ * about twice as long.
  * Errors: DG_ERR_INVALID_ARG (group, act), DG_ERR_DTYPE, DG_ERR_SHAPE_MISMATCH,
  * DG_ERR_UNSUPPORTED_VIEW (A's or Q's rows not contiguous), DG_ERR_STRIDE,
  * DG_ERR_ALIAS, DG_ERR_OVERFLOW (K above 2^20, row strides of 32 MiB or more, 2^23
