@@ -355,7 +355,7 @@ dg_status moe_gemm_entry(const dg_view *A, const dg_view *offsets, const dg_view
     if (w.E < 1 || w.one.rows != x.cols || c.rows != x.rows || c.cols != w.one.cols) return DG_ERR_SHAPE_MISMATCH;
     DG_TRY(index_vector(offsets, w.E + 1, &off));
     const int64_t n = x.rows, K = x.cols, N = c.cols;
-    if (n > MOE_MAX_ROWS || K > MOE_MAX_EXTENT || N > MOE_MAX_EXTENT || w.E > INT32_MAX / 2) return DG_ERR_OVERFLOW;
+    if (n > MOE_MAX_ROWS || K > MOE_MAX_EXTENT || N > MOE_MAX_EXTENT || w.E > MOE_MAX_SCANNED) return DG_ERR_OVERFLOW;
     if (act != DG_ACT_NONE && act != DG_ACT_RELU && act != DG_ACT_GELU_TANH) return DG_ERR_INVALID_ARG;
     if (self_overlaps(c)) return DG_ERR_STRIDE;
     if (spans_overlap(c, x) || spans_overlap(c, w.span) || spans_overlap(c, off)) return DG_ERR_ALIAS;
@@ -500,7 +500,7 @@ dg_status w4_entry(const dg_view *A, const dg_view *offsets, const dg_view *Q, c
     if (q.E < 1 || s.E != q.E || s.one.rows != N || s.one.cols != groups) return DG_ERR_SHAPE_MISMATCH;
     if (Z && (z.E != q.E || z.one.rows != N || z.one.cols != groups)) return DG_ERR_SHAPE_MISMATCH;
     if (experts) DG_TRY(index_vector(offsets, q.E + 1, &off));
-    if (M > (experts ? MOE_MAX_ROWS : MOE_MAX_EXTENT) || K > (1 << 20) || N > MOE_MAX_EXTENT || q.E > INT32_MAX / 2) return DG_ERR_OVERFLOW;
+    if (M > (experts ? MOE_MAX_ROWS : MOE_MAX_EXTENT) || K > (1 << 20) || N > MOE_MAX_EXTENT || q.E > MOE_MAX_SCANNED) return DG_ERR_OVERFLOW;
     if (!x.cols_contig() || !q.one.cols_contig()) return DG_ERR_UNSUPPORTED_VIEW;
     // lane offsets within a workgroup's rows and columns are 32-bit
     const int64_t lim = ((int64_t)1 << 31) / 64;

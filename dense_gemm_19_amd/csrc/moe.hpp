@@ -17,6 +17,7 @@ constexpr int64_t MOE_MAX_EXTENT = INT32_MAX - 4095;
 
 constexpr int MOE_MAX_EXPERTS = 2048;    // LDS counters of a sort workgroup: 16 waves x E
 constexpr int MOE_MAX_ROWS = 1 << 28;     // of the experts' products: tile counts of 64 experts fit 32 bits
+constexpr int MOE_MAX_SCANNED = 1 << 14; // experts of the products whose workgroups scan the offsets (find_slot)
 constexpr int SORT_T = 1024;             // threads of a sort workgroup
 constexpr int SORT_ONE_MAX = 16384;      // ids sorted by one workgroup; more take two launches or three
 // Ids a thread of that workgroup holds at most: few where few ids allow it, for

@@ -41,7 +41,9 @@ __device__ __forceinline__ void group_rows(const char *off, int64_t o_s, int E, 
 // units (tiles_n: units per row of tiles).  False: b is past the last unit, or
 // the offsets name more than the grid's `units`, which only overlapping groups
 // can (n is at most 2^28, so that 64 groups' tile rows fit 32 bits).  Every wave
-// does this by itself.
+// does this by itself, so a call's scans grow with the square of E (4096 rows of 63
+// experts, 512 -> 1024: 16.5 us where there are no others, 58 us among 256, 107 among
+// 512, 273 among 1024, 893 among 2048), and E is bounded (MOE_MAX_SCANNED).
 template <int BM>
 __device__ __forceinline__ bool find_slot(const char *off, int64_t o_s, int E, int n, int tiles_n, int units, int b, Slot &s) {
     const int lane = threadIdx.x & 63;

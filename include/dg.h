@@ -457,14 +457,15 @@ dg_status dg_moe_combine_grad(const dg_view *dY, const dg_view *Ys, const dg_vie
  *   act: a dg_act value.
  * Errors: DG_ERR_NDIM (W not 3-D), DG_ERR_INVALID_ARG (act), DG_ERR_DTYPE,
  * DG_ERR_SHAPE_MISMATCH, DG_ERR_STRIDE, DG_ERR_ALIAS, DG_ERR_OVERFLOW (more than
- * 2^28 rows, or a launch of 2^32 threads: 2^24 tiles, 2^23 of the 256-wide ones),
- * view errors. */
+ * 2^28 rows, more than 16384 experts, whose offsets every workgroup scans, or a
+ * launch of 2^32 threads: 2^24 tiles, 2^23 of the 256-wide ones), view errors. */
 dg_status dg_moe_gemm(const dg_view *A, const dg_view *offsets, const dg_view *W, const dg_view *C, dg_act act,
                       hipStream_t stream);
 
 /* dW[e] <- sum over expert e's rows of A[r]^T * D[r] (zero for an expert without rows).
  *   A [n][K] and D [n][N]: both DG_F16 or both DG_BF16; dW [E][K][N] DG_F32, DG_F16
- *   or DG_BF16.  Otherwise as dg_moe_gemm, but for the rows: up to 2^31 - 4096. */
+ *   or DG_BF16.  Otherwise as dg_moe_gemm, but up to 2^31 - 4096 rows, and as many
+ *   experts as the tiles allow. */
 dg_status dg_moe_gemm_wgrad(const dg_view *A, const dg_view *D, const dg_view *offsets, const dg_view *dW,
                             hipStream_t stream);
 
@@ -481,7 +482,7 @@ dg_status dg_moe_gemm_wgrad(const dg_view *A, const dg_view *D, const dg_view *o
  * Quickest where K is a multiple of 32, rows of A and Q begin at multiples of 16
  * bytes, the groups of S and Z are adjacent, and each of S and Z begins and ends at
  * a multiple of 4 bytes (dg_gemm_w4_plan: "aligned words"); any other layout takes
- * about twice as long.
+ * up to one and a half times as long.
  * Errors: DG_ERR_INVALID_ARG (group, act), DG_ERR_DTYPE, DG_ERR_SHAPE_MISMATCH,
  * DG_ERR_UNSUPPORTED_VIEW (A's or Q's rows not contiguous), DG_ERR_STRIDE,
  * DG_ERR_ALIAS, DG_ERR_OVERFLOW (K above 2^20, row strides of 32 MiB or more, 2^23

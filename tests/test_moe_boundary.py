@@ -237,3 +237,10 @@ def test_plans_refuse_what_the_calls_refuse():
     assert dg.moe_gemm_plan(z(0, H), i32(E + 1), z(E, H, N), z(0, N)) == "nothing to do"
     assert dg.STATUS[dg.lib().dg_gemm_w4_plan(None, None, None, None, None, 32, None, 8)] == "DG_ERR_INVALID_ARG"
     assert dg.STATUS[dg.lib().dg_gemm_w4_plan(None, None, None, None, None, 32, None, 0)] == "DG_ERR_NULL"
+
+
+def test_experts_whose_offsets_are_scanned_are_bounded():
+    for E, status in ((16384, "STRIDE"), (16385, "OVERFLOW"), (1 << 30, "OVERFLOW")):
+        off = one(E + 1, dt=I32)
+        refused(status, dg.moe_gemm, z(R, H), off, one(E, H, N), one(R, N))
+        refused(status, dg.moe_gemm_w4, z(R, 64), off, z(1, N, 32, dt=U8).expand(E, N, 32), one(E, N, 2), one(R, N), 32)
