@@ -11,6 +11,8 @@ HIP kernels.  PyTorch provides the device memory and the current stream.
     dg.moe_sort(ids, E, offsets, order, pos)                   # tokens by expert, on the device
     dg.moe_gemm(Xs, offsets, W, C)                             # every expert's product
     dg.gemm_w4(A, Q, S, C, group=128)                          # 4-bit weights
+    dg.quant_mx4(X, Q, S)                                      # to microscaled 4-bit codes (MXFP4)
+    dg.gemm_mx4(A, Q, S, C, SA=SA)                             # their product
 
 Tensors may have any strides (transposes, padded rows, up to 4-D views whose
 leading dims merge into one row stride); views are passed as pointer + shape +
@@ -29,6 +31,8 @@ LIB_PATH = os.path.join(_HERE, "libdg.so")
 
 # dg_dtype codes
 DG_F32, DG_F16, DG_BF16, DG_F8E4M3, DG_I32, DG_I64, DG_U8 = 0, 1, 2, 3, 4, 5, 6
+# dg_mx4_mode codes (the scale of a block)
+DG_MX4_FLOOR, DG_MX4_CEIL = 0, 1
 # dg_act codes (fused epilogue activation)
 DG_ACT_NONE, DG_ACT_RELU, DG_ACT_GELU_TANH = 0, 1, 2
 _DTYPE = {torch.float32: DG_F32, torch.float16: DG_F16, torch.bfloat16: DG_BF16,
@@ -113,7 +117,8 @@ def lib() -> ctypes.CDLL:
         L.dg_quant_fp8.restype = ctypes.c_int
         I, B, Z = ctypes.c_int32, ctypes.c_char_p, ctypes.c_size_t
         for name, args in (("moe_sort", [P, I, P, P, P]), ("moe_gemm", [P] * 4), ("moe_gemm_wgrad", [P] * 4),
-                           ("gemm_w4", [P] * 5 + [I]), ("moe_gemm_w4", [P] * 6 + [I])):
+                           ("gemm_w4", [P] * 5 + [I]), ("moe_gemm_w4", [P] * 6 + [I]), ("gemm_mx4", [P] * 5),
+                           ("moe_gemm_mx4", [P] * 6)):
             f = getattr(L, f"dg_{name}_plan")
             f.argtypes, f.restype = args + [B, Z], ctypes.c_int
         D = ctypes.POINTER(ctypes.c_double)
@@ -444,6 +449,49 @@ def gemm_w4_plan(A, Q, S, C, group: int, Z=None) -> str:
 def moe_gemm_w4_plan(A, offsets, Q, S, C, group: int, Z=None) -> str:
     """Describe the kernel moe_gemm_w4 would run."""
     return _plan_text("moe_gemm_w4", A, offsets, Q, S, Z, C, group)
+
+
+# ---- microscaled 4-bit operands (MXFP4)
+
+def quant_mx4(X: torch.Tensor, Q: torch.Tensor, S: torch.Tensor, mode: int = DG_MX4_FLOOR, stream=None):
+    """Codes Q [M, ceil(K/2)] and scale bytes S [M, ceil(K/32)] (uint8) of X [M, K], any strides (or 3-D stacks
+    of each): 32 elements along K share the power of two 2^(b - 127) that the largest of them asks for
+    (DG_MX4_FLOOR: the specification's, sizes above 6 of it saturate; DG_MX4_CEIL: nothing saturates).
+    Returns (Q, S)."""
+    _check(_bind().quant_mx4(X, Q, S, mode, _raw(stream)), "dg_quant_mx4")
+    return Q, S
+
+
+def dequant_mx4(Q: torch.Tensor, S: torch.Tensor, Y: torch.Tensor, stream=None) -> torch.Tensor:
+    """Y [M, K] <- the numbers that codes and scales stand for; returns Y."""
+    _check(_bind().dequant_mx4(Q, S, Y, _raw(stream)), "dg_dequant_mx4")
+    return Y
+
+
+def gemm_mx4(A: torch.Tensor, Q: torch.Tensor, S: torch.Tensor, C: torch.Tensor, SA: torch.Tensor | None = None,
+             act: int = DG_ACT_NONE, stream=None) -> torch.Tensor:
+    """C <- act(A @ W.T), W [N, K] in codes Q and scales S; A [M, K] in 16 bits, or codes [M, ceil(K/2)] with
+    scales SA [M, ceil(K/32)].  Returns C."""
+    _check(_bind().gemm_mx4(A, SA, Q, S, C, act, _raw(stream)), "dg_gemm_mx4")
+    return C
+
+
+def moe_gemm_mx4(A: torch.Tensor, offsets: torch.Tensor, Q: torch.Tensor, S: torch.Tensor, C: torch.Tensor,
+                 SA: torch.Tensor | None = None, act: int = DG_ACT_NONE, stream=None) -> torch.Tensor:
+    """gemm_mx4 for the rows of every expert (Q and S with a leading expert dim); rows of no expert are zero.
+    Returns C."""
+    _check(_bind().moe_gemm_mx4(A, SA, offsets, Q, S, C, act, _raw(stream)), "dg_moe_gemm_mx4")
+    return C
+
+
+def gemm_mx4_plan(A, Q, S, C, SA=None) -> str:
+    """Describe the kernel gemm_mx4 would run."""
+    return _plan_text("gemm_mx4", A, SA, Q, S, C)
+
+
+def moe_gemm_mx4_plan(A, offsets, Q, S, C, SA=None) -> str:
+    """Describe the kernel moe_gemm_mx4 would run."""
+    return _plan_text("moe_gemm_mx4", A, SA, offsets, Q, S, C)
 
 
 # ---- measured roofline denominators (include/dg_calib.h)

@@ -5,6 +5,7 @@
 
 #include <hip/hip_runtime_api.h>
 
+#include "dg.h"
 #include "kernels.hpp"
 
 namespace dg {
@@ -140,5 +141,18 @@ constexpr int w4_chunk(int tm) { return tm == 1 ? 1024 : 512; }
 // tm: rows of a workgroup / 16, 1 to W4_MAX_TM (4, whose chunk of A leaves LDS
 // no room for a second, took 26 us for 248 x 1452 x 2592 where 3 takes 14.2 to 21)
 hipError_t launch_w4(int in_kind, int tm, const W4Args &a, int64_t units, hipStream_t stream);
+// The same for microscaled weights (w4_mx.hip): E2M1 codes, E8M0 scale bytes, G = 32, no zero points
+hipError_t launch_w4_mx(int in_kind, int tm, const W4Args &a, int64_t units, hipStream_t stream);
+
+// Row strides below this keep lane offsets within a workgroup's 64 rows or columns in 32 bits.
+constexpr int64_t W4_MAX_PITCH = ((int64_t)1 << 31) / 64;
+
+// Plans and launches a product with 4-bit weights whose arguments are checked (moe.cpp).
+// mx: microscaled weights.  zeros: null for none.
+struct Stack;
+struct Mat;
+struct Report;
+dg_status w4_run(const Mat &x, const Mat &off, const Stack &q, const Stack &s, const Stack *zeros, const Mat &c, int group, int act,
+                 bool experts, bool mx, hipStream_t stream, Report *r);
 
 }  // namespace dg

@@ -1,0 +1,241 @@
+// mx4.cpp -- the entry points of the microscaled 4-bit (MXFP4) operators: validation,
+// kernel selection and launch (see include/dg.h for the contracts).
+#include <hip/hip_runtime_api.h>
+
+#include <cmath>
+
+#include "entry.hpp"
+#include "moe.hpp"
+#include "mx4.hpp"
+
+namespace dg {
+namespace {
+
+// A matrix, or a stack of them where the view is 3-D.
+dg_status matrices(const dg_view *v, Stack *s) {
+    if (v && v->ndim == 3) return canonicalize_stack(v, s);
+    DG_TRY(canonicalize(v, &s->one));
+    s->E = 1;
+    s->span = s->one;
+    return DG_SUCCESS;
+}
+
+// Codes and scales of E matrices of M x K.
+dg_status codes_of(const Stack &q, const Stack &s, int64_t E, int64_t M, int64_t K) {
+    if (q.one.dtype != DG_U8 || s.one.dtype != DG_U8) return DG_ERR_DTYPE;
+    if (q.E != E || q.one.rows != M || q.one.cols != cdiv(K, 2)) return DG_ERR_SHAPE_MISMATCH;
+    if (s.E != E || s.one.rows != M || s.one.cols != cdiv(K, 32)) return DG_ERR_SHAPE_MISMATCH;
+    if (!q.one.cols_contig()) return DG_ERR_UNSUPPORTED_VIEW;
+    return DG_SUCCESS;
+}
+
+// Workgroups of the kernels whose threads take MX4_RUN chunks of 8 elements each.
+dg_status runs(int64_t E, int64_t M, int64_t K, int *chunks, uint32_t *mul, int64_t *units) {
+    *chunks = (int)(4 * cdiv(K, 32));
+    *mul = (uint32_t)((((uint64_t)1 << 32) + *chunks - 1) / *chunks);
+    int64_t total;
+    if (__builtin_mul_overflow(E, M, &total) || __builtin_mul_overflow(total, (int64_t)*chunks, &total)) return DG_ERR_OVERFLOW;
+    *units = cdiv(total, 256 * MX4_RUN);
+    return fits_a_launch(*units, 256) ? DG_SUCCESS : DG_ERR_OVERFLOW;
+}
+
+dg_status quant_entry(const dg_view *X, const dg_view *Q, const dg_view *S, int mode, hipStream_t stream) {
+    Stack x, q, s;
+    DG_TRY(matrices(X, &x));
+    DG_TRY(matrices(Q, &q));
+    DG_TRY(matrices(S, &s));
+    if (mode != DG_MX4_FLOOR && mode != DG_MX4_CEIL) return DG_ERR_INVALID_ARG;
+    if (!is_float(x.one.dtype)) return DG_ERR_DTYPE;
+    const int64_t M = x.one.rows, K = x.one.cols;
+    DG_TRY(codes_of(q, s, x.E, M, K));
+    if (M > MOE_MAX_EXTENT || K > MOE_MAX_EXTENT || x.E > INT32_MAX) return DG_ERR_OVERFLOW;
+    if (stack_overlaps(q) || stack_overlaps(s)) return DG_ERR_STRIDE;
+    if (spans_overlap(q.span, x.span) || spans_overlap(s.span, x.span) || spans_overlap(q.span, s.span)) return DG_ERR_ALIAS;
+    if (x.E == 0 || x.one.empty()) return DG_SUCCESS;
+    Device d;
+    DG_TRY(ready({&x.span, &q.span, &s.span}, &d, nullptr));
+    Mx4QuantArgs a = {};
+    a.X = x.one.ptr; a.x_es = x.es; a.x_rs = x.one.rs; a.x_cs = x.one.cs;
+    a.Q = out_ptr(q.one); a.q_es = q.es; a.q_rs = q.one.rs;
+    a.S = out_ptr(s.one); a.s_es = s.es; a.s_rs = s.one.rs; a.s_cs = s.one.cs;
+    a.x_kind = x.one.dtype;
+    a.M = (int)M; a.K = (int)K; a.E = (int)x.E;
+    a.ceil = mode == DG_MX4_CEIL;
+    const bool by_columns = !x.one.cols_contig();
+    int64_t units;
+    if (by_columns) {
+        a.vec = x.one.rows_contig();
+        a.tiles_m = (int)cdiv(M, MX4_TILE_M);
+        a.tiles_k = (int)cdiv(K, MX4_TILE_K);
+        const int64_t tiles = (int64_t)a.tiles_m * a.tiles_k;
+        if (tiles > INT32_MAX || __builtin_mul_overflow(tiles, x.E, &units) || !fits_a_launch(units, 512)) return DG_ERR_OVERFLOW;
+    } else {
+        DG_TRY(runs(x.E, M, K, &a.chunks, &a.chunk_mul, &units));
+    }
+    return done(launch_mx4_quant(by_columns, a, units, stream), stream);
+}
+
+dg_status dequant_entry(const dg_view *Q, const dg_view *S, const dg_view *Y, hipStream_t stream) {
+    Stack q, s, y;
+    DG_TRY(matrices(Q, &q));
+    DG_TRY(matrices(S, &s));
+    DG_TRY(matrices(Y, &y));
+    if (!is_float(y.one.dtype)) return DG_ERR_DTYPE;
+    const int64_t M = y.one.rows, K = y.one.cols;
+    DG_TRY(codes_of(q, s, y.E, M, K));
+    if (M > MOE_MAX_EXTENT || K > MOE_MAX_EXTENT || y.E > INT32_MAX) return DG_ERR_OVERFLOW;
+    if (stack_overlaps(y)) return DG_ERR_STRIDE;
+    if (spans_overlap(y.span, q.span) || spans_overlap(y.span, s.span)) return DG_ERR_ALIAS;
+    if (y.E == 0 || y.one.empty()) return DG_SUCCESS;
+    Device d;
+    DG_TRY(ready({&q.span, &s.span, &y.span}, &d, nullptr));
+    Mx4DequantArgs a = {};
+    a.Q = q.one.ptr; a.q_es = q.es; a.q_rs = q.one.rs;
+    a.S = s.one.ptr; a.s_es = s.es; a.s_rs = s.one.rs; a.s_cs = s.one.cs;
+    a.Y = out_ptr(y.one); a.y_es = y.es; a.y_rs = y.one.rs; a.y_cs = y.one.cs;
+    a.y_kind = y.one.dtype;
+    a.M = (int)M; a.K = (int)K; a.E = (int)y.E;
+    a.vec = y.one.cols_contig();
+    int64_t units;
+    DG_TRY(runs(y.E, M, K, &a.chunks, &a.chunk_mul, &units));
+    return done(launch_mx4_dequant(a, units, stream), stream);
+}
+
+// The product of codes with codes, its arguments checked.
+dg_status codes_product(const Mat &x, const Mat &sx, const Mat &off, const Stack &q, const Stack &s, const Mat &c, int act, bool experts,
+                        hipStream_t stream, Report *r) {
+    Device d;
+    DG_TRY(ready({&x, &sx, &off, &q.span, &s.span, &c}, &d, r));
+    const int64_t M = x.rows, N = c.cols, bytes = x.cols;
+    Mx4GemmArgs a = {};
+    a.A = x.ptr; a.a_rs = x.rs;
+    a.SA = sx.ptr; a.sa_rs = sx.rs; a.sa_cs = sx.cols > 1 ? sx.cs : 1;
+    a.Q = q.one.ptr; a.q_rs = q.one.rs; a.q_es = q.es;
+    a.S = s.one.ptr; a.s_rs = s.one.rs; a.s_cs = s.one.cols > 1 ? s.one.cs : 1; a.s_es = s.es;
+    a.C = out_ptr(c); a.c_rs = c.rs; a.c_cs = c.cs; a.out_kind = c.dtype; a.act = act;
+    a.vec4 = c.cs == c.esize;
+    a.M = (int)M; a.N = (int)N;
+    a.row_bytes = (int)bytes;
+    a.blocks = (int)cdiv(bytes, 16);
+    if (experts) { a.offsets = off.ptr; a.o_s = off.cs; }
+    a.E = (int)q.E;
+    a.ktiles = (int)cdiv(bytes, 128);
+    // Loads to LDS: rows at multiples of 4 bytes, none overlapping the next one, since
+    // the last chunk of a row may reach into it; lane offsets within a tile are 32-bit.
+    auto words = [&](const Mat &m, int64_t es) {
+        return reinterpret_cast<uintptr_t>(m.ptr) % 4 == 0 && es % 4 == 0 &&
+               (m.rows <= 1 || (m.rs % 4 == 0 && m.rs >= bytes && m.rs < ((int64_t)1 << 23)));
+    };
+    int load = MX4_ANY;
+    if (a.sa_cs == 1 && a.s_cs == 1 && a.blocks >= 8) load = words(x, 0) && words(q.one, q.E > 1 ? q.es : 0) ? MX4_DIRECT : MX4_BYTES;
+    const int64_t used = experts ? std::min(q.E, M) : 1, mean = M / used;
+    auto expected = [&](int t) {
+        const int64_t bm = mx4_tile_m(t);
+        return (experts ? std::max(used, used / 2 + cdiv(M, bm)) : cdiv(M, bm)) * cdiv(N, mx4_tile_n(t));
+    };
+    int tile = MX4_T64;
+    if (load == MX4_DIRECT && mean > 128 && expected(MX4_T256) >= d.cus) tile = MX4_T256;
+    else if (load != MX4_ANY && mean > 64 && expected(MX4_T128) >= d.cus / 2) tile = MX4_T128;
+    const int64_t bm = mx4_tile_m(tile), bn = mx4_tile_n(tile);
+    a.tiles_n = (int)cdiv(N, bn);
+    a.group_m = tile == MX4_T256 ? 4 : 8;
+    int64_t units = experts ? ((M + std::min(q.E + 1, M) * (bm - 1)) / bm) * a.tiles_n : cdiv(M, bm) * a.tiles_n;
+    // K in pieces where the tiles leave most of the device idle; a captured call runs
+    // whole: the pieces' workspace may have to be allocated.
+    int64_t splits = 1;
+    if (!experts && tile != MX4_T256 && 2 * units <= d.cus && a.ktiles >= 4 && !capturing(stream, r))
+        splits = std::min<int64_t>(d.cus / units, a.ktiles / 2);
+    a.kt_per_split = (int)cdiv(std::max(a.ktiles, 1), splits);
+    a.splits = (int)cdiv(std::max(a.ktiles, 1), a.kt_per_split);
+    if (units > INT32_MAX / a.splits || !fits_a_launch(units * a.splits, 512)) return DG_ERR_OVERFLOW;
+    a.units = (int)(units * a.splits);
+    if (r)
+        return r->say("%s loads, %dx%d tiles, K in %d pieces, %d workgroups", load == MX4_DIRECT ? "direct" : load == MX4_BYTES ? "vector" : "element", (int)bm, (int)bn, a.splits, a.units);
+    WsLease lease;
+    if (a.splits > 1) {
+        if (lease_workspace(stream, (size_t)units * a.splits * bm * bn * sizeof(float), (size_t)units, &lease) != hipSuccess) {
+            (void)hipGetLastError();
+            return DG_ERR_HIP;
+        }
+        a.ws = lease.ws;
+        a.counters = lease.counters;
+    }
+    return done(launch_mx4_gemm(tile, load, a, a.units, stream), stream);
+}
+
+dg_status gemm_entry(const dg_view *A, const dg_view *SA, const dg_view *offsets, const dg_view *Q, const dg_view *S,
+                     const dg_view *C, int act, bool experts, hipStream_t stream, Report *r) {
+    Mat x, sx, c, off;
+    Stack q, s;
+    DG_TRY(canonicalize(A, &x));
+    if (SA) DG_TRY(canonicalize(SA, &sx));
+    DG_TRY(canonicalize(C, &c));
+    if (experts) {
+        DG_TRY(canonicalize_stack(Q, &q));
+        DG_TRY(canonicalize_stack(S, &s));
+    } else {
+        DG_TRY(canonicalize(Q, &q.one));
+        DG_TRY(canonicalize(S, &s.one));
+        for (Stack *t : {&q, &s}) { t->E = 1; t->span = t->one; }
+    }
+    const bool codes = x.dtype == DG_U8;
+    if (!(codes || is_half(x.dtype)) || !is_float(c.dtype)) return DG_ERR_DTYPE;
+    if (codes && !SA) return DG_ERR_NULL;
+    if (!codes && SA) return DG_ERR_INVALID_ARG;
+    if (act != DG_ACT_NONE && act != DG_ACT_RELU && act != DG_ACT_GELU_TANH) return DG_ERR_INVALID_ARG;
+    if (x.cols > MOE_MAX_EXTENT / 2) return DG_ERR_OVERFLOW;
+    const int64_t M = x.rows, N = c.cols, K = codes ? 2 * x.cols : x.cols;
+    if (c.rows != M || q.E < 1) return DG_ERR_SHAPE_MISMATCH;
+    DG_TRY(codes_of(q, s, q.E, N, K));
+    if (codes && sx.dtype != DG_U8) return DG_ERR_DTYPE;
+    if (codes && (sx.rows != M || sx.cols != cdiv(K, 32))) return DG_ERR_SHAPE_MISMATCH;
+    if (experts) DG_TRY(index_vector(offsets, q.E + 1, &off));
+    if (M > (experts ? MOE_MAX_ROWS : MOE_MAX_EXTENT) || N > MOE_MAX_EXTENT || q.E > MOE_MAX_SCANNED) return DG_ERR_OVERFLOW;
+    if (!x.cols_contig()) return DG_ERR_UNSUPPORTED_VIEW;
+    if (!codes && (K > (1 << 20) || x.rs >= W4_MAX_PITCH || q.one.rs >= W4_MAX_PITCH || s.one.rs >= W4_MAX_PITCH)) return DG_ERR_OVERFLOW;
+    if (self_overlaps(c)) return DG_ERR_STRIDE;
+    for (const Mat *m : {&x, &sx, &q.span, &s.span, &off})
+        if (spans_overlap(c, *m)) return DG_ERR_ALIAS;
+    if (c.empty()) return nothing(r);
+    if (codes) return codes_product(x, sx, off, q, s, c, act, experts, stream, r);
+    return w4_run(x, off, q, s, nullptr, c, 32, act, experts, true, stream, r);
+}
+
+}  // namespace
+}  // namespace dg
+
+extern "C" {
+
+dg_status dg_quant_mx4(const dg_view *X, const dg_view *Q, const dg_view *S, dg_mx4_mode mode, hipStream_t stream) {
+    return dg::quant_entry(X, Q, S, (int)mode, stream);
+}
+
+dg_status dg_dequant_mx4(const dg_view *Q, const dg_view *S, const dg_view *Y, hipStream_t stream) {
+    return dg::dequant_entry(Q, S, Y, stream);
+}
+
+dg_status dg_gemm_mx4(const dg_view *A, const dg_view *SA, const dg_view *Q, const dg_view *S, const dg_view *C, dg_act act,
+                      hipStream_t stream) {
+    return dg::gemm_entry(A, SA, nullptr, Q, S, C, (int)act, false, stream, nullptr);
+}
+
+dg_status dg_moe_gemm_mx4(const dg_view *A, const dg_view *SA, const dg_view *offsets, const dg_view *Q, const dg_view *S,
+                          const dg_view *C, dg_act act, hipStream_t stream) {
+    return dg::gemm_entry(A, SA, offsets, Q, S, C, (int)act, true, stream, nullptr);
+}
+
+dg_status dg_gemm_mx4_plan(const dg_view *A, const dg_view *SA, const dg_view *Q, const dg_view *S, const dg_view *C, char *buf,
+                           size_t len) {
+    if (!buf && len) return DG_ERR_INVALID_ARG;
+    dg::Report r = {buf, len};
+    return dg::gemm_entry(A, SA, nullptr, Q, S, C, DG_ACT_NONE, false, nullptr, &r);
+}
+
+dg_status dg_moe_gemm_mx4_plan(const dg_view *A, const dg_view *SA, const dg_view *offsets, const dg_view *Q, const dg_view *S,
+                               const dg_view *C, char *buf, size_t len) {
+    if (!buf && len) return DG_ERR_INVALID_ARG;
+    dg::Report r = {buf, len};
+    return dg::gemm_entry(A, SA, offsets, Q, S, C, DG_ACT_NONE, true, nullptr, &r);
+}
+
+}  // extern "C"

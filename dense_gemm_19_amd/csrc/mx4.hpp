@@ -1,0 +1,83 @@
+// mx4.hpp -- argument blocks and launchers of the microscaled 4-bit (MXFP4) operators
+// (host and device).  All strides are in bytes.
+//
+// A matrix of codes is [rows][ceil(K / 2)] bytes, rows contiguous; its scales are
+// [rows][ceil(K / 32)] bytes with any strides.
+#pragma once
+#include <cstdint>
+
+#include <hip/hip_runtime_api.h>
+
+#include "kernels.hpp"
+
+namespace dg {
+
+// ---------------------------------------------------------------- quantiser (mx4_quant.hip)
+
+constexpr int MX4_RUN = 4;         // 8-element chunks of a thread (rows kernels)
+constexpr int MX4_TILE_M = 256;    // tile of the columns kernel: rows of X, and K
+constexpr int MX4_TILE_K = 256;
+
+struct Mx4QuantArgs {
+    const char *X; int64_t x_es, x_rs, x_cs;   // [E][M][K]
+    char *Q; int64_t q_es, q_rs;               // [E][M][ceil(K / 2)]
+    char *S; int64_t s_es, s_rs, s_cs;         // [E][M][ceil(K / 32)]
+    int x_kind;                                // OutKind numbering
+    int M, K, E;
+    int chunks;                                // of a row: 4 * ceil(K / 32)
+    uint32_t chunk_mul;                        // ceil(2^32 / chunks), for chunks < 4096
+    int tiles_m, tiles_k;                      // columns kernel
+    int ceil;                                  // the scale at which nothing saturates
+    int vec;                                   // columns kernel: rows of X are adjacent
+};
+
+// by_columns: X's rows are not contiguous.
+hipError_t launch_mx4_quant(bool by_columns, const Mx4QuantArgs &a, int64_t units, hipStream_t stream);
+
+struct Mx4DequantArgs {
+    const char *Q; int64_t q_es, q_rs;
+    const char *S; int64_t s_es, s_rs, s_cs;
+    char *Y; int64_t y_es, y_rs, y_cs;         // [E][M][K]
+    int y_kind;
+    int M, K, E;
+    int chunks;
+    uint32_t chunk_mul;
+    int vec;                                   // rows of Y are contiguous
+};
+hipError_t launch_mx4_dequant(const Mx4DequantArgs &a, int64_t units, hipStream_t stream);
+
+// ---------------------------------------------------------------- products (mx4_gemm.hip)
+
+// C[m][n] = act(sum over k of A[m][k] W[n][k]), both in MXFP4.
+struct Mx4GemmArgs {
+    const char *A; int64_t a_rs;               // [M][row_bytes]
+    const char *SA; int64_t sa_rs, sa_cs;      // [M][blocks]
+    const char *Q; int64_t q_rs, q_es;         // [E][N][row_bytes]
+    const char *S; int64_t s_rs, s_cs, s_es;   // [E][N][blocks]
+    char *C; int64_t c_rs, c_cs;
+    int out_kind, act;
+    int vec4;                                  // rows of C are contiguous
+    int M, N;
+    int row_bytes, blocks;                     // ceil(K / 2), ceil(K / 32)
+    const char *offsets; int64_t o_s; int E;   // offsets null: one group of all M rows
+    int tiles_n, ktiles;
+    int group_m;
+    int units;                                 // workgroups of the grid
+    int splits, kt_per_split;                  // K in pieces (one matrix only)
+    float *ws; int *counters;
+};
+
+// Tiles of the products.
+enum Mx4Tile : int { MX4_T256 = 0, MX4_T128 = 1, MX4_T64 = 2, NUM_MX4_TILES = 3 };
+constexpr int mx4_tile_m(int t) { return t == MX4_T256 ? 256 : t == MX4_T128 ? 128 : 64; }
+constexpr int mx4_tile_n(int t) { return t == MX4_T256 ? 256 : t == MX4_T128 ? 128 : 64; }
+
+// Loads of the products.
+//  MX4_DIRECT: codes from memory to LDS: rows begin at multiples of 4 bytes; scale bytes
+//              adjacent, 8 of a row at least.
+//  MX4_BYTES : codes through registers, 16 bytes at any alignment; scales as above.
+//  MX4_ANY   : the same with scales byte by byte.
+enum Mx4Load : int { MX4_DIRECT = 0, MX4_BYTES = 1, MX4_ANY = 2 };
+hipError_t launch_mx4_gemm(int tile, int load, const Mx4GemmArgs &a, int64_t units, hipStream_t stream);
+
+}  // namespace dg

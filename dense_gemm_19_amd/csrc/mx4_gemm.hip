@@ -1,0 +1,378 @@
+// mx4_gemm.hip -- products of two microscaled 4-bit (MXFP4) operands, for one matrix or
+// for the experts of a mixture:
+//
+//   C[m][n] = act(sum over blocks b of 32 k's of 2^(sa[m][b] + s[n][b] - 254) * sum over k in b of a[m][k] w[n][k])
+//
+// gfx950 multiplies the format as it is: one v_mfma_scale_f32_32x32x64_f8f6f4 takes 32
+// rows of each operand x 64 elements of K and a scale byte for each row and block, and
+// adds into FP32.  (Register-only loops on this part: 7.9 PFLOP/s; the 16x16x128 form
+// 4.2.)
+#include "bytes.hpp"
+#include "device_common.hpp"
+#include "gemm_dtl.hpp"
+#include "moe_slot.hpp"
+#include "mx4.hpp"
+
+namespace dg {
+namespace {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr int KB = 128;          // bytes of K in a tile: 256 elements, 8 blocks
+
+// 16 bytes from `at` on of a row of `bytes`, zeros past its end.
+__device__ __forceinline__ u32x4 row_chunk(const char *row, int at, int bytes) {
+    const int n = bytes - at;
+    if (n >= 16) return *reinterpret_cast<const u32x4_any *>(row + at);
+    if (n <= 0) return u32x4{0u, 0u, 0u, 0u};
+    if (bytes >= 16) return down_bytes(*reinterpret_cast<const u32x4_any *>(row + bytes - 16), 16 - n);
+    return load_part<1>(row + at, 1, n);
+}
+
+// The first n (1 to 15) bytes of v, zeros above.
+__device__ __forceinline__ u32x4 first_bytes(u32x4 v, int n) {
+    uint64_t lo = v[0] | (uint64_t)v[1] << 32, hi = v[2] | (uint64_t)v[3] << 32;
+    if (n < 8) lo &= ((uint64_t)1 << (8 * n)) - 1;
+    hi = n > 8 ? hi & (((uint64_t)1 << (8 * (n - 8))) - 1) : 0;
+    return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
+
+// The scale bytes of 8 blocks from `at` on of a row of `blocks`, zeros past its end: the
+// codes read there, whatever they are, then count 2^-254 times at most 36, nothing.
+// RUN: bytes adjacent, 8 of them at least: loaded from 8 before the row's end at the
+// latest, and moved down when they are used.
+template <bool RUN>
+__device__ __forceinline__ u32x2 load_scales(const char *row, int64_t stride, int at, int blocks) {
+    if constexpr (RUN) {
+        return *reinterpret_cast<const u32x2_byte *>(row + min(at, blocks - 8));
+    } else {
+        row += at * stride;
+        uint32_t v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            v[j] = 0;
+            if (at + j < blocks) v[j] = *reinterpret_cast<const uint8_t *>(row + j * stride);
+        }
+        return u32x2{v[0] | v[1] << 8 | v[2] << 16 | v[3] << 24, v[4] | v[5] << 8 | v[6] << 16 | v[7] << 24};
+    }
+}
+template <bool RUN>
+__device__ __forceinline__ u32x2 place_scales(u32x2 v, int at, int blocks) {
+    if constexpr (RUN) {
+        const uint64_t w = (v[0] | (uint64_t)v[1] << 32) >> (8 * max(at + 8 - blocks, 0));
+        return u32x2{(uint32_t)w, (uint32_t)(w >> 32)};
+    }
+    return v;
+}
+
+// One block column of the matrix cores: 64 elements of K (two blocks, of the lanes below
+// 32 and of the others), scale byte STEP of each lane's word.
+template <int STEP>
+__device__ __forceinline__ f32x16 mfma(u32x4 a, uint32_t sa, u32x4 b, uint32_t sb, f32x16 c) {
+    const i32x8 x = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0}, y = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, STEP, (int)sa, STEP, (int)sb);
+}
+
+// One operand's K tile: R rows x 128 bytes, 16-byte chunks XOR-swizzled by their row
+// (dtl::kmaj_off), so that the rows that a fragment read touches fall on distinct banks.
+template <int R, int NW>
+struct TileIO {
+    static constexpr int INSTS = R * 8 / 64 / NW;   // load-to-LDS instructions of a wave
+    static constexpr int CHUNKS = R * 8 / (64 * NW);   // chunks of a thread
+    struct Src { uint32_t off[INSTS]; };
+    // rows past `lim` read the last one (their results are not stored)
+    __device__ static Src sources(int64_t rs, int r0, int lim, int wave, int lane) {
+        Src s;
+#pragma unroll
+        for (int j = 0; j < INSTS; ++j) {
+            const int pos = (wave + NW * j) * 64 + lane, row = pos >> 3;
+            s.off[j] = (uint32_t)min(row, lim - 1 - r0) * (uint32_t)rs + (((pos & 7) ^ (row & 7)) << 4);
+        }
+        return s;
+    }
+    __device__ static void issue(uint32_t lds, const Src &s, const char *base, int wave_u) {
+#pragma unroll
+        for (int j = 0; j < INSTS; ++j) dtl::lds_load16(base, s.off[j], lds + (uint32_t)((wave_u + NW * j) * 1024));
+    }
+    // through registers, at any alignment
+    __device__ static void load(u32x4 (&reg)[CHUNKS], const char *base, int64_t rs, int r0, int lim, int at, int bytes, int tid) {
+#pragma unroll
+        for (int i = 0; i < CHUNKS; ++i) {
+            const int pos = tid + i * 64 * NW, row = pos >> 3;
+            reg[i] = row_chunk(base + (int64_t)min(row, lim - 1 - r0) * rs, at + (((pos & 7) ^ (row & 7)) << 4), bytes);
+        }
+    }
+    __device__ static void store(char *lds, const u32x4 (&reg)[CHUNKS], int tid) {
+#pragma unroll
+        for (int i = 0; i < CHUNKS; ++i) *reinterpret_cast<u32x4 *>(lds + (tid + i * 64 * NW) * 16) = reg[i];
+    }
+};
+
+// BM x BN tiles, waves WGM x WGN, a two-stage LDS ring.  DIRECT: rows begin at multiples
+// of 4 bytes and codes go from memory to LDS by load-to-LDS instructions; else through
+// registers.  RUN: see row_scales.
+// K order within a tile: lanes 0-31 take blocks 0-3 and lanes 32-63 blocks 4-7, one at
+// each of the four steps, so that a row's four scale bytes of a lane are one word and
+// the step picks the byte.
+// A ragged K, DIRECT: chunks past the end of a row read the next row, or for the last row its
+// end again.  Whole blocks past the end have scale bytes of zero; of the last block the
+// codes past the end are cleared in W's tile, and the last rows' are moved to where they
+// belong in both.
+template <int BM, int BN, int WGM, int WGN, bool DIRECT, bool RUN, bool SPLIT>
+__global__ void __launch_bounds__(64 * WGM * WGN) mx4_tile(Mx4GemmArgs a) {
+    constexpr int NW = WGM * WGN, NT = 64 * NW, WTM = BM / WGM, WTN = BN / WGN, TM = WTM / 32, TN = WTN / 32;
+    constexpr int A_BYTES = BM * KB, B_BYTES = BN * KB, SA_OFF = A_BYTES + B_BYTES, SB_OFF = SA_OFF + BM * 8, STAGE = SB_OFF + BN * 8;
+    constexpr int SROWS = (BM + BN + NT - 1) / NT;  // scale rows of a thread
+    using AIO = TileIO<BM, NW>;
+    using BIO = TileIO<BN, NW>;
+    static_assert((BM + BN) % NT == 0 || BM + BN < NT, "whole scale rows");
+    static_assert(2 * STAGE <= 160 * 1024 - 64, "LDS");
+    __shared__ __attribute__((aligned(16))) char ring[2 * STAGE];
+    __shared__ int is_last;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wave_u = __builtin_amdgcn_readfirstlane(wave);
+    const int wm = wave / WGN, wn = wave % WGN, l = lane & 31, h = lane >> 5;
+
+    int e = 0, begin = 0, M = a.M, t, z = 0, ktiles = a.ktiles;
+    if (a.offsets) {
+        moe::Slot s;
+        if (!moe::find_slot<BM>(a.offsets, a.o_s, a.E, a.M, a.tiles_n, a.units, blockIdx.x, s)) return;
+        e = s.e; begin = s.begin; M = s.rows; t = s.unit;
+        if (e == a.E) e = 0, ktiles = 0;           // rows of no expert: zero
+    } else {
+        t = moe::xcd_run(blockIdx.x, a.units);
+        if (SPLIT) {
+            const int u = t / a.splits;
+            z = t - u * a.splits;
+            t = u;
+        }
+    }
+    int tm, tn;
+    dtl::raster(t, (M + BM - 1) / BM, a.tiles_n, a.group_m, tm, tn);
+    const int m0 = tm * BM, n0 = tn * BN, N = a.N;
+    const int kt0 = SPLIT ? z * a.kt_per_split : 0, kt1 = SPLIT ? min(kt0 + a.kt_per_split, ktiles) : ktiles;
+
+    const char *pa = a.A + (int64_t)(begin + m0) * a.a_rs, *pb = a.Q + (int64_t)e * a.q_es + (int64_t)n0 * a.q_rs;
+    const char *psa = a.SA + (int64_t)(begin + m0) * a.sa_rs, *psb = a.S + (int64_t)e * a.s_es + (int64_t)n0 * a.s_rs;
+    const uint32_t ring_lds = dtl::lds_addr(ring);
+    typename AIO::Src a_src;
+    typename BIO::Src b_src;
+    if (DIRECT) {
+        a_src = AIO::sources(a.a_rs, m0, M, wave, lane);
+        b_src = BIO::sources(a.q_rs, n0, N, wave, lane);
+    }
+    u32x4 ra[DIRECT ? 1 : AIO::CHUNKS], rb[DIRECT ? 1 : BIO::CHUNKS];
+    // this thread's rows of scales: A's, then W's
+    const char *srow[SROWS];
+    int64_t scol[SROWS];
+    u32x2 rs[SROWS];
+#pragma unroll
+    for (int i = 0; i < SROWS; ++i) {
+        const int r = min(tid + i * NT, BM + BN - 1);
+        const bool is_a = r < BM;
+        srow[i] = is_a ? psa + (int64_t)min(r, M - 1 - m0) * a.sa_rs : psb + (int64_t)min(r - BM, N - 1 - n0) * a.s_rs;
+        scol[i] = is_a ? a.sa_cs : a.s_cs;
+    }
+    auto fetch_scales = [&](int kt) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < SROWS; ++i) rs[i] = load_scales<RUN>(srow[i], scol[i], kt * 8, a.blocks);
+    };
+    auto fetch = [&](int stage, int kt) __attribute__((always_inline)) {
+        fetch_scales(kt);
+        if constexpr (DIRECT) {
+            const uint32_t st = ring_lds + (uint32_t)(stage * STAGE);
+            AIO::issue(st, a_src, pa + kt * KB, wave_u);
+            BIO::issue(st + A_BYTES, b_src, pb + kt * KB, wave_u);
+        } else {
+            AIO::load(ra, pa, a.a_rs, m0, M, kt * KB, a.row_bytes, tid);
+            BIO::load(rb, pb, a.q_rs, n0, N, kt * KB, a.row_bytes, tid);
+        }
+    };
+    // The ragged last tile, DIRECT: chunks begin at row_bytes - 16 at the latest in the
+    // last rows, and anywhere up to the row's end in the others, whose next row is there.
+    auto fetch_ragged = [&](int stage, int kt) __attribute__((always_inline)) {
+        fetch_scales(kt);
+        const uint32_t st = ring_lds + (uint32_t)(stage * STAGE);
+        auto issue = [&](auto io, uint32_t lds, const char *base, int64_t stride, int r0, int lim) __attribute__((always_inline)) {
+#pragma unroll 1
+            for (int j = 0; j < decltype(io)::INSTS; ++j) {
+                const int pos = (wave + NW * j) * 64 + lane, row = min(pos >> 3, lim - 1 - r0);
+                const int at = kt * KB + (((pos & 7) ^ ((pos >> 3) & 7)) << 4);
+                const int most = row == lim - 1 - r0 ? a.row_bytes - 16 : (a.row_bytes - 1) & ~15;
+                dtl::lds_load16(base, (uint32_t)row * (uint32_t)stride + (uint32_t)min(at, most), lds + (uint32_t)((wave_u + NW * j) * 1024));
+            }
+        };
+        issue(AIO(), st, pa, a.a_rs, m0, M);
+        issue(BIO(), st + A_BYTES, pb, a.q_rs, n0, N);
+    };
+    auto put = [&](int stage, int kt) __attribute__((always_inline)) {
+        char *st = ring + stage * STAGE;
+#pragma unroll
+        for (int i = 0; i < SROWS; ++i)
+            if (NT * SROWS == BM + BN || tid + i * NT < BM + BN)
+                *reinterpret_cast<u32x2 *>(st + SA_OFF + (tid + i * NT) * 8) = place_scales<RUN>(rs[i], kt * 8, a.blocks);
+        if constexpr (!DIRECT) {
+            AIO::store(st, ra, tid);
+            BIO::store(st + A_BYTES, rb, tid);
+        }
+    };
+    // The last chunks of a ragged last tile, DIRECT: see above.
+    auto mend = [&](int stage, int kt) __attribute__((always_inline)) {
+        const int left = a.row_bytes - kt * KB, n = left & 15;
+        if (n == 0) return;
+#pragma unroll 1
+        for (int r = tid; r < BM + BN; r += NT) {
+            const bool is_a = r < BM, last = is_a ? m0 + r >= M - 1 : n0 + r - BM >= N - 1;
+            if (is_a && !last) continue;
+            u32x4 *p = reinterpret_cast<u32x4 *>(ring + stage * STAGE + (is_a ? 0 : A_BYTES) + dtl::kmaj_off(is_a ? r : r - BM, left >> 4));
+            const u32x4 v = *p;
+            *p = last ? down_bytes(v, 16 - n) : first_bytes(v, n);
+        }
+    };
+
+    f32x16 acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+    auto compute = [&](int stage) __attribute__((always_inline)) {
+        const char *st = ring + stage * STAGE, *la = st + (wm * WTM + l) * KB, *lb = st + A_BYTES + (wn * WTN + l) * KB;
+        uint32_t sa[TM], sb[TN];
+#pragma unroll
+        for (int i = 0; i < TM; ++i) sa[i] = *reinterpret_cast<const uint32_t *>(st + SA_OFF + (wm * WTM + 32 * i + l) * 8 + 4 * h);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) sb[j] = *reinterpret_cast<const uint32_t *>(st + SB_OFF + (wn * WTN + 32 * j + l) * 8 + 4 * h);
+        // fragments are read a step ahead of their use
+        u32x4 fa[2][TM], fb[2][TN];
+        auto read = [&](int s) __attribute__((always_inline)) {
+            const int at = ((4 * h + s) ^ (l & 7)) << 4;
+#pragma unroll
+            for (int i = 0; i < TM; ++i) fa[s & 1][i] = *reinterpret_cast<const u32x4 *>(la + 32 * i * KB + at);
+#pragma unroll
+            for (int j = 0; j < TN; ++j) fb[s & 1][j] = *reinterpret_cast<const u32x4 *>(lb + 32 * j * KB + at);
+        };
+        auto step = [&](auto s) __attribute__((always_inline)) {
+            constexpr int STEP = decltype(s)::value;
+            if (STEP < 3) read(STEP + 1);
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) acc[i][j] = mfma<STEP>(fb[STEP & 1][j], sb[j], fa[STEP & 1][i], sa[i], acc[i][j]);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        read(0);
+        step(std::integral_constant<int, 0>());
+        step(std::integral_constant<int, 1>());
+        step(std::integral_constant<int, 2>());
+        step(std::integral_constant<int, 3>());
+    };
+
+    // tile kt is in LDS, tile kt - 1 has been read
+    auto arrive = [&]() __attribute__((always_inline)) { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+    if (kt0 < kt1) {
+        const bool ragged = DIRECT && kt1 * KB > a.row_bytes;   // the last tile
+        const int full = kt1 - (ragged ? 1 : 0);
+        if (kt0 < full) fetch(kt0 & 1, kt0);
+        else fetch_ragged(kt0 & 1, kt0);
+        put(kt0 & 1, kt0);
+        int kt = kt0;
+        for (; kt + 1 < full; ++kt) {
+            arrive();
+            fetch((kt & 1) ^ 1, kt + 1);
+            compute(kt & 1);
+            put((kt & 1) ^ 1, kt + 1);
+        }
+        if (ragged) {
+            if (kt < full) {
+                arrive();
+                fetch_ragged((kt & 1) ^ 1, kt + 1);
+                compute(kt & 1);
+                put((kt & 1) ^ 1, kt + 1);
+                ++kt;
+            }
+            arrive();
+            mend(kt & 1, kt);
+        }
+        arrive();
+        compute(kt & 1);
+    }
+
+    if constexpr (SPLIT) {
+        // [tile][piece][element][thread]: every thread adds its own elements, in the order of K
+        const int S = a.splits;
+        float *part = a.ws + (int64_t)t * S * (BM * BN) + tid;
+        auto at = [&](int q, int i, int j, int r) __attribute__((always_inline)) { return part + (int64_t)q * (BM * BN) + ((i * TN + j) * 16 + r) * NT; };
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) __hip_atomic_store(at(z, i, j, r), acc[i][j][r], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+        if (tid == 0) is_last = take_last_ticket(a.counters + t, S);
+        __syncthreads();
+        if (!is_last) return;
+#pragma unroll 1
+        for (int q = 0; q < S; ++q) {
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    float v[16];
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) v[r] = __hip_atomic_load(at(q, i, j, r), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) acc[i][j][r] = q == 0 ? v[r] : acc[i][j][r] + v[r];
+                }
+        }
+        if (tid == 0) __hip_atomic_store(a.counters + t, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    // a lane holds row l and 4 adjacent columns, four times, of each 32 x 32 block
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        const int m = m0 + wm * WTM + 32 * i + l;
+        if (m >= M) continue;
+        char *row = a.C + (int64_t)(begin + m) * a.c_rs;
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int n = n0 + wn * WTN + 32 * j + 8 * q + 4 * h;
+                float v[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[r] = activate(a.act, acc[i][j][4 * q + r]);
+                if (a.vec4 && n + 3 < N) {
+                    store_out4(row + (int64_t)n * a.c_cs, a.out_kind, v);
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (n + r < N) store_out(row + (int64_t)(n + r) * a.c_cs, a.out_kind, v[r]);
+                }
+            }
+    }
+}
+
+}  // namespace
+
+hipError_t launch_mx4_gemm(int tile, int load, const Mx4GemmArgs &a, int64_t units, hipStream_t s) {
+#define DG_TILE(B, GM, GN, D, R, S) hipLaunchKernelGGL((mx4_tile<B, B, GM, GN, D, R, S>), dim3((unsigned)units), dim3(64 * GM * GN), 0, s, a)
+#define DG_SPLITS(B, D, R)                              \
+    do {                                                \
+        if (a.splits > 1) DG_TILE(B, 2, 2, D, R, true); \
+        else DG_TILE(B, 2, 2, D, R, false);             \
+    } while (0)
+    if (tile == MX4_T256 && load == MX4_DIRECT && a.splits <= 1) DG_TILE(256, 2, 4, true, true, false);
+    else if (tile == MX4_T128 && load == MX4_DIRECT) DG_SPLITS(128, true, true);
+    else if (tile == MX4_T128 && load == MX4_BYTES) DG_SPLITS(128, false, true);
+    else if (tile == MX4_T64 && load == MX4_DIRECT) DG_SPLITS(64, true, true);
+    else if (tile == MX4_T64 && load == MX4_BYTES) DG_SPLITS(64, false, true);
+    else if (tile == MX4_T64 && load == MX4_ANY) DG_SPLITS(64, false, false);
+    else return hipErrorInvalidValue;
+#undef DG_SPLITS
+#undef DG_TILE
+    return hipGetLastError();
+}
+
+}  // namespace dg

@@ -1,4 +1,4 @@
-// torch_bind.cpp -- the quick Python binding of the mixture-of-experts and 4-bit
+// torch_bind.cpp -- the quick Python binding of the mixture-of-experts, 4-bit and MXFP4
 // entry points: tensors become dg_views on the C++ side, the stream is torch's
 // current one unless given.  A decoding step makes many calls of a few
 // microseconds each; describing five tensors through ctypes costs 7 us of host
@@ -197,6 +197,50 @@ PyObject *moe_w4(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+PyObject *quant_mx4(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        Arg X, Q, S;
+        int32_t mode;
+        hipStream_t s;
+        if (!count(n, 5) || !X.set(a[0]) || !Q.set(a[1]) || !S.set(a[2]) || !to_int(a[3], &mode) || !to_stream(a[4], &s))
+            return nullptr;
+        return status([&] { return dg_quant_mx4(X.p, Q.p, S.p, (dg_mx4_mode)mode, s); });
+    });
+}
+
+PyObject *dequant_mx4(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        Arg Q, S, Y;
+        hipStream_t s;
+        if (!count(n, 4) || !Q.set(a[0]) || !S.set(a[1]) || !Y.set(a[2]) || !to_stream(a[3], &s)) return nullptr;
+        return status([&] { return dg_dequant_mx4(Q.p, S.p, Y.p, s); });
+    });
+}
+
+PyObject *mx4(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        Arg A, SA, Q, S, C;
+        int32_t act;
+        hipStream_t s;
+        if (!count(n, 7) || !A.set(a[0]) || !SA.set(a[1]) || !Q.set(a[2]) || !S.set(a[3]) || !C.set(a[4]) ||
+            !to_int(a[5], &act) || !to_stream(a[6], &s))
+            return nullptr;
+        return status([&] { return dg_gemm_mx4(A.p, SA.p, Q.p, S.p, C.p, (dg_act)act, s); });
+    });
+}
+
+PyObject *moe_mx4(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        Arg A, SA, off, Q, S, C;
+        int32_t act;
+        hipStream_t s;
+        if (!count(n, 8) || !A.set(a[0]) || !SA.set(a[1]) || !off.set(a[2]) || !Q.set(a[3]) || !S.set(a[4]) ||
+            !C.set(a[5]) || !to_int(a[6], &act) || !to_stream(a[7], &s))
+            return nullptr;
+        return status([&] { return dg_moe_gemm_mx4(A.p, SA.p, off.p, Q.p, S.p, C.p, (dg_act)act, s); });
+    });
+}
+
 // The view of a tensor as bytes (the layout of dg_view), for tests.
 PyObject *view(PyObject *, PyObject *o) {
     return guarded([&]() -> PyObject * {
@@ -211,7 +255,8 @@ PyObject *view(PyObject *, PyObject *o) {
 PyMethodDef methods[] = {
     DG_FAST("moe_sort", sort), DG_FAST("moe_gather", gather), DG_FAST("moe_combine", combine),
     DG_FAST("moe_combine_grad", combine_grad), DG_FAST("moe_gemm", gemm), DG_FAST("moe_gemm_wgrad", gemm_wgrad),
-    DG_FAST("gemm_w4", w4), DG_FAST("moe_gemm_w4", moe_w4), {"view", view, METH_O, nullptr},
+    DG_FAST("gemm_w4", w4), DG_FAST("moe_gemm_w4", moe_w4), DG_FAST("quant_mx4", quant_mx4),
+    DG_FAST("dequant_mx4", dequant_mx4), DG_FAST("gemm_mx4", mx4), DG_FAST("moe_gemm_mx4", moe_mx4), {"view", view, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_dgtorch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,24 @@
+// w4_mx.hip -- products of 16-bit activations with microscaled 4-bit weights (E2M1
+// codes, an E8M0 scale byte for 32 of them): the kernels of w4.hpp with that decoding.
+#include "w4.hpp"
+
+namespace dg {
+namespace {
+
+template <int IN>
+hipError_t launch(int tm, const W4Args &a, int64_t units, hipStream_t s) {
+    switch (tm) {
+    case 1: return launch_t<IN, 1, 4, 1>(a, units, s);
+    case 2: return launch_t<IN, 2, 4, 1>(a, units, s);
+    case 3: return launch_t<IN, 3, 4, 1>(a, units, s);
+    }
+    return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+hipError_t launch_w4_mx(int in_kind, int tm, const W4Args &a, int64_t units, hipStream_t s) {
+    return in_kind == IN_BF16 ? launch<IN_BF16>(tm, a, units, s) : launch<IN_F16>(tm, a, units, s);
+}
+
+}  // namespace dg

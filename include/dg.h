@@ -72,7 +72,7 @@ typedef enum {
     DG_F8E4M3 = 3,  /* OCP E4M3FN: bias 7, 3 mantissa bits, max 448, no Inf */
     DG_I32 = 4,     /* 32-bit integers (expert ids, offsets and places) */
     DG_I64 = 5,     /* 64-bit integers (expert ids) */
-    DG_U8 = 6       /* bytes (two 4-bit codes each, or zero points) */
+    DG_U8 = 6       /* bytes (two 4-bit codes each, zero points, or scales of 4-bit codes) */
 } dg_dtype;
 
 typedef enum {
@@ -421,7 +421,7 @@ dg_status dg_moe_sort(const dg_view *ids, int32_t E, const dg_view *offsets, con
                       const dg_view *pos, hipStream_t stream);
 
 /* Xs[r] <- X[order[r] / k], a row of zeros where order[r] is outside 0 .. T*k - 1.
- *   X [T][H], Xs [n][H]: one dtype (DG_F32, DG_F16, DG_BF16 or DG_F8E4M3), any
+ *   X [T][H], Xs [n][H]: one dtype (DG_F32, DG_F16, DG_BF16, DG_F8E4M3 or DG_U8), any
  *   strides; order [n] DG_I32, any stride; k >= 1.
  * The gradient with respect to X is dg_moe_combine of dXs without weights.
  * Errors: DG_ERR_INVALID_ARG (k), DG_ERR_DTYPE, DG_ERR_SHAPE_MISMATCH,
@@ -510,6 +510,81 @@ dg_status dg_gemm_w4_plan(const dg_view *A, const dg_view *Q, const dg_view *S, 
                           int32_t group, char *buf, size_t len);
 dg_status dg_moe_gemm_w4_plan(const dg_view *A, const dg_view *offsets, const dg_view *Q, const dg_view *S,
                               const dg_view *Z, const dg_view *C, int32_t group, char *buf, size_t len);
+
+/*
+ * Microscaled 4-bit operands (MXFP4 of the OCP Microscaling Formats specification,
+ * v1.0), which gfx950's matrix cores multiply as they are.  (The pages name no 4-bit
+ * format; block scales applied inside the product are those of sheratonhq.com deep
+ * dive, section 2.4.)
+ *
+ * A matrix [rows][K] is codes and scales:
+ *   codes  [rows][ceil(K / 2)] DG_U8, rows contiguous: element k in the low (k even) or
+ *          high (k odd) half of byte k / 2, E2M1: a sign bit above the number of one of
+ *          0, .5, 1, 1.5, 2, 3, 4, 6.
+ *   scales [rows][ceil(K / 32)] DG_U8, any strides: for 32 elements along K a byte b,
+ *          2^(b - 127); 255 makes them NaN.
+ * Where K is odd the last byte's high half stands for no element and must be zero, as
+ * dg_quant_mx4 writes it.
+ * Conventions as for the GEMM entry points (asynchronous on `stream`, outputs untouched
+ * on error, results bitwise reproducible); every call may be captured in a HIP graph.
+ * Extents are at most 2^31 - 4096 where no tighter limit is given: DG_ERR_OVERFLOW
+ * above.
+ */
+
+/* Quantise X.  For each block of 32 elements along K, of largest size a:
+ *   DG_MX4_FLOOR  e = floor(log2 a) - 2, the specification's choice: sizes above
+ *                 6 * 2^e become 6 * 2^e;
+ *   DG_MX4_CEIL   e the least with a <= 6 * 2^e: nothing saturates;
+ *   b = max(e + 127, 0), and each code is the number nearest to x / 2^(b - 127), ties
+ *   to the even code; the sign of a zero is kept.  A block of zeros has b = 0.  A block
+ *   that holds a NaN or an infinity has b = 255 and codes of zero.
+ *   X  [M][K] DG_F32, DG_F16 or DG_BF16, any strides: the transpose that a gradient sums
+ *      over is a view.  Quickest where its rows or its columns are contiguous.
+ *   Q  codes, S scales (written).
+ * X, Q and S are matrices, or 3-D stacks of as many each (the experts' weights).
+ * Errors: DG_ERR_INVALID_ARG (mode), DG_ERR_DTYPE, DG_ERR_SHAPE_MISMATCH,
+ * DG_ERR_UNSUPPORTED_VIEW (Q's rows not contiguous), DG_ERR_STRIDE / DG_ERR_ALIAS (Q or S
+ * overlaps itself or another view), DG_ERR_OVERFLOW (also: a launch of 2^32 threads, from
+ * 2^37 elements on), view errors. */
+typedef enum { DG_MX4_FLOOR = 0, DG_MX4_CEIL = 1 } dg_mx4_mode;
+
+dg_status dg_quant_mx4(const dg_view *X, const dg_view *Q, const dg_view *S, dg_mx4_mode mode, hipStream_t stream);
+
+/* Y <- the numbers that codes and scales stand for, rounded once to Y's dtype (exact in
+ * DG_F32, but 4 and 6 times 2^126 or 2^127, which are infinite where they pass its range;
+ * exact in DG_BF16 and DG_F16 within theirs).
+ *   Q, S as written by dg_quant_mx4; Y [M][K] DG_F32, DG_F16 or DG_BF16, any strides
+ *   (written); matrices or 3-D stacks.
+ * Errors as for dg_quant_mx4. */
+dg_status dg_dequant_mx4(const dg_view *Q, const dg_view *S, const dg_view *Y, hipStream_t stream);
+
+/* C <- act(A * W^T), W [N][K] in MXFP4 (codes Q, scales S).
+ *   A  codes [M][ceil(K / 2)] DG_U8 with scales SA [M][ceil(K / 32)], or [M][K] DG_F16 or
+ *      DG_BF16, K-contiguous, with SA NULL.
+ *   C  [M][N] DG_F32, DG_F16 or DG_BF16.  act: a dg_act value.
+ * FP32 accumulation, one rounding to C's dtype.  No operand is rounded.
+ * Training: with Y = X W^T, dX = dY W is the product of dY and of W's transpose, both
+ * quantised along N, and dW = dY^T X that of both transposes quantised along the rows.
+ * Codes are quickest where their rows begin at multiples of 4 bytes; 16-bit A where its
+ * layout is dg_gemm_w4's quickest one.
+ * Errors: DG_ERR_NULL (codes without SA), DG_ERR_INVALID_ARG (SA with a 16-bit A, act),
+ * DG_ERR_DTYPE, DG_ERR_SHAPE_MISMATCH, DG_ERR_UNSUPPORTED_VIEW (A's or Q's rows not
+ * contiguous), DG_ERR_STRIDE, DG_ERR_ALIAS, DG_ERR_OVERFLOW (16-bit A: K above 2^20, row
+ * strides of 32 MiB or more; launches of 2^32 threads), view errors. */
+dg_status dg_gemm_mx4(const dg_view *A, const dg_view *SA, const dg_view *Q, const dg_view *S, const dg_view *C,
+                      dg_act act, hipStream_t stream);
+
+/* The same for the experts of a mixture: C[r] <- act(A[r] * W[e]^T) with Q
+ * [E][N][ceil(K / 2)], S [E][N][ceil(K / 32)] and rows as in dg_moe_gemm.  Tokens may be
+ * quantised once and their codes and scales gathered by dg_moe_gather. */
+dg_status dg_moe_gemm_mx4(const dg_view *A, const dg_view *SA, const dg_view *offsets, const dg_view *Q,
+                          const dg_view *S, const dg_view *C, dg_act act, hipStream_t stream);
+
+/* What these calls would run, as dg_gemm_w4_plan does. */
+dg_status dg_gemm_mx4_plan(const dg_view *A, const dg_view *SA, const dg_view *Q, const dg_view *S, const dg_view *C,
+                           char *buf, size_t len);
+dg_status dg_moe_gemm_mx4_plan(const dg_view *A, const dg_view *SA, const dg_view *offsets, const dg_view *Q,
+                               const dg_view *S, const dg_view *C, char *buf, size_t len);
 
 /* Helper (no page passage): static, human-readable name of a status code
  * ("DG_ERR_ALIAS", ...); "DG_ERR_UNKNOWN" for a value outside dg_status. */
