@@ -3,6 +3,7 @@
 #include <hip/hip_runtime_api.h>
 
 #include <cmath>
+#include <cstdlib>
 
 #include "entry.hpp"
 #include "moe.hpp"
@@ -126,6 +127,9 @@ dg_status codes_product(const Mat &x, const Mat &sx, const Mat &off, const Stack
         return reinterpret_cast<uintptr_t>(m.ptr) % 4 == 0 && es % 4 == 0 &&
                (m.rows <= 1 || (m.rs % 4 == 0 && m.rs >= bytes && m.rs < ((int64_t)1 << 23)));
     };
+    auto pieces = [&](const Mat &m, int64_t es) {
+        return reinterpret_cast<uintptr_t>(m.ptr) % 16 == 0 && es % 16 == 0 && (m.rows <= 1 || (m.rs % 16 == 0 && m.rs < ((int64_t)1 << 23)));
+    };
     int load = MX4_ANY;
     if (a.sa_cs == 1 && a.s_cs == 1 && a.blocks >= 8) load = words(x, 0) && words(q.one, q.E > 1 ? q.es : 0) ? MX4_DIRECT : MX4_BYTES;
     const int64_t used = experts ? std::min(q.E, M) : 1, mean = M / used;
@@ -136,6 +140,9 @@ dg_status codes_product(const Mat &x, const Mat &sx, const Mat &off, const Stack
     int tile = MX4_T64;
     if (load == MX4_DIRECT && mean > 128 && expected(MX4_T256) >= d.cus) tile = MX4_T256;
     else if (load != MX4_ANY && mean > 64 && expected(MX4_T128) >= d.cus / 2) tile = MX4_T128;
+    const int64_t q_es = q.E > 1 ? q.es : 0, s_es = q.E > 1 ? s.es : 0;
+    const bool ring = tile != MX4_T64 && bytes % 256 == 0 && a.sa_cs == 1 && a.s_cs == 1 && pieces(x, 0) && pieces(q.one, q_es) && pieces(sx, 0) &&
+                      pieces(s.one, s_es);
     const int64_t bm = mx4_tile_m(tile), bn = mx4_tile_n(tile);
     a.tiles_n = (int)cdiv(N, bn);
     a.group_m = tile == MX4_T256 ? 4 : 8;
@@ -143,14 +150,14 @@ dg_status codes_product(const Mat &x, const Mat &sx, const Mat &off, const Stack
     // K in pieces where the tiles leave most of the device idle; a captured call runs
     // whole: the pieces' workspace may have to be allocated.
     int64_t splits = 1;
-    if (!experts && tile != MX4_T256 && 2 * units <= d.cus && a.ktiles >= 4 && !capturing(stream, r))
+    if (!experts && !ring && tile != MX4_T256 && 2 * units <= d.cus && a.ktiles >= 4 && !capturing(stream, r))
         splits = std::min<int64_t>(d.cus / units, a.ktiles / 2);
     a.kt_per_split = (int)cdiv(std::max(a.ktiles, 1), splits);
     a.splits = (int)cdiv(std::max(a.ktiles, 1), a.kt_per_split);
     if (units > INT32_MAX / a.splits || !fits_a_launch(units * a.splits, 512)) return DG_ERR_OVERFLOW;
     a.units = (int)(units * a.splits);
     if (r)
-        return r->say("%s loads, %dx%d tiles, K in %d pieces, %d workgroups", load == MX4_DIRECT ? "direct" : load == MX4_BYTES ? "vector" : "element", (int)bm, (int)bn, a.splits, a.units);
+        return r->say("%s loads, %dx%d tiles, K in %d pieces, %d workgroups", ring ? "ring" : load == MX4_DIRECT ? "direct" : load == MX4_BYTES ? "vector" : "element", (int)bm, (int)bn, a.splits, a.units);
     WsLease lease;
     if (a.splits > 1) {
         if (lease_workspace(stream, (size_t)units * a.splits * bm * bn * sizeof(float), (size_t)units, &lease) != hipSuccess) {
@@ -160,7 +167,7 @@ dg_status codes_product(const Mat &x, const Mat &sx, const Mat &off, const Stack
         a.ws = lease.ws;
         a.counters = lease.counters;
     }
-    return done(launch_mx4_gemm(tile, load, a, a.units, stream), stream);
+    return done(ring ? launch_mx4_ring(tile, a, a.units, stream) : launch_mx4_gemm(tile, load, a, a.units, stream), stream);
 }
 
 dg_status gemm_entry(const dg_view *A, const dg_view *SA, const dg_view *offsets, const dg_view *Q, const dg_view *S,

@@ -80,4 +80,8 @@ constexpr int mx4_tile_n(int t) { return t == MX4_T256 ? 256 : t == MX4_T128 ? 1
 enum Mx4Load : int { MX4_DIRECT = 0, MX4_BYTES = 1, MX4_ANY = 2 };
 hipError_t launch_mx4_gemm(int tile, int load, const Mx4GemmArgs &a, int64_t units, hipStream_t stream);
 
+// The same by mx4_ring.hip, tiles of 256 and 128: K a multiple of 512, rows and scale rows
+// at multiples of 16 bytes.
+hipError_t launch_mx4_ring(int tile, const Mx4GemmArgs &a, int64_t units, hipStream_t stream);
+
 }  // namespace dg

@@ -8,15 +8,10 @@
 // adds into FP32.  (Register-only loops on this part: 7.9 PFLOP/s; the 16x16x128 form
 // 4.2.)
 #include "bytes.hpp"
-#include "device_common.hpp"
-#include "gemm_dtl.hpp"
-#include "moe_slot.hpp"
-#include "mx4.hpp"
+#include "mx4_tile.hpp"
 
 namespace dg {
 namespace {
-
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int KB = 128;          // bytes of K in a tile: 256 elements, 8 blocks
 
@@ -65,16 +60,10 @@ __device__ __forceinline__ u32x2 place_scales(u32x2 v, int at, int blocks) {
     return v;
 }
 
-// One block column of the matrix cores: 64 elements of K (two blocks, of the lanes below
-// 32 and of the others), scale byte STEP of each lane's word.
-template <int STEP>
-__device__ __forceinline__ f32x16 mfma(u32x4 a, uint32_t sa, u32x4 b, uint32_t sb, f32x16 c) {
-    const i32x8 x = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0}, y = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, STEP, (int)sa, STEP, (int)sb);
-}
+// One operand's K tile: R rows x 128 bytes, 16-byte chunks XOR-swizzled by row / 2, so that
+// the rows whose reads share a cycle fall on distinct banks.
+__device__ __forceinline__ int chunk_off(int r, int c) { return r * KB + ((c ^ ((r >> 1) & 7)) << 4); }
 
-// One operand's K tile: R rows x 128 bytes, 16-byte chunks XOR-swizzled by their row
-// (dtl::kmaj_off), so that the rows that a fragment read touches fall on distinct banks.
 template <int R, int NW>
 struct TileIO {
     static constexpr int INSTS = R * 8 / 64 / NW;   // load-to-LDS instructions of a wave
@@ -86,7 +75,7 @@ struct TileIO {
 #pragma unroll
         for (int j = 0; j < INSTS; ++j) {
             const int pos = (wave + NW * j) * 64 + lane, row = pos >> 3;
-            s.off[j] = (uint32_t)min(row, lim - 1 - r0) * (uint32_t)rs + (((pos & 7) ^ (row & 7)) << 4);
+            s.off[j] = (uint32_t)min(row, lim - 1 - r0) * (uint32_t)rs + (((pos & 7) ^ ((row >> 1) & 7)) << 4);
         }
         return s;
     }
@@ -99,7 +88,7 @@ struct TileIO {
 #pragma unroll
         for (int i = 0; i < CHUNKS; ++i) {
             const int pos = tid + i * 64 * NW, row = pos >> 3;
-            reg[i] = row_chunk(base + (int64_t)min(row, lim - 1 - r0) * rs, at + (((pos & 7) ^ (row & 7)) << 4), bytes);
+            reg[i] = row_chunk(base + (int64_t)min(row, lim - 1 - r0) * rs, at + (((pos & 7) ^ ((row >> 1) & 7)) << 4), bytes);
         }
     }
     __device__ static void store(char *lds, const u32x4 (&reg)[CHUNKS], int tid) {
@@ -126,30 +115,16 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_tile(Mx4GemmArgs a) {
     using AIO = TileIO<BM, NW>;
     using BIO = TileIO<BN, NW>;
     static_assert((BM + BN) % NT == 0 || BM + BN < NT, "whole scale rows");
-    static_assert(2 * STAGE <= 160 * 1024 - 64, "LDS");
+    static_assert(2 * STAGE <= 160 * 1024 - 64 && NW * MX4_STORE_LDS<TN> <= 2 * STAGE, "LDS");
     __shared__ __attribute__((aligned(16))) char ring[2 * STAGE];
     __shared__ int is_last;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wave_u = __builtin_amdgcn_readfirstlane(wave);
     const int wm = wave / WGN, wn = wave % WGN, l = lane & 31, h = lane >> 5;
 
-    int e = 0, begin = 0, M = a.M, t, z = 0, ktiles = a.ktiles;
-    if (a.offsets) {
-        moe::Slot s;
-        if (!moe::find_slot<BM>(a.offsets, a.o_s, a.E, a.M, a.tiles_n, a.units, blockIdx.x, s)) return;
-        e = s.e; begin = s.begin; M = s.rows; t = s.unit;
-        if (e == a.E) e = 0, ktiles = 0;           // rows of no expert: zero
-    } else {
-        t = moe::xcd_run(blockIdx.x, a.units);
-        if (SPLIT) {
-            const int u = t / a.splits;
-            z = t - u * a.splits;
-            t = u;
-        }
-    }
-    int tm, tn;
-    dtl::raster(t, (M + BM - 1) / BM, a.tiles_n, a.group_m, tm, tn);
-    const int m0 = tm * BM, n0 = tn * BN, N = a.N;
-    const int kt0 = SPLIT ? z * a.kt_per_split : 0, kt1 = SPLIT ? min(kt0 + a.kt_per_split, ktiles) : ktiles;
+    Mx4Part p;
+    if (!mx4_part<BM, BN, SPLIT>(a, p)) return;
+    const int e = p.e, begin = p.begin, M = p.M, m0 = p.m0, n0 = p.n0, N = a.N, ktiles = p.live ? a.ktiles : 0;
+    const int kt0 = SPLIT ? p.z * a.kt_per_split : 0, kt1 = SPLIT ? min(kt0 + a.kt_per_split, ktiles) : ktiles;
 
     const char *pa = a.A + (int64_t)(begin + m0) * a.a_rs, *pb = a.Q + (int64_t)e * a.q_es + (int64_t)n0 * a.q_rs;
     const char *psa = a.SA + (int64_t)(begin + m0) * a.sa_rs, *psb = a.S + (int64_t)e * a.s_es + (int64_t)n0 * a.s_rs;
@@ -196,7 +171,7 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_tile(Mx4GemmArgs a) {
 #pragma unroll 1
             for (int j = 0; j < decltype(io)::INSTS; ++j) {
                 const int pos = (wave + NW * j) * 64 + lane, row = min(pos >> 3, lim - 1 - r0);
-                const int at = kt * KB + (((pos & 7) ^ ((pos >> 3) & 7)) << 4);
+                const int at = kt * KB + (((pos & 7) ^ ((pos >> 4) & 7)) << 4);
                 const int most = row == lim - 1 - r0 ? a.row_bytes - 16 : (a.row_bytes - 1) & ~15;
                 dtl::lds_load16(base, (uint32_t)row * (uint32_t)stride + (uint32_t)min(at, most), lds + (uint32_t)((wave_u + NW * j) * 1024));
             }
@@ -223,7 +198,7 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_tile(Mx4GemmArgs a) {
         for (int r = tid; r < BM + BN; r += NT) {
             const bool is_a = r < BM, last = is_a ? m0 + r >= M - 1 : n0 + r - BM >= N - 1;
             if (is_a && !last) continue;
-            u32x4 *p = reinterpret_cast<u32x4 *>(ring + stage * STAGE + (is_a ? 0 : A_BYTES) + dtl::kmaj_off(is_a ? r : r - BM, left >> 4));
+            u32x4 *p = reinterpret_cast<u32x4 *>(ring + stage * STAGE + (is_a ? 0 : A_BYTES) + chunk_off(is_a ? r : r - BM, left >> 4));
             const u32x4 v = *p;
             *p = last ? down_bytes(v, 16 - n) : first_bytes(v, n);
         }
@@ -246,7 +221,7 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_tile(Mx4GemmArgs a) {
         // fragments are read a step ahead of their use
         u32x4 fa[2][TM], fb[2][TN];
         auto read = [&](int s) __attribute__((always_inline)) {
-            const int at = ((4 * h + s) ^ (l & 7)) << 4;
+            const int at = ((4 * h + s) ^ ((l >> 1) & 7)) << 4;
 #pragma unroll
             for (int i = 0; i < TM; ++i) fa[s & 1][i] = *reinterpret_cast<const u32x4 *>(la + 32 * i * KB + at);
 #pragma unroll
@@ -258,7 +233,7 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_tile(Mx4GemmArgs a) {
 #pragma unroll
             for (int i = 0; i < TM; ++i)
 #pragma unroll
-                for (int j = 0; j < TN; ++j) acc[i][j] = mfma<STEP>(fb[STEP & 1][j], sb[j], fa[STEP & 1][i], sa[i], acc[i][j]);
+                for (int j = 0; j < TN; ++j) acc[i][j] = mx4_mfma<STEP>(fb[STEP & 1][j], sb[j], fa[STEP & 1][i], sa[i], acc[i][j]);
             __builtin_amdgcn_sched_barrier(0);
         };
         read(0);
@@ -301,17 +276,17 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_tile(Mx4GemmArgs a) {
     if constexpr (SPLIT) {
         // [tile][piece][element][thread]: every thread adds its own elements, in the order of K
         const int S = a.splits;
-        float *part = a.ws + (int64_t)t * S * (BM * BN) + tid;
+        float *part = a.ws + (int64_t)p.t * S * (BM * BN) + tid;
         auto at = [&](int q, int i, int j, int r) __attribute__((always_inline)) { return part + (int64_t)q * (BM * BN) + ((i * TN + j) * 16 + r) * NT; };
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
             for (int j = 0; j < TN; ++j)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) __hip_atomic_store(at(z, i, j, r), acc[i][j][r], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                for (int r = 0; r < 16; ++r) __hip_atomic_store(at(p.z, i, j, r), acc[i][j][r], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         __builtin_amdgcn_s_waitcnt(0);
         __syncthreads();
-        if (tid == 0) is_last = take_last_ticket(a.counters + t, S);
+        if (tid == 0) is_last = take_last_ticket(a.counters + p.t, S);
         __syncthreads();
         if (!is_last) return;
 #pragma unroll 1
@@ -327,31 +302,10 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_tile(Mx4GemmArgs a) {
                     for (int r = 0; r < 16; ++r) acc[i][j][r] = q == 0 ? v[r] : acc[i][j][r] + v[r];
                 }
         }
-        if (tid == 0) __hip_atomic_store(a.counters + t, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (tid == 0) __hip_atomic_store(a.counters + p.t, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    // a lane holds row l and 4 adjacent columns, four times, of each 32 x 32 block
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-        const int m = m0 + wm * WTM + 32 * i + l;
-        if (m >= M) continue;
-        char *row = a.C + (int64_t)(begin + m) * a.c_rs;
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int n = n0 + wn * WTN + 32 * j + 8 * q + 4 * h;
-                float v[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) v[r] = activate(a.act, acc[i][j][4 * q + r]);
-                if (a.vec4 && n + 3 < N) {
-                    store_out4(row + (int64_t)n * a.c_cs, a.out_kind, v);
-                } else {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (n + r < N) store_out(row + (int64_t)(n + r) * a.c_cs, a.out_kind, v[r]);
-                }
-            }
-    }
+    __syncthreads();                               // every wave has read its last tile
+    mx4_store<TM, TN>(a, p, acc, wm * WTM, wn * WTN, lane, ring + wave * MX4_STORE_LDS<TN>);
 }
 
 }  // namespace
