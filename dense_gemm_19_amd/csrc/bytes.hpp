@@ -45,4 +45,12 @@ __device__ __forceinline__ u32x4 down_bytes(u32x4 v, int by) {
     return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
 }
 
+// The first n (1 to 15) bytes of v, zeros above.
+__device__ __forceinline__ u32x4 first_bytes(u32x4 v, int n) {
+    uint64_t lo = v[0] | (uint64_t)v[1] << 32, hi = v[2] | (uint64_t)v[3] << 32;
+    if (n < 8) lo &= ((uint64_t)1 << (8 * n)) - 1;
+    hi = n > 8 ? hi & (((uint64_t)1 << (8 * (n - 8))) - 1) : 0;
+    return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
+
 }  // namespace dg

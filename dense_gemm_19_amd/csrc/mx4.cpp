@@ -170,6 +170,43 @@ dg_status codes_product(const Mat &x, const Mat &sx, const Mat &off, const Stack
     return done(ring ? launch_mx4_ring(tile, a, a.units, stream) : launch_mx4_gemm(tile, load, a, a.units, stream), stream);
 }
 
+// The product of 16-bit rows with codes where many rows meet every weight (*taken; else
+// nothing happens).
+dg_status half_product(const Mat &x, const Mat &off, const Stack &q, const Stack &s, const Mat &c, int act, bool experts, hipStream_t stream,
+                       Report *r, bool *taken) {
+    const int64_t M = x.rows, N = c.cols, K = x.cols, bytes = q.one.cols;
+    const int64_t used = experts ? std::min(q.E, M) : 1, mean = M / used;
+    const int64_t s_cs = s.one.cols > 1 ? s.one.cs : 1, near = (int64_t)1 << 31;
+    auto at = [](const Mat &m, int64_t es, int64_t n) { return reinterpret_cast<uintptr_t>(m.ptr) % n == 0 && es % n == 0 && (m.rows <= 1 || m.rs % n == 0); };
+    *taken = K >= 32 && K % 8 == 0 && mean > 64 && at(x, 0, 16) && at(q.one, q.E > 1 ? q.es : 0, 4) && (N <= 1 || q.one.rs >= bytes) &&
+             128 * x.rs + 2 * K < near && 256 * q.one.rs + bytes < near && 256 * s.one.rs + s.one.cols * s_cs < near;
+    if (!*taken) return DG_SUCCESS;
+    Device d;
+    DG_TRY(ready({&x, &off, &q.span, &s.span, &c}, &d, r));
+    Mx4GemmArgs a = {};
+    a.A = x.ptr; a.a_rs = x.rs;
+    a.Q = q.one.ptr; a.q_rs = q.one.rs; a.q_es = q.es;
+    a.S = s.one.ptr; a.s_rs = s.one.rs; a.s_cs = s_cs; a.s_es = s.es;
+    a.C = out_ptr(c); a.c_rs = c.rs; a.c_cs = c.cs; a.out_kind = c.dtype; a.act = act;
+    a.vec4 = c.cs == c.esize;
+    a.M = (int)M; a.N = (int)N; a.K = (int)K;
+    a.row_bytes = (int)bytes;
+    a.blocks = (int)cdiv(K, 32);
+    if (experts) { a.offsets = off.ptr; a.o_s = off.cs; }
+    a.E = (int)q.E;
+    a.splits = 1;
+    auto expected = [&](int64_t bm, int64_t bn) { return (experts ? std::max(used, used / 2 + cdiv(M, bm)) : cdiv(M, bm)) * cdiv(N, bn); };
+    const int tile = expected(128, 256) > d.cus / 2 ? MX4_T128x256 : MX4_T64x128;
+    const int64_t bm = tile == MX4_T128x256 ? 128 : 64, bn = 2 * bm;
+    a.tiles_n = (int)cdiv(N, bn);
+    a.group_m = 8;
+    const int64_t units = experts ? ((M + std::min(q.E + 1, M) * (bm - 1)) / bm) * a.tiles_n : cdiv(M, bm) * a.tiles_n;
+    if (units > INT32_MAX || !fits_a_launch(units, 512)) return DG_ERR_OVERFLOW;
+    a.units = (int)units;
+    if (r) return r->say("many rows, %dx%d tiles, %d workgroups", (int)bm, (int)bn, a.units);
+    return done(launch_mx4_half(x.dtype == DG_F16 ? IN_F16 : IN_BF16, tile, a, units, stream), stream);
+}
+
 dg_status gemm_entry(const dg_view *A, const dg_view *SA, const dg_view *offsets, const dg_view *Q, const dg_view *S,
                      const dg_view *C, int act, bool experts, hipStream_t stream, Report *r) {
     Mat x, sx, c, off;
@@ -205,6 +242,9 @@ dg_status gemm_entry(const dg_view *A, const dg_view *SA, const dg_view *offsets
         if (spans_overlap(c, *m)) return DG_ERR_ALIAS;
     if (c.empty()) return nothing(r);
     if (codes) return codes_product(x, sx, off, q, s, c, act, experts, stream, r);
+    bool done_here = false;
+    const dg_status st = half_product(x, off, q, s, c, act, experts, stream, r, &done_here);
+    if (done_here) return st;
     return w4_run(x, off, q, s, nullptr, c, 32, act, experts, true, stream, r);
 }
 

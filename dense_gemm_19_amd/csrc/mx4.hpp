@@ -48,16 +48,16 @@ hipError_t launch_mx4_dequant(const Mx4DequantArgs &a, int64_t units, hipStream_
 
 // ---------------------------------------------------------------- products (mx4_gemm.hip)
 
-// C[m][n] = act(sum over k of A[m][k] W[n][k]), both in MXFP4.
+// C[m][n] = act(sum over k of A[m][k] W[n][k]), W in MXFP4, A too or in 16 bits.
 struct Mx4GemmArgs {
-    const char *A; int64_t a_rs;               // [M][row_bytes]
-    const char *SA; int64_t sa_rs, sa_cs;      // [M][blocks]
+    const char *A; int64_t a_rs;               // [M][row_bytes] codes, or [M][K] 16-bit
+    const char *SA; int64_t sa_rs, sa_cs;      // [M][blocks]; codes
     const char *Q; int64_t q_rs, q_es;         // [E][N][row_bytes]
     const char *S; int64_t s_rs, s_cs, s_es;   // [E][N][blocks]
     char *C; int64_t c_rs, c_cs;
     int out_kind, act;
     int vec4;                                  // rows of C are contiguous
-    int M, N;
+    int M, N, K;                               // K: 16-bit A (mx4_half.hip)
     int row_bytes, blocks;                     // ceil(K / 2), ceil(K / 32)
     const char *offsets; int64_t o_s; int E;   // offsets null: one group of all M rows
     int tiles_n, ktiles;
@@ -83,5 +83,10 @@ hipError_t launch_mx4_gemm(int tile, int load, const Mx4GemmArgs &a, int64_t uni
 // The same by mx4_ring.hip, tiles of 256 and 128: K a multiple of 512, rows and scale rows
 // at multiples of 16 bytes.
 hipError_t launch_mx4_ring(int tile, const Mx4GemmArgs &a, int64_t units, hipStream_t stream);
+
+// 16-bit A (mx4_half.hip): K a multiple of 8 and 32 at least, A's rows at multiples of 16
+// bytes, W's at multiples of 4.
+enum Mx4HalfTile : int { MX4_T128x256 = 0, MX4_T64x128 = 1 };
+hipError_t launch_mx4_half(int in_kind, int tile, const Mx4GemmArgs &a, int64_t units, hipStream_t stream);
 
 }  // namespace dg

@@ -24,14 +24,6 @@ __device__ __forceinline__ u32x4 row_chunk(const char *row, int at, int bytes) {
     return load_part<1>(row + at, 1, n);
 }
 
-// The first n (1 to 15) bytes of v, zeros above.
-__device__ __forceinline__ u32x4 first_bytes(u32x4 v, int n) {
-    uint64_t lo = v[0] | (uint64_t)v[1] << 32, hi = v[2] | (uint64_t)v[3] << 32;
-    if (n < 8) lo &= ((uint64_t)1 << (8 * n)) - 1;
-    hi = n > 8 ? hi & (((uint64_t)1 << (8 * (n - 8))) - 1) : 0;
-    return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
-}
-
 // The scale bytes of 8 blocks from `at` on of a row of `blocks`, zeros past its end: the
 // codes read there, whatever they are, then count 2^-254 times at most 36, nothing.
 // RUN: bytes adjacent, 8 of them at least: loaded from 8 before the row's end at the

@@ -1,0 +1,322 @@
+// mx4_half.hip -- products of 16-bit activations with microscaled 4-bit weights where many
+// rows meet every weight (few rows: w4.hpp):
+//
+//   C[m][n] = act(sum over blocks b of 32 k's of 2^(s[n][b] - 127) * sum over k in b of A[m][k] w[n][k])
+//
+// BF16: the weights of a block times their scale are BF16 numbers, exactly (E2M1 has two
+// significant bits), which one instruction converts two at a time; the matrix cores do the
+// rest.  FP16 does not hold every scale: there the codes are converted as they are, a
+// block's sum is formed in FP32 on the matrix cores and enters the FP32 accumulator times
+// its scale.
+#include "bytes.hpp"
+#include "device_common.hpp"
+#include "gemm_dtl.hpp"
+#include "moe_slot.hpp"
+#include "mx4_tile.hpp"
+
+namespace dg {
+namespace {
+
+constexpr int KB = 128;          // bytes of a row in LDS: 64 elements of A, 256 codes of W
+
+__device__ __forceinline__ void load_lds16(const char *base, uint32_t off, uint32_t a) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(a), "v"(off), "s"(base) : "m0");
+}
+// one byte a lane, a word each in LDS
+__device__ __forceinline__ void load_lds1(const char *base, uint32_t off, uint32_t a) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ubyte %1, %2" ::"s"(a), "v"(off), "s"(base) : "m0");
+}
+template <int N>
+__device__ __forceinline__ void arrive() {   // all but the last N loads of this wave are there, in every wave
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+template <int N> using Int = std::integral_constant<int, N>;
+
+// 2^(b - 127) (0: subnormal, 255: NaN).
+__device__ __forceinline__ float power(uint32_t b) {
+    return __builtin_bit_cast(float, max(b << 23, 0x00400000u) | (b == 255u ? 0x00400000u : 0u));
+}
+
+// 8 codes as 16-bit numbers, times the scale.
+template <int IN>
+__device__ __forceinline__ u32x4 decode(uint32_t q, float s) {
+    u32x4 v;
+#define DG_PAIR(j)                                                                                                          \
+    if constexpr (IN == IN_BF16) v[j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, j));   \
+    else v[j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, s, j));
+    DG_PAIR(0) DG_PAIR(1) DG_PAIR(2) DG_PAIR(3)
+#undef DG_PAIR
+    return v;
+}
+
+template <int IN>
+__device__ __forceinline__ f32x16 mfma(u32x4 a, u32x4 b, f32x16 c) {
+    if constexpr (IN == IN_BF16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+// BM x BN tiles, waves WGM x WGN.  LDS: a ring of four 64-element parts of A, two tiles of
+// 256 codes of W, the scale bytes of two such tiles, a word each ([block][row]).
+// A part is four steps of 16 elements.  BF16: lanes 0-31 take the part's first block and
+// lanes 32-63 its second, 8 elements at each step, so that a lane's codes are one read and
+// its scale is one.  FP16: a step lies within a block, 8 elements of either half.
+//  - Fragments are read a step ahead.  The barrier before a part's last step says that the
+//    part has been read by every wave and the next one has arrived; the loads of four
+//    parts later go into its slot (W's of two tiles later where the part is a tile's last).
+//  - Loads return in order and every wave issues the same number, so the waits count them.
+//  - A ragged K: parts past the end are not computed; what the last one holds past it is
+//    cleared, scales and codes too, since a large scale makes infinities of what is there.
+template <int IN, int BM, int BN, int WGM, int WGN>
+__global__ void __launch_bounds__(64 * WGM * WGN) mx4_half(Mx4GemmArgs a) {
+    constexpr bool BF = IN == IN_BF16;
+    constexpr int NW = WGM * WGN, NT = 64 * NW, WTM = BM / WGM, WTN = BN / WGN, TM = WTM / 32, TN = WTN / 32;
+    constexpr int PART = BM * KB, W_OFF = 4 * PART, WTILE = BN * KB, S_OFF = W_OFF + 2 * WTILE, STILE = 8 * BN * 4, LDS = S_OFF + 2 * STILE;
+    constexpr int AI = BM * 8 / 64 / NW, WI = BN * 8 / 64 / NW, SI = 8 * BN / 64 / NW, SR = BN / 64;
+    static_assert(AI * 64 * NW == BM * 8 && WI * 64 * NW == BN * 8 && SI * 64 * NW == 8 * BN && SI % 2 == 0 && NW % SR == 0, "whole loads");
+    static_assert(LDS <= 160 * 1024 && NW * MX4_STORE_LDS<TN> <= LDS, "LDS");
+    constexpr int CH = BF ? 1 : 2;                 // W: chunks and scales of a part that a lane reads
+    __shared__ __attribute__((aligned(16))) char lds[LDS];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WGN, wn = wave % WGN, l = lane & 31, h = lane >> 5;
+    Mx4Part p;
+    if (!mx4_part<BM, BN>(a, p)) return;
+    const int K = p.live ? a.K : 0, parts = (K + 63) / 64, tiles = (K + 255) / 256;
+
+    const char *pa = a.A + (int64_t)(p.begin + p.m0) * a.a_rs;
+    const char *pw = a.Q + (int64_t)p.e * a.q_es + (int64_t)p.n0 * a.q_rs, *ps = a.S + (int64_t)p.e * a.s_es + (int64_t)p.n0 * a.s_rs;
+    const uint32_t lds0 = dtl::lds_addr(lds);
+    const int last_m = p.M - 1 - p.m0, last_n = a.N - 1 - p.n0;   // rows past them read these (not stored)
+    uint32_t a_off[AI], w_off[WI], s_off;
+    int w_most[WI];
+    // chunk (16 bytes) of this lane's loads: position ^ row / 2 of A and W alike
+    const int chunk = ((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7)) << 4;
+    static_assert(NW * 4 % 8 == 0, "one chunk for every load of a lane");
+#pragma unroll
+    for (int j = 0; j < AI; ++j) a_off[j] = (uint32_t)min((wave + NW * j) * 8 + (lane >> 3), last_m) * (uint32_t)a.a_rs;
+#pragma unroll
+    for (int j = 0; j < WI; ++j) {
+        const int row = min((wave + NW * j) * 8 + (lane >> 3), last_n);
+        w_off[j] = (uint32_t)row * (uint32_t)a.q_rs;
+        // the last row's last chunk ends with it; any other one may reach into the next row
+        w_most[j] = row == last_n ? a.row_bytes - 16 : (a.row_bytes - 1) & ~15;
+    }
+    s_off = (uint32_t)min((wave % SR) * 64 + lane, last_n) * (uint32_t)a.s_rs;
+    auto load_a = [&](int j, int t) __attribute__((always_inline)) {   // chunks past K: the last one
+        load_lds16(pa, a_off[j] + (uint32_t)min(t * KB + chunk, 2 * K - 16), lds0 + (uint32_t)((t & 3) * PART + (wave + NW * j) * 1024));
+    };
+    auto load_w = [&](int j, int T) __attribute__((always_inline)) {
+        load_lds16(pw, w_off[j] + (uint32_t)min(T * KB + chunk, w_most[j]), lds0 + (uint32_t)(W_OFF + (T & 1) * WTILE + (wave + NW * j) * 1024));
+    };
+    auto load_s = [&](int j, int T) __attribute__((always_inline)) {   // one block of 64 rows
+        const int b = wave / SR + (NW / SR) * j;
+        load_lds1(ps, s_off + (uint32_t)min(8 * T + b, a.blocks - 1) * (uint32_t)a.s_cs, lds0 + (uint32_t)(S_OFF + (T & 1) * STILE + b * (BN * 4) + (wave % SR) * 256));
+    };
+
+    f32x16 acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+    u32x4 fa[2][TM], wq[2][TN][CH];                // of even and odd steps; of even and odd parts
+    uint32_t sw[2][TN][CH];                        // scale bytes
+    float sc[TN][CH];                              // what they stand for: the part at hand
+    const int ra = (wm * WTM + l) * KB, rw = W_OFF + (wn * WTN + l) * KB, rs = S_OFF + (wn * WTN + l) * 4, swz = (l >> 1) & 7;
+    auto read_a = [&](int step, int i, int slot) __attribute__((always_inline)) {
+        fa[step & 1][i] = *reinterpret_cast<const u32x4 *>(lds + ra + slot * PART + 32 * i * KB + (((BF ? 4 * h + step : 2 * step + h) ^ swz) << 4));
+    };
+    auto read_w = [&](int j, int q, int T) __attribute__((always_inline)) {   // the codes and scales of part q of tile T
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int b = 2 * q + (BF ? h : c);
+            wq[q & 1][j][c] = *reinterpret_cast<const u32x4 *>(lds + rw + (T & 1) * WTILE + 32 * j * KB + ((b ^ swz) << 4));
+            sw[q & 1][j][c] = *reinterpret_cast<const uint32_t *>(lds + rs + (T & 1) * STILE + b * (BN * 4) + 128 * j);
+        }
+    };
+    f32x16 blk[BF ? 1 : TM][BF ? 1 : TN];          // FP16: a block's sums
+    auto multiply = [&](auto s, int q) __attribute__((always_inline)) {
+        constexpr int STEP = decltype(s)::value;
+        u32x4 fb[TN];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            if constexpr (BF) fb[j] = decode<IN>(wq[q & 1][j][0][STEP], sc[j][0]);
+            else {
+                const u32x4 c = wq[q & 1][j][STEP >> 1];
+                fb[j] = decode<IN>(h ? c[2 * (STEP & 1) + 1] : c[2 * (STEP & 1)], 1.0f);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                if constexpr (BF) acc[i][j] = mfma<IN>(fa[STEP & 1][i], fb[j], acc[i][j]);
+                else {
+                    f32x16 zero;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) zero[r] = 0.f;
+                    blk[i][j] = mfma<IN>(fa[STEP & 1][i], fb[j], STEP & 1 ? blk[i][j] : zero);
+                }
+            }
+        if constexpr (!BF && (STEP & 1)) {
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) acc[i][j][r] = fmaf(sc[j][STEP >> 1], blk[i][j][r], acc[i][j][r]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // Part q of tile T (part t = 4 T + q of K).  REFILL: its slots are filled again; MORE:
+    // another whole part follows, whose first fragments are read; LEFT: loads that may be
+    // in flight then.
+    auto part = [&](auto qc, auto refill, auto more, auto left, int T) __attribute__((always_inline)) {
+        constexpr int Q = decltype(qc)::value;
+        const int t = 4 * T + Q;
+        auto next = [&](int step) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < TM; ++i) read_a(step, i, Q);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        next(1);
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int c = 0; c < CH; ++c) sc[j][c] = power(sw[Q & 1][j][c]);
+        multiply(Int<0>(), Q);
+        next(2);
+        multiply(Int<1>(), Q);
+        next(3);
+        multiply(Int<2>(), Q);
+        if constexpr (decltype(more)::value) {
+            arrive<decltype(left)::value>();
+#pragma unroll
+            for (int i = 0; i < TM; ++i) read_a(0, i, (Q + 1) & 3);
+#pragma unroll
+            for (int j = 0; j < TN; ++j) read_w(j, (Q + 1) & 3, T + (Q == 3));
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (decltype(refill)::value && Q < 2) {
+#pragma unroll
+                for (int j = Q * (SI / 2); j < (Q + 1) * (SI / 2); ++j) load_s(j, T + 1);
+            }
+            if constexpr (decltype(refill)::value) {
+#pragma unroll
+                for (int j = 0; j < AI; ++j) load_a(j, t + 4);
+            }
+            if constexpr (decltype(refill)::value && Q == 3) {
+#pragma unroll
+                for (int j = 0; j < WI; ++j) load_w(j, T + 2);
+            }
+        }
+        multiply(Int<3>(), Q);
+    };
+    using Yes = Int<1>;
+    using No = Int<0>;
+
+    if (parts > 0) {
+        // as the four parts before the first would have issued them
+#pragma unroll
+        for (int j = 0; j < WI; ++j) load_w(j, 0);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            if (t < 2) {
+#pragma unroll
+                for (int j = t * (SI / 2); j < (t + 1) * (SI / 2); ++j) load_s(j, 0);
+            }
+#pragma unroll
+            for (int j = 0; j < AI; ++j) load_a(j, t);
+        }
+#pragma unroll
+        for (int j = 0; j < WI; ++j) load_w(j, 1);   // (past the end: the rows' ends)
+        const int whole = K / 64;                  // parts without an end in them
+        if (whole > 0) {
+            arrive<3 * AI + WI>();
+#pragma unroll
+            for (int i = 0; i < TM; ++i) read_a(0, i, 0);
+#pragma unroll
+            for (int j = 0; j < TN; ++j) read_w(j, 0, 0);
+        }
+        // Loads in flight that a part does not wait for: those that the two parts before it
+        // issued, but the scales that the part after a tile's last one reads.
+        int T = 0;
+#pragma unroll 1
+        for (; 4 * T + 4 < whole; ++T) {
+            part(Int<0>(), Yes(), Yes(), Int<2 * AI + WI>(), T);
+            part(Int<1>(), Yes(), Yes(), Int<2 * AI + WI + SI / 2>(), T);
+            part(Int<2>(), Yes(), Yes(), Int<2 * AI + SI>(), T);
+            part(Int<3>(), Yes(), Yes(), Int<2 * AI>(), T);
+        }
+        // the last one to four whole parts
+        const int rest = whole - 4 * T;
+        if (rest == 1) part(Int<0>(), No(), No(), Int<0>(), T);
+        if (rest > 1) {
+            part(Int<0>(), No(), Yes(), Int<0>(), T);
+            if (rest == 2) part(Int<1>(), No(), No(), Int<0>(), T);
+        }
+        if (rest > 2) {
+            part(Int<1>(), No(), Yes(), Int<0>(), T);
+            if (rest == 3) part(Int<2>(), No(), No(), Int<0>(), T);
+        }
+        if (rest > 3) {
+            part(Int<2>(), No(), Yes(), Int<0>(), T);
+            part(Int<3>(), No(), No(), Int<0>(), T);
+        }
+        if (parts > whole) {
+            const int t = whole, TT = t >> 2, q = t & 3, left = a.row_bytes - TT * KB, n = left & 15, blocks = a.blocks - 8 * TT;
+            if (q == 0 && t > 0) {                 // the first of its tile: no part before loaded these
+#pragma unroll
+                for (int j = 0; j < SI; ++j) load_s(j, TT);
+#pragma unroll
+                for (int j = 0; j < AI; ++j) load_a(j, t);
+            }
+            arrive<0>();
+#pragma unroll 1
+            for (int i = tid; i < BM * 8; i += NT)   // A: chunks from K on (K is a multiple of 8)
+                if (64 * t + 8 * ((i & 7) ^ ((i >> 4) & 7)) >= K) *reinterpret_cast<u32x4 *>(lds + (t & 3) * PART + 16 * i) = u32x4{0u, 0u, 0u, 0u};
+            if (n != 0) {                          // W: the last chunk of the rows
+#pragma unroll 1
+                for (int r = tid; r < BN; r += NT) {
+                    u32x4 *c = reinterpret_cast<u32x4 *>(lds + W_OFF + (TT & 1) * WTILE + r * KB + (((left >> 4) ^ ((r >> 1) & 7)) << 4));
+                    *c = r >= last_n ? down_bytes(*c, 16 - n) : first_bytes(*c, n);
+                }
+            }
+#pragma unroll 1
+            for (int i = tid; i < 8 * BN; i += NT)   // scales of blocks past the end
+                if (i / BN >= blocks) *reinterpret_cast<uint32_t *>(lds + S_OFF + (TT & 1) * STILE + 4 * i) = 0u;
+            arrive<0>();
+            auto ragged = [&](auto qc) __attribute__((always_inline)) {
+                constexpr int Q = decltype(qc)::value;
+#pragma unroll
+                for (int i = 0; i < TM; ++i) read_a(0, i, Q);
+#pragma unroll
+                for (int j = 0; j < TN; ++j) read_w(j, Q, TT);
+                part(qc, No(), No(), Int<0>(), TT);
+            };
+            if (q == 0) ragged(Int<0>());
+            else if (q == 1) ragged(Int<1>());
+            else if (q == 2) ragged(Int<2>());
+            else ragged(Int<3>());
+        }
+    }
+    arrive<0>();                                   // every wave has read its last fragments
+    mx4_store<TM, TN, true>(a, p, acc, wm * WTM, wn * WTN, lane, lds + wave * MX4_STORE_LDS<TN>);
+}
+
+}  // namespace
+
+hipError_t launch_mx4_half(int in_kind, int tile, const Mx4GemmArgs &a, int64_t units, hipStream_t s) {
+#define DG_HALF(IN, BM, BN, GM, GN) hipLaunchKernelGGL((mx4_half<IN, BM, BN, GM, GN>), dim3((unsigned)units), dim3(64 * GM * GN), 0, s, a)
+    if (tile == MX4_T128x256 && in_kind == IN_BF16) DG_HALF(IN_BF16, 128, 256, 2, 4);
+    else if (tile == MX4_T128x256) DG_HALF(IN_F16, 128, 256, 2, 4);
+    else if (tile == MX4_T64x128 && in_kind == IN_BF16) DG_HALF(IN_BF16, 64, 128, 2, 2);
+    else if (tile == MX4_T64x128) DG_HALF(IN_F16, 64, 128, 2, 2);
+    else return hipErrorInvalidValue;
+#undef DG_HALF
+    return hipGetLastError();
+}
+
+}  // namespace dg

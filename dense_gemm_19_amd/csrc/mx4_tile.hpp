@@ -53,12 +53,12 @@ __device__ __forceinline__ bool mx4_part(const Mx4GemmArgs &a, Mx4Part &p) {
 template <int TN> constexpr int MX4_STORE_LDS = 32 * (32 * TN + 4) * 4;
 
 // A wave's 32 TM x 32 TN sums at (r0, c0) of the tile: a lane holds row l and 4 adjacent
-// columns, four times, of each 32 x 32 block.  32 rows at a time go through the wave's own
+// columns, four times, of each 32 x 32 block (ROWS: column l and 4 adjacent rows).  32 rows at a time go through the wave's own
 // part of LDS, so that 8 adjacent columns leave in one access, whole lines of a row from
 // adjacent lanes, and the code for types and edges is there once (stored from where they
 // are, the 256 x 256 tile's sums took 10000 instructions).  The caller's waves have all
 // left the ring.
-template <int TM, int TN>
+template <int TM, int TN, bool ROWS = false>
 __device__ __forceinline__ void mx4_store(const Mx4GemmArgs &a, const Mx4Part &p, const f32x16 (&acc)[TM][TN], int r0, int c0, int lane, char *lds) {
     constexpr int PITCH = 32 * TN + 4, CPR = 4 * TN;   // floats of a row, chunks of 8 columns in it
     const int l = lane & 31, h = lane >> 5, esize = a.out_kind == OUT_F32 ? 4 : 2;
@@ -68,9 +68,15 @@ __device__ __forceinline__ void mx4_store(const Mx4GemmArgs &a, const Mx4Part &p
 #pragma unroll
         for (int j = 0; j < TN; ++j)
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                *reinterpret_cast<f32x4 *>(buf + l * PITCH + 32 * j + 8 * q + 4 * h) =
-                    f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+            for (int q = 0; q < 4; ++q) {
+                if constexpr (ROWS) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) buf[(8 * q + 4 * h + e) * PITCH + 32 * j + l] = acc[i][j][4 * q + e];
+                } else {
+                    *reinterpret_cast<f32x4 *>(buf + l * PITCH + 32 * j + 8 * q + 4 * h) =
+                        f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+                }
+            }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll 1
         for (int c = lane; c < 32 * CPR; c += 64) {
