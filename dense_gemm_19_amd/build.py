@@ -34,7 +34,7 @@ HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-I" + os.path.join(ROOT, "
 
 HIP_SOURCES = ["gemm_mfma.hip", "gemm_dtl_f16.hip", "gemm_dtl_bf16.hip", "gemm_dtl_f8.hip", "gemm_dtl_f8s.hip", "skinny.hip",
                "epilogue.hip", "calib.hip", "quant.hip", "noalloc.hip", "moe_gemm_f16.hip", "moe_gemm_bf16.hip", "w4.hip",
-               "w4_mx.hip", "moe_route.hip", "mx4_quant.hip", "mx4_gemm.hip", "mx4_ring.hip", "mx4_half.hip"]
+               "w4_mx.hip", "moe_route.hip", "mx4_quant.hip", "mx4_gemm.hip", "mx4_ring.hip", "mx4_half.hip", "mx4_few.hip"]
 HOST_SOURCES = ["view.cpp", "plan.cpp", "dg.cpp", "gemm_dtl.cpp", "moe.cpp", "mx4.cpp"]
 
 

@@ -3,7 +3,6 @@
 #include <hip/hip_runtime_api.h>
 
 #include <cmath>
-#include <cstdlib>
 
 #include "entry.hpp"
 #include "moe.hpp"
@@ -170,6 +169,57 @@ dg_status codes_product(const Mat &x, const Mat &sx, const Mat &off, const Stack
     return done(ring ? launch_mx4_ring(tile, a, a.units, stream) : launch_mx4_gemm(tile, load, a, a.units, stream), stream);
 }
 
+// The product with codes where few rows meet every weight: 16-bit rows (sx null) or codes.
+dg_status few_product(const Mat &x, const Mat *sx, const Mat &off, const Stack &q, const Stack &s, const Mat &c, int act, bool experts,
+                      hipStream_t stream, Report *r) {
+    Device d;
+    DG_TRY(ready({&x, sx, &off, &q.span, &s.span, &c}, &d, r));
+    const int64_t M = x.rows, N = c.cols, bytes = q.one.cols, K = sx ? 2 * bytes : x.cols;
+    Mx4GemmArgs a = {};
+    a.A = x.ptr; a.a_rs = x.rs;
+    if (sx) { a.SA = sx->ptr; a.sa_rs = sx->rs; a.sa_cs = sx->cols > 1 ? sx->cs : 1; }
+    a.Q = q.one.ptr; a.q_rs = q.one.rs; a.q_es = q.es;
+    a.S = s.one.ptr; a.s_rs = s.one.rs; a.s_cs = s.one.cols > 1 ? s.one.cs : 1; a.s_es = s.es;
+    a.C = out_ptr(c); a.c_rs = c.rs; a.c_cs = c.cs; a.out_kind = c.dtype; a.act = act;
+    a.M = (int)M; a.N = (int)N; a.K = (int)K;
+    a.row_bytes = (int)bytes;
+    a.blocks = (int)cdiv(K, 32);
+    if (experts) { a.offsets = off.ptr; a.o_s = off.cs; }
+    a.E = (int)q.E;
+    const int64_t used = experts ? std::min(q.E, M) : 1, mean = cdiv(M, used);
+    const int tm = mean > 16 ? 2 : 1;
+    const int64_t rows = 16 * tm;
+    // 32 weights to a workgroup halve the reads of A and pay where 16 would fill the device
+    // more than twice (N = 14336, K = 4096, 16 rows: BF16 14.4 us beside 19.0, codes 10.6
+    // beside 12.0) and not where they leave CUs idle (N = 4096, K = 14336: 19.3 beside 14.8
+    // and 12.5 beside 11.3), nor for so few rows that A is little (one: 11.4 beside 10.1).
+    const int nf = mean > 8 && cdiv(N, 32) * used >= d.cus ? 2 : 1;
+    if (!sx && reinterpret_cast<uintptr_t>(x.ptr) % 4 == 0 && (M <= 1 || x.rs % 4 == 0)) a.a_rows = (int)std::min<int64_t>(M, rows);
+    a.tiles_n = (int)cdiv(N, 16 * nf);
+    const int64_t units = (experts ? (M + std::min(q.E + 1, M) * (rows - 1)) / rows : cdiv(M, rows)) * a.tiles_n, k_units = cdiv(bytes, 256);
+    // K in pieces where two of every tile fit the device at once and K is long (16 x 1024 x
+    // 8192, 64 tiles: BF16 7.2 us whole, 6.6 in two, 6.3 in four; codes 6.8, 6.2, 5.8); a
+    // short K loses (1 x 1024 x 4096: 3.9 whole, 4.6), and so do more tiles (256 of 16 x 4096 x
+    // 14336: 14.8 whole, 18.2 in two).  A captured call runs whole, as above.
+    int64_t splits = 1;
+    if (!experts && 2 * units <= d.cus && k_units >= 16 && !capturing(stream, r)) splits = std::min<int64_t>(d.cus / units, k_units / 4);
+    a.kt_per_split = (int)cdiv(std::max<int64_t>(k_units, 1), splits);
+    a.splits = (int)cdiv(std::max<int64_t>(k_units, 1), a.kt_per_split);
+    if (units > INT32_MAX / a.splits || !fits_a_launch(units * a.splits, 512)) return DG_ERR_OVERFLOW;
+    a.units = (int)(units * a.splits);
+    if (r) return r->say("few rows, %dx%d tiles, K in %d pieces, %d workgroups", (int)rows, 16 * nf, a.splits, a.units);
+    WsLease lease;
+    if (a.splits > 1) {
+        if (lease_workspace(stream, (size_t)units * a.splits * rows * 16 * nf * sizeof(float), (size_t)units, &lease) != hipSuccess) {
+            (void)hipGetLastError();
+            return DG_ERR_HIP;
+        }
+        a.ws = lease.ws;
+        a.counters = lease.counters;
+    }
+    return done(launch_mx4_few(sx ? MX4_CODES : x.dtype == DG_F16 ? IN_F16 : IN_BF16, tm, nf, a, a.units, stream), stream);
+}
+
 // The product of 16-bit rows with codes where many rows meet every weight (*taken; else
 // nothing happens).
 dg_status half_product(const Mat &x, const Mat &off, const Stack &q, const Stack &s, const Mat &c, int act, bool experts, hipStream_t stream,
@@ -194,7 +244,6 @@ dg_status half_product(const Mat &x, const Mat &off, const Stack &q, const Stack
     a.blocks = (int)cdiv(K, 32);
     if (experts) { a.offsets = off.ptr; a.o_s = off.cs; }
     a.E = (int)q.E;
-    a.splits = 1;
     auto expected = [&](int64_t bm, int64_t bn) { return (experts ? std::max(used, used / 2 + cdiv(M, bm)) : cdiv(M, bm)) * cdiv(N, bn); };
     const int tile = expected(128, 256) > d.cus / 2 ? MX4_T128x256 : MX4_T64x128;
     const int64_t bm = tile == MX4_T128x256 ? 128 : 64, bn = 2 * bm;
@@ -241,6 +290,10 @@ dg_status gemm_entry(const dg_view *A, const dg_view *SA, const dg_view *offsets
     for (const Mat *m : {&x, &sx, &q.span, &s.span, &off})
         if (spans_overlap(c, *m)) return DG_ERR_ALIAS;
     if (c.empty()) return nothing(r);
+    const int64_t mean = cdiv(M, experts ? std::min(q.E, M) : 1);
+    // Few rows: the kernel's own waves share K (N = 14336, K = 4096: 16 rows 14.4 us BF16 and
+    // 10.6 codes, beside 17.6 and 15.9 of the kernels below; 32 rows of codes 16.0, 16.3).
+    if (mean <= (codes ? 32 : 16)) return few_product(x, codes ? &sx : nullptr, off, q, s, c, act, experts, stream, r);
     if (codes) return codes_product(x, sx, off, q, s, c, act, experts, stream, r);
     bool done_here = false;
     const dg_status st = half_product(x, off, q, s, c, act, experts, stream, r, &done_here);

@@ -57,13 +57,14 @@ struct Mx4GemmArgs {
     char *C; int64_t c_rs, c_cs;
     int out_kind, act;
     int vec4;                                  // rows of C are contiguous
-    int M, N, K;                               // K: 16-bit A (mx4_half.hip)
+    int M, N, K;                               // K of codes: 2 * row_bytes
     int row_bytes, blocks;                     // ceil(K / 2), ceil(K / 32)
     const char *offsets; int64_t o_s; int E;   // offsets null: one group of all M rows
     int tiles_n, ktiles;
     int group_m;
     int units;                                 // workgroups of the grid
     int splits, kt_per_split;                  // K in pieces (one matrix only)
+    int a_rows;                                // mx4_few.hip: rows of a 16-bit A that a workgroup stages in LDS, or 0
     float *ws; int *counters;
 };
 
@@ -88,5 +89,10 @@ hipError_t launch_mx4_ring(int tile, const Mx4GemmArgs &a, int64_t units, hipStr
 // bytes, W's at multiples of 4.
 enum Mx4HalfTile : int { MX4_T128x256 = 0, MX4_T64x128 = 1 };
 hipError_t launch_mx4_half(int in_kind, int tile, const Mx4GemmArgs &a, int64_t units, hipStream_t stream);
+
+// Few rows (mx4_few.hip): any layout.  kind: MX4_CODES, or the type of a 16-bit A; tm, nf:
+// 16 tm rows (tm 2: codes only) x 16 nf columns of a workgroup; pieces of K of kt_per_split units of 512.
+constexpr int MX4_CODES = 3;               // beside IN_F16 and IN_BF16
+hipError_t launch_mx4_few(int kind, int tm, int nf, const Mx4GemmArgs &a, int64_t units, hipStream_t stream);
 
 }  // namespace dg

@@ -33,8 +33,11 @@ __device__ __forceinline__ void arrive() {   // all but the last N loads of this
 
 template <int N> using Int = std::integral_constant<int, N>;
 
-// 2^(b - 127) (0: subnormal, 255: NaN).
+// 2^(b - 127) (0: subnormal, 255: NaN).  BF16: its exponent, which is all that the
+// conversion reads.
+template <int IN>
 __device__ __forceinline__ float power(uint32_t b) {
+    if constexpr (IN == IN_BF16) return __builtin_bit_cast(float, b << 23);
     return __builtin_bit_cast(float, max(b << 23, 0x00400000u) | (b == 255u ? 0x00400000u : 0u));
 }
 
@@ -186,7 +189,7 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_half(Mx4GemmArgs a) {
 #pragma unroll
         for (int j = 0; j < TN; ++j)
 #pragma unroll
-            for (int c = 0; c < CH; ++c) sc[j][c] = power(sw[Q & 1][j][c]);
+            for (int c = 0; c < CH; ++c) sc[j][c] = power<IN>(sw[Q & 1][j][c]);
         multiply(Int<0>(), Q);
         next(2);
         multiply(Int<1>(), Q);
