@@ -228,11 +228,27 @@ dg_status half_product(const Mat &x, const Mat &off, const Stack &q, const Stack
     const int64_t used = experts ? std::min(q.E, M) : 1, mean = M / used;
     const int64_t s_cs = s.one.cols > 1 ? s.one.cs : 1, near = (int64_t)1 << 31;
     auto at = [](const Mat &m, int64_t es, int64_t n) { return reinterpret_cast<uintptr_t>(m.ptr) % n == 0 && es % n == 0 && (m.rows <= 1 || m.rs % n == 0); };
-    *taken = K >= 32 && K % 8 == 0 && mean > 64 && at(x, 0, 16) && at(q.one, q.E > 1 ? q.es : 0, 4) && (N <= 1 || q.one.rs >= bytes) &&
+    *taken = mean > 48 && K >= 32 && K % 8 == 0 && at(x, 0, 16) && at(q.one, q.E > 1 ? q.es : 0, 4) && (N <= 1 || q.one.rs >= bytes) &&
              128 * x.rs + 2 * K < near && 256 * q.one.rs + bytes < near && 256 * s.one.rs + s.one.cols * s_cs < near;
     if (!*taken) return DG_SUCCESS;
     Device d;
     DG_TRY(ready({&x, &off, &q.span, &s.span, &c}, &d, r));
+    auto expected = [&](int64_t bm, int64_t bn) { return (experts ? std::max(used, used / 2 + cdiv(M, bm)) : cdiv(M, bm)) * cdiv(N, bn); };
+    const int tile = expected(128, 256) > d.cus / 2 ? MX4_T128x256 : MX4_T64x128;
+    const int64_t bm = tile == MX4_T128x256 ? 128 : 64, bn = 2 * bm;
+    const int64_t units = experts ? ((M + std::min(q.E + 1, M) * (bm - 1)) / bm) * cdiv(N, bn) : cdiv(M, bm) * cdiv(N, bn);
+    // K in pieces of whole tiles of 256, four at least, where that fills idle CUs but each
+    // only once (64 x 4096 x 14336, 32 tiles: 71.9 us whole, 26.7 in four pieces, 21.8 in
+    // eight, 28.1 in 16; 64 x 4096 x 4096: 14.7 in two, 12.6 in four, 14.2 in eight).  A
+    // captured call runs whole, as above.
+    const int64_t ktiles = std::max<int64_t>(K / 256, 1);
+    int64_t splits = 1;
+    if (!experts && tile == MX4_T64x128 && 2 * units <= d.cus && ktiles >= 8 && !capturing(stream, r)) splits = std::min<int64_t>(d.cus / units, ktiles / 4);
+    // Few rows leave too little work here where the pieces are few, too (64 x 1024 x 8192: 14.2
+    // us beside 10.1 of the kernel for few rows; 64 x 4096 x 14336: 21.8 beside 26.8; 64 x
+    // 14336 x 4096: 19.1 beside 30.5; 33 x 4096 x 14336: 21.1 beside 20.6).
+    *taken = mean > 128 || 2 * splits * expected(bm, bn) >= d.cus;
+    if (!*taken) return DG_SUCCESS;
     Mx4GemmArgs a = {};
     a.A = x.ptr; a.a_rs = x.rs;
     a.Q = q.one.ptr; a.q_rs = q.one.rs; a.q_es = q.es;
@@ -244,16 +260,24 @@ dg_status half_product(const Mat &x, const Mat &off, const Stack &q, const Stack
     a.blocks = (int)cdiv(K, 32);
     if (experts) { a.offsets = off.ptr; a.o_s = off.cs; }
     a.E = (int)q.E;
-    auto expected = [&](int64_t bm, int64_t bn) { return (experts ? std::max(used, used / 2 + cdiv(M, bm)) : cdiv(M, bm)) * cdiv(N, bn); };
-    const int tile = expected(128, 256) > d.cus / 2 ? MX4_T128x256 : MX4_T64x128;
-    const int64_t bm = tile == MX4_T128x256 ? 128 : 64, bn = 2 * bm;
+    a.s_words = K % 128 == 0 && s_cs == 1 && at(s.one, s.E > 1 ? s.es : 0, 4);
     a.tiles_n = (int)cdiv(N, bn);
     a.group_m = 8;
-    const int64_t units = experts ? ((M + std::min(q.E + 1, M) * (bm - 1)) / bm) * a.tiles_n : cdiv(M, bm) * a.tiles_n;
-    if (units > INT32_MAX || !fits_a_launch(units, 512)) return DG_ERR_OVERFLOW;
-    a.units = (int)units;
-    if (r) return r->say("many rows, %dx%d tiles, %d workgroups", (int)bm, (int)bn, a.units);
-    return done(launch_mx4_half(x.dtype == DG_F16 ? IN_F16 : IN_BF16, tile, a, units, stream), stream);
+    a.kt_per_split = (int)cdiv(ktiles, splits);
+    a.splits = (int)cdiv(ktiles, a.kt_per_split);
+    if (units > INT32_MAX / a.splits || !fits_a_launch(units * a.splits, 512)) return DG_ERR_OVERFLOW;
+    a.units = (int)(units * a.splits);
+    if (r) return r->say("many rows, %dx%d tiles, K in %d pieces, %d workgroups", (int)bm, (int)bn, a.splits, a.units);
+    WsLease lease;
+    if (a.splits > 1) {
+        if (lease_workspace(stream, (size_t)units * a.splits * bm * bn * sizeof(float), (size_t)units, &lease) != hipSuccess) {
+            (void)hipGetLastError();
+            return DG_ERR_HIP;
+        }
+        a.ws = lease.ws;
+        a.counters = lease.counters;
+    }
+    return done(launch_mx4_half(x.dtype == DG_F16 ? IN_F16 : IN_BF16, tile, a, a.units, stream), stream);
 }
 
 dg_status gemm_entry(const dg_view *A, const dg_view *SA, const dg_view *offsets, const dg_view *Q, const dg_view *S,

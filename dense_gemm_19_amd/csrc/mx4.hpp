@@ -64,6 +64,7 @@ struct Mx4GemmArgs {
     int group_m;
     int units;                                 // workgroups of the grid
     int splits, kt_per_split;                  // K in pieces (one matrix only)
+    int s_words;                               // mx4_half.hip: scales at aligned words, K a multiple of 128
     int a_rows;                                // mx4_few.hip: rows of a 16-bit A that a workgroup stages in LDS, or 0
     float *ws; int *counters;
 };

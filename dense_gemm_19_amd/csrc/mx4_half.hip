@@ -22,6 +22,9 @@ constexpr int KB = 128;          // bytes of a row in LDS: 64 elements of A, 256
 __device__ __forceinline__ void load_lds16(const char *base, uint32_t off, uint32_t a) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(a), "v"(off), "s"(base) : "m0");
 }
+__device__ __forceinline__ void load_lds4(const char *base, uint32_t off, uint32_t a) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(a), "v"(off), "s"(base) : "m0");
+}
 // one byte a lane, a word each in LDS
 __device__ __forceinline__ void load_lds1(const char *base, uint32_t off, uint32_t a) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ubyte %1, %2" ::"s"(a), "v"(off), "s"(base) : "m0");
@@ -72,24 +75,26 @@ __device__ __forceinline__ f32x16 mfma(u32x4 a, u32x4 b, f32x16 c) {
 //  - Loads return in order and every wave issues the same number, so the waits count them.
 //  - A ragged K: parts past the end are not computed; what the last one holds past it is
 //    cleared, scales and codes too, since a large scale makes infinities of what is there.
-template <int IN, int BM, int BN, int WGM, int WGN>
+// WORDS: the scales come four to a word (side by side, aligned, K in whole groups of 128).
+template <int IN, int BM, int BN, int WGM, int WGN, bool WORDS>
 __global__ void __launch_bounds__(64 * WGM * WGN) mx4_half(Mx4GemmArgs a) {
-    constexpr bool BF = IN == IN_BF16;
     constexpr int NW = WGM * WGN, NT = 64 * NW, WTM = BM / WGM, WTN = BN / WGN, TM = WTM / 32, TN = WTN / 32;
-    constexpr int PART = BM * KB, W_OFF = 4 * PART, WTILE = BN * KB, S_OFF = W_OFF + 2 * WTILE, STILE = 8 * BN * 4, LDS = S_OFF + 2 * STILE;
-    constexpr int AI = BM * 8 / 64 / NW, WI = BN * 8 / 64 / NW, SI = 8 * BN / 64 / NW, SR = BN / 64;
-    static_assert(AI * 64 * NW == BM * 8 && WI * 64 * NW == BN * 8 && SI * 64 * NW == 8 * BN && SI % 2 == 0 && NW % SR == 0, "whole loads");
-    static_assert(LDS <= 160 * 1024 && NW * MX4_STORE_LDS<TN> <= LDS, "LDS");
-    constexpr int CH = BF ? 1 : 2;                 // W: chunks and scales of a part that a lane reads
+    constexpr bool SPLIT = BM == 64;               // K in pieces
+    constexpr int PART = BM * KB, W_OFF = 4 * PART, WTILE = BN * KB, S_OFF = W_OFF + 2 * WTILE, SB = WORDS ? 4 : 1, STILE = 8 / SB * BN * 4, LDS = S_OFF + 2 * STILE;
+    constexpr int AI = BM * 8 / 64 / NW, WI = BN * 8 / 64 / NW, SI = 8 / SB * BN / 64 / NW, S1 = (SI + 1) / 2, SR = BN / 64;
+    static_assert(AI * 64 * NW == BM * 8 && WI * 64 * NW == BN * 8 && SI * SB * 64 * NW == 8 * BN && NW % SR == 0, "whole loads");
+    static_assert(LDS + 64 <= 160 * 1024 && NW * MX4_STORE_LDS<TN> <= LDS, "LDS");
     __shared__ __attribute__((aligned(16))) char lds[LDS];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WGN, wn = wave % WGN, l = lane & 31, h = lane >> 5;
     Mx4Part p;
-    if (!mx4_part<BM, BN>(a, p)) return;
-    const int K = p.live ? a.K : 0, parts = (K + 63) / 64, tiles = (K + 255) / 256;
+    if (!mx4_part<BM, BN, SPLIT>(a, p)) return;
+    // this piece of K: whole tiles, the last one what is left of K too
+    const int k0 = p.z * a.kt_per_split * 256, K = !p.live ? 0 : !SPLIT || p.z == a.splits - 1 ? a.K - k0 : a.kt_per_split * 256, parts = (K + 63) / 64;
+    const int row_bytes = (K + 1) / 2, blocks = (K + 31) / 32;
 
-    const char *pa = a.A + (int64_t)(p.begin + p.m0) * a.a_rs;
-    const char *pw = a.Q + (int64_t)p.e * a.q_es + (int64_t)p.n0 * a.q_rs, *ps = a.S + (int64_t)p.e * a.s_es + (int64_t)p.n0 * a.s_rs;
+    const char *pa = a.A + (int64_t)(p.begin + p.m0) * a.a_rs + (int64_t)k0 * 2;
+    const char *pw = a.Q + (int64_t)p.e * a.q_es + (int64_t)p.n0 * a.q_rs + k0 / 2, *ps = a.S + (int64_t)p.e * a.s_es + (int64_t)p.n0 * a.s_rs + (int64_t)(k0 / 32) * a.s_cs;
     const uint32_t lds0 = dtl::lds_addr(lds);
     const int last_m = p.M - 1 - p.m0, last_n = a.N - 1 - p.n0;   // rows past them read these (not stored)
     uint32_t a_off[AI], w_off[WI], s_off;
@@ -104,7 +109,7 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_half(Mx4GemmArgs a) {
         const int row = min((wave + NW * j) * 8 + (lane >> 3), last_n);
         w_off[j] = (uint32_t)row * (uint32_t)a.q_rs;
         // the last row's last chunk ends with it; any other one may reach into the next row
-        w_most[j] = row == last_n ? a.row_bytes - 16 : (a.row_bytes - 1) & ~15;
+        w_most[j] = row == last_n ? row_bytes - 16 : (row_bytes - 1) & ~15;
     }
     s_off = (uint32_t)min((wave % SR) * 64 + lane, last_n) * (uint32_t)a.s_rs;
     auto load_a = [&](int j, int t) __attribute__((always_inline)) {   // chunks past K: the last one
@@ -113,9 +118,10 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_half(Mx4GemmArgs a) {
     auto load_w = [&](int j, int T) __attribute__((always_inline)) {
         load_lds16(pw, w_off[j] + (uint32_t)min(T * KB + chunk, w_most[j]), lds0 + (uint32_t)(W_OFF + (T & 1) * WTILE + (wave + NW * j) * 1024));
     };
-    auto load_s = [&](int j, int T) __attribute__((always_inline)) {   // one block of 64 rows
+    auto load_s = [&](int j, int T) __attribute__((always_inline)) {   // one block, or word, of 64 rows
         const int b = wave / SR + (NW / SR) * j;
-        load_lds1(ps, s_off + (uint32_t)min(8 * T + b, a.blocks - 1) * (uint32_t)a.s_cs, lds0 + (uint32_t)(S_OFF + (T & 1) * STILE + b * (BN * 4) + (wave % SR) * 256));
+        if constexpr (WORDS) load_lds4(ps, s_off + (uint32_t)min(8 * T + 4 * b, blocks - 4), lds0 + (uint32_t)(S_OFF + (T & 1) * STILE + b * (BN * 4) + (wave % SR) * 256));
+        else load_lds1(ps, s_off + (uint32_t)min(8 * T + b, blocks - 1) * (uint32_t)a.s_cs, lds0 + (uint32_t)(S_OFF + (T & 1) * STILE + b * (BN * 4) + (wave % SR) * 256));
     };
 
     f32x16 acc[TM][TN];
@@ -125,116 +131,108 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_half(Mx4GemmArgs a) {
         for (int j = 0; j < TN; ++j)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-    u32x4 fa[2][TM], wq[2][TN][CH];                // of even and odd steps; of even and odd parts
-    uint32_t sw[2][TN][CH];                        // scale bytes
-    float sc[TN][CH];                              // what they stand for: the part at hand
-    const int ra = (wm * WTM + l) * KB, rw = W_OFF + (wn * WTN + l) * KB, rs = S_OFF + (wn * WTN + l) * 4, swz = (l >> 1) & 7;
-    auto read_a = [&](int step, int i, int slot) __attribute__((always_inline)) {
-        fa[step & 1][i] = *reinterpret_cast<const u32x4 *>(lds + ra + slot * PART + 32 * i * KB + (((BF ? 4 * h + step : 2 * step + h) ^ swz) << 4));
-    };
-    auto read_w = [&](int j, int q, int T) __attribute__((always_inline)) {   // the codes and scales of part q of tile T
+    // ONE: a lane's elements of a part are of one block, and W's are taken times its scale.
+    auto run = [&](auto one) __attribute__((always_inline)) {
+        constexpr bool ONE = decltype(one)::value;
+        constexpr int CH = ONE ? 1 : 2;            // W: chunks and scales of a part that a lane reads
+        u32x4 fa[2][TM], wq[2][TN][CH];                // of even and odd steps; of even and odd parts
+        uint32_t sw[2][TN][CH];                        // scale bytes
+        float sc[TN][CH];                              // what they stand for: the part at hand
+        const int ra = (wm * WTM + l) * KB, rw = W_OFF + (wn * WTN + l) * KB, rs = S_OFF + (wn * WTN + l) * 4, swz = (l >> 1) & 7;
+        auto read_a = [&](int step, int i, int slot) __attribute__((always_inline)) {
+            fa[step & 1][i] = *reinterpret_cast<const u32x4 *>(lds + ra + slot * PART + 32 * i * KB + (((ONE ? 4 * h + step : 2 * step + h) ^ swz) << 4));
+        };
+        auto read_w = [&](int j, int q, int T) __attribute__((always_inline)) {   // the codes and scales of part q of tile T
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const int b = 2 * q + (BF ? h : c);
-            wq[q & 1][j][c] = *reinterpret_cast<const u32x4 *>(lds + rw + (T & 1) * WTILE + 32 * j * KB + ((b ^ swz) << 4));
-            sw[q & 1][j][c] = *reinterpret_cast<const uint32_t *>(lds + rs + (T & 1) * STILE + b * (BN * 4) + 128 * j);
-        }
-    };
-    f32x16 blk[BF ? 1 : TM][BF ? 1 : TN];          // FP16: a block's sums
-    auto multiply = [&](auto s, int q) __attribute__((always_inline)) {
-        constexpr int STEP = decltype(s)::value;
-        u32x4 fb[TN];
-#pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            if constexpr (BF) fb[j] = decode<IN>(wq[q & 1][j][0][STEP], sc[j][0]);
-            else {
-                const u32x4 c = wq[q & 1][j][STEP >> 1];
-                fb[j] = decode<IN>(h ? c[2 * (STEP & 1) + 1] : c[2 * (STEP & 1)], 1.0f);
+            for (int c = 0; c < CH; ++c) {
+                const int b = 2 * q + (ONE ? h : c);
+                const char *at = lds + rs + (T & 1) * STILE + 128 * j;
+                wq[q & 1][j][c] = *reinterpret_cast<const u32x4 *>(lds + rw + (T & 1) * WTILE + 32 * j * KB + ((b ^ swz) << 4));
+                if constexpr (WORDS) sw[q & 1][j][c] = *reinterpret_cast<const uint8_t *>(at + (q >> 1) * (BN * 4) + (b & 3));
+                else sw[q & 1][j][c] = *reinterpret_cast<const uint32_t *>(at + b * (BN * 4));
             }
-        }
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
+        };
+        f32x16 blk[ONE ? 1 : TM][ONE ? 1 : TN];          // FP16: a block's sums
+        auto multiply = [&](auto s, int q) __attribute__((always_inline)) {
+            constexpr int STEP = decltype(s)::value;
+            u32x4 fb[TN];
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
-                if constexpr (BF) acc[i][j] = mfma<IN>(fa[STEP & 1][i], fb[j], acc[i][j]);
+                if constexpr (ONE) fb[j] = decode<IN>(wq[q & 1][j][0][STEP], sc[j][0]);
                 else {
-                    f32x16 zero;
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) zero[r] = 0.f;
-                    blk[i][j] = mfma<IN>(fa[STEP & 1][i], fb[j], STEP & 1 ? blk[i][j] : zero);
+                    const u32x4 c = wq[q & 1][j][STEP >> 1];
+                    fb[j] = decode<IN>(h ? c[2 * (STEP & 1) + 1] : c[2 * (STEP & 1)], 1.0f);
                 }
             }
-        if constexpr (!BF && (STEP & 1)) {
 #pragma unroll
             for (int i = 0; i < TM; ++i)
 #pragma unroll
-                for (int j = 0; j < TN; ++j)
+                for (int j = 0; j < TN; ++j) {
+                    if constexpr (ONE) acc[i][j] = mfma<IN>(fa[STEP & 1][i], fb[j], acc[i][j]);
+                    else {
+                        f32x16 zero;
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) acc[i][j][r] = fmaf(sc[j][STEP >> 1], blk[i][j][r], acc[i][j][r]);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-    };
-    // Part q of tile T (part t = 4 T + q of K).  REFILL: its slots are filled again; MORE:
-    // another whole part follows, whose first fragments are read; LEFT: loads that may be
-    // in flight then.
-    auto part = [&](auto qc, auto refill, auto more, auto left, int T) __attribute__((always_inline)) {
-        constexpr int Q = decltype(qc)::value;
-        const int t = 4 * T + Q;
-        auto next = [&](int step) __attribute__((always_inline)) {
+                        for (int r = 0; r < 16; ++r) zero[r] = 0.f;
+                        blk[i][j] = mfma<IN>(fa[STEP & 1][i], fb[j], STEP & 1 ? blk[i][j] : zero);
+                    }
+                }
+            if constexpr (!ONE && (STEP & 1)) {
 #pragma unroll
-            for (int i = 0; i < TM; ++i) read_a(step, i, Q);
+                for (int i = 0; i < TM; ++i)
+#pragma unroll
+                    for (int j = 0; j < TN; ++j)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) acc[i][j][r] = fmaf(sc[j][STEP >> 1], blk[i][j][r], acc[i][j][r]);
+            }
             __builtin_amdgcn_sched_barrier(0);
         };
-        next(1);
+        // Part q of tile T (part t = 4 T + q of K).  REFILL: its slots are filled again; MORE:
+        // another whole part follows, whose first fragments are read; LEFT: loads that may be
+        // in flight then.
+        auto part = [&](auto qc, auto refill, auto more, auto left, int T) __attribute__((always_inline)) {
+            constexpr int Q = decltype(qc)::value;
+            const int t = 4 * T + Q;
+            auto next = [&](int step) __attribute__((always_inline)) {
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
+                for (int i = 0; i < TM; ++i) read_a(step, i, Q);
+                __builtin_amdgcn_sched_barrier(0);
+            };
+            next(1);
 #pragma unroll
-            for (int c = 0; c < CH; ++c) sc[j][c] = power<IN>(sw[Q & 1][j][c]);
-        multiply(Int<0>(), Q);
-        next(2);
-        multiply(Int<1>(), Q);
-        next(3);
-        multiply(Int<2>(), Q);
-        if constexpr (decltype(more)::value) {
-            arrive<decltype(left)::value>();
+            for (int j = 0; j < TN; ++j)
 #pragma unroll
-            for (int i = 0; i < TM; ++i) read_a(0, i, (Q + 1) & 3);
+                for (int c = 0; c < CH; ++c) sc[j][c] = power<IN>(sw[Q & 1][j][c]);
+            multiply(Int<0>(), Q);
+            next(2);
+            multiply(Int<1>(), Q);
+            next(3);
+            multiply(Int<2>(), Q);
+            if constexpr (decltype(more)::value) {
+                arrive<decltype(left)::value>();
 #pragma unroll
-            for (int j = 0; j < TN; ++j) read_w(j, (Q + 1) & 3, T + (Q == 3));
-            __builtin_amdgcn_sched_barrier(0);
-            if constexpr (decltype(refill)::value && Q < 2) {
+                for (int i = 0; i < TM; ++i) read_a(0, i, (Q + 1) & 3);
 #pragma unroll
-                for (int j = Q * (SI / 2); j < (Q + 1) * (SI / 2); ++j) load_s(j, T + 1);
+                for (int j = 0; j < TN; ++j) read_w(j, (Q + 1) & 3, T + (Q == 3));
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (decltype(refill)::value && Q < 2) {
+#pragma unroll
+                    for (int j = Q * S1; j < (Q ? SI : S1); ++j) load_s(j, T + 1);
+                }
+                if constexpr (decltype(refill)::value) {
+#pragma unroll
+                    for (int j = 0; j < AI; ++j) load_a(j, t + 4);
+                }
+                if constexpr (decltype(refill)::value && Q == 3) {
+#pragma unroll
+                    for (int j = 0; j < WI; ++j) load_w(j, T + 2);
+                }
             }
-            if constexpr (decltype(refill)::value) {
-#pragma unroll
-                for (int j = 0; j < AI; ++j) load_a(j, t + 4);
-            }
-            if constexpr (decltype(refill)::value && Q == 3) {
-#pragma unroll
-                for (int j = 0; j < WI; ++j) load_w(j, T + 2);
-            }
-        }
-        multiply(Int<3>(), Q);
-    };
-    using Yes = Int<1>;
-    using No = Int<0>;
+            multiply(Int<3>(), Q);
+        };
+        using Yes = Int<1>;
+        using No = Int<0>;
 
-    if (parts > 0) {
-        // as the four parts before the first would have issued them
-#pragma unroll
-        for (int j = 0; j < WI; ++j) load_w(j, 0);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            if (t < 2) {
-#pragma unroll
-                for (int j = t * (SI / 2); j < (t + 1) * (SI / 2); ++j) load_s(j, 0);
-            }
-#pragma unroll
-            for (int j = 0; j < AI; ++j) load_a(j, t);
-        }
-#pragma unroll
-        for (int j = 0; j < WI; ++j) load_w(j, 1);   // (past the end: the rows' ends)
+
         const int whole = K / 64;                  // parts without an end in them
         if (whole > 0) {
             arrive<3 * AI + WI>();
@@ -249,7 +247,7 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_half(Mx4GemmArgs a) {
 #pragma unroll 1
         for (; 4 * T + 4 < whole; ++T) {
             part(Int<0>(), Yes(), Yes(), Int<2 * AI + WI>(), T);
-            part(Int<1>(), Yes(), Yes(), Int<2 * AI + WI + SI / 2>(), T);
+            part(Int<1>(), Yes(), Yes(), Int<2 * AI + WI + S1>(), T);
             part(Int<2>(), Yes(), Yes(), Int<2 * AI + SI>(), T);
             part(Int<3>(), Yes(), Yes(), Int<2 * AI>(), T);
         }
@@ -268,8 +266,8 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_half(Mx4GemmArgs a) {
             part(Int<2>(), No(), Yes(), Int<0>(), T);
             part(Int<3>(), No(), No(), Int<0>(), T);
         }
-        if (parts > whole) {
-            const int t = whole, TT = t >> 2, q = t & 3, left = a.row_bytes - TT * KB, n = left & 15, blocks = a.blocks - 8 * TT;
+        if (!WORDS && parts > whole) {
+            const int t = whole, TT = t >> 2, q = t & 3, left = row_bytes - TT * KB, n = left & 15, there = blocks - 8 * TT;
             if (q == 0 && t > 0) {                 // the first of its tile: no part before loaded these
 #pragma unroll
                 for (int j = 0; j < SI; ++j) load_s(j, TT);
@@ -289,7 +287,7 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_half(Mx4GemmArgs a) {
             }
 #pragma unroll 1
             for (int i = tid; i < 8 * BN; i += NT)   // scales of blocks past the end
-                if (i / BN >= blocks) *reinterpret_cast<uint32_t *>(lds + S_OFF + (TT & 1) * STILE + 4 * i) = 0u;
+                if (i / BN >= there) *reinterpret_cast<uint32_t *>(lds + S_OFF + (TT & 1) * STILE + 4 * i) = 0u;
             arrive<0>();
             auto ragged = [&](auto qc) __attribute__((always_inline)) {
                 constexpr int Q = decltype(qc)::value;
@@ -304,15 +302,84 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_half(Mx4GemmArgs a) {
             else if (q == 2) ragged(Int<2>());
             else ragged(Int<3>());
         }
+    };
+    if (parts > 0) {
+        // as the four parts before the first would have issued them
+#pragma unroll
+        for (int j = 0; j < WI; ++j) load_w(j, 0);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            if (t < 2) {
+#pragma unroll
+                for (int j = t * S1; j < (t ? SI : S1); ++j) load_s(j, 0);
+            }
+#pragma unroll
+            for (int j = 0; j < AI; ++j) load_a(j, t);
+        }
+#pragma unroll
+        for (int j = 0; j < WI; ++j) load_w(j, 1);   // (past the end: the rows' ends)
+        if constexpr (IN == IN_BF16) run(Int<1>());
+        else if constexpr (!WORDS) run(Int<0>());
+        else {
+            // does FP16 hold every code times its scale: 2^-24 .. 2^15, scales 2^-23 .. 2^13?
+            uint32_t far = 0;
+            const int words = blocks / 4, rows = min(BN, last_n + 1);
+#pragma unroll 1
+            for (int c = lane & 15; c < words; c += 16)
+#pragma unroll 8
+                for (int r = tid >> 4; r < BN; r += NT / 16) {
+                    const uint32_t v = *reinterpret_cast<const uint32_t *>(ps + (int64_t)min(r, rows - 1) * a.s_rs + 4 * c);
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) far |= ((v >> (8 * b)) & 255u) - 104u > 36u;
+                }
+            if (__syncthreads_or((int)far)) run(Int<0>());
+            else run(Int<1>());
+        }
     }
     arrive<0>();                                   // every wave has read its last fragments
+    if (SPLIT && a.splits > 1) {
+        // [tile][piece][element][thread]: every thread adds its own elements, in the order of
+        // K, four pieces on the way at once
+        constexpr int REGS = TM * TN * 16;
+        __shared__ int is_last;
+        float *sums = a.ws + (int64_t)p.t * a.splits * (BM * BN) + tid;
+#pragma unroll
+        for (int k = 0; k < REGS; ++k)
+            __hip_atomic_store(sums + (int64_t)p.z * (BM * BN) + k * NT, acc[k / 16 / TN][k / 16 % TN][k % 16], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+        if (tid == 0) is_last = take_last_ticket(a.counters + p.t, a.splits);
+        __syncthreads();
+        if (!is_last) return;
+#pragma unroll
+        for (int k = 0; k < REGS; ++k) acc[k / 16 / TN][k / 16 % TN][k % 16] = 0.f;
+#pragma unroll 1
+        for (int q = 0; q < a.splits; q += 4) {
+            float v[4][REGS];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (q + u < a.splits)
+#pragma unroll
+                    for (int k = 0; k < REGS; ++k) v[u][k] = __hip_atomic_load(sums + (int64_t)(q + u) * (BM * BN) + k * NT, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (q + u < a.splits)
+#pragma unroll
+                    for (int k = 0; k < REGS; ++k) acc[k / 16 / TN][k / 16 % TN][k % 16] += v[u][k];
+        }
+        if (tid == 0) __hip_atomic_store(a.counters + p.t, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
     mx4_store<TM, TN, true>(a, p, acc, wm * WTM, wn * WTN, lane, lds + wave * MX4_STORE_LDS<TN>);
 }
 
 }  // namespace
 
 hipError_t launch_mx4_half(int in_kind, int tile, const Mx4GemmArgs &a, int64_t units, hipStream_t s) {
-#define DG_HALF(IN, BM, BN, GM, GN) hipLaunchKernelGGL((mx4_half<IN, BM, BN, GM, GN>), dim3((unsigned)units), dim3(64 * GM * GN), 0, s, a)
+#define DG_HALF(IN, BM, BN, GM, GN)                                                                                                                     \
+    do {                                                                                                                                                \
+        if (a.s_words) hipLaunchKernelGGL((mx4_half<IN, BM, BN, GM, GN, true>), dim3((unsigned)units), dim3(64 * GM * GN), 0, s, a);                    \
+        else hipLaunchKernelGGL((mx4_half<IN, BM, BN, GM, GN, false>), dim3((unsigned)units), dim3(64 * GM * GN), 0, s, a);                             \
+    } while (0)
     if (tile == MX4_T128x256 && in_kind == IN_BF16) DG_HALF(IN_BF16, 128, 256, 2, 4);
     else if (tile == MX4_T128x256) DG_HALF(IN_F16, 128, 256, 2, 4);
     else if (tile == MX4_T64x128 && in_kind == IN_BF16) DG_HALF(IN_BF16, 64, 128, 2, 2);

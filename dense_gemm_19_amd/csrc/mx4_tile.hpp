@@ -36,7 +36,7 @@ __device__ __forceinline__ bool mx4_part(const Mx4GemmArgs &a, Mx4Part &p) {
         if (p.e == a.E) p.e = p.live = 0;
     } else {
         p.t = moe::xcd_run(blockIdx.x, a.units);
-        if (SPLIT) {
+        if (SPLIT && a.splits > 1) {
             const int u = p.t / a.splits;
             p.z = p.t - u * a.splits;
             p.t = u;
