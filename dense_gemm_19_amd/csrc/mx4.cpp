@@ -169,6 +169,9 @@ dg_status codes_product(const Mat &x, const Mat &sx, const Mat &off, const Stack
     return done(ring ? launch_mx4_ring(tile, a, a.units, stream) : launch_mx4_gemm(tile, load, a, a.units, stream), stream);
 }
 
+// A 16-bit A that the kernel for few rows stages in LDS.
+bool few_aligned(const Mat &x) { return reinterpret_cast<uintptr_t>(x.ptr) % 4 == 0 && (x.rows <= 1 || (x.rs % 4 == 0 && x.rs < 1 << 24)); }
+
 // The product with codes where few rows meet every weight: 16-bit rows (sx null) or codes.
 dg_status few_product(const Mat &x, const Mat *sx, const Mat &off, const Stack &q, const Stack &s, const Mat &c, int act, bool experts,
                       hipStream_t stream, Report *r) {
@@ -187,22 +190,27 @@ dg_status few_product(const Mat &x, const Mat *sx, const Mat &off, const Stack &
     if (experts) { a.offsets = off.ptr; a.o_s = off.cs; }
     a.E = (int)q.E;
     const int64_t used = experts ? std::min(q.E, M) : 1, mean = cdiv(M, used);
-    const int tm = mean > 16 ? 2 : 1;
-    const int64_t rows = 16 * tm;
-    // 32 weights to a workgroup halve the reads of A and pay where 16 would fill the device
-    // more than twice (N = 14336, K = 4096, 16 rows: BF16 14.4 us beside 19.0, codes 10.6
-    // beside 12.0) and not where they leave CUs idle (N = 4096, K = 14336: 19.3 beside 14.8
-    // and 12.5 beside 11.3), nor for so few rows that A is little (one: 11.4 beside 10.1).
-    const int nf = mean > 8 && cdiv(N, 32) * used >= d.cus ? 2 : 1;
-    if (!sx && reinterpret_cast<uintptr_t>(x.ptr) % 4 == 0 && (M <= 1 || x.rs % 4 == 0)) a.a_rows = (int)std::min<int64_t>(M, rows);
+    const bool aligned = !sx && few_aligned(x);
+    const int tm = mean > 32 ? 3 : mean > 16 ? 2 : 1;
+    const int64_t rows = mx4_few_rows(tm);
+    if (aligned) a.a_rows = (int)std::min<int64_t>(M, rows);
+    const int64_t k_units = cdiv(bytes, 256), tiles = cdiv(N, 32) * used;
+    const bool pieces = !experts && k_units >= 16 && !capturing(stream, r);
+    // 32 columns to a workgroup halve the reads of A.  They pay where they still fill the
+    // device (N = 14336, K = 4096, 16 rows: BF16 12.9 us beside 16.5, codes 10.4 beside 12.0)
+    // or fill it with a long K in two pieces (N = 4096, K = 14336: 32 rows 17.5 beside 20,
+    // 16 rows 14.1 beside 14.5, codes 11.1 beside 11.3), and not for so few rows that A is
+    // little (N = 14336, 1 row: 10.0 beside 8.9; N = 4096, 8 rows: 13.3 beside 12.4).
+    const bool wide = sx || aligned;
+    const int nf = wide && mean > 8 && (tiles >= d.cus || (pieces && 2 * tiles >= d.cus)) ? 2 : 1;
     a.tiles_n = (int)cdiv(N, 16 * nf);
-    const int64_t units = (experts ? (M + std::min(q.E + 1, M) * (rows - 1)) / rows : cdiv(M, rows)) * a.tiles_n, k_units = cdiv(bytes, 256);
+    const int64_t units = (experts ? (M + std::min(q.E + 1, M) * (rows - 1)) / rows : cdiv(M, rows)) * a.tiles_n;
     // K in pieces where two of every tile fit the device at once and K is long (16 x 1024 x
     // 8192, 64 tiles: BF16 7.2 us whole, 6.6 in two, 6.3 in four; codes 6.8, 6.2, 5.8); a
     // short K loses (1 x 1024 x 4096: 3.9 whole, 4.6), and so do more tiles (256 of 16 x 4096 x
     // 14336: 14.8 whole, 18.2 in two).  A captured call runs whole, as above.
     int64_t splits = 1;
-    if (!experts && 2 * units <= d.cus && k_units >= 16 && !capturing(stream, r)) splits = std::min<int64_t>(d.cus / units, k_units / 4);
+    if (pieces && 2 * units <= d.cus) splits = std::min<int64_t>(d.cus / units, k_units / 4);
     a.kt_per_split = (int)cdiv(std::max<int64_t>(k_units, 1), splits);
     a.splits = (int)cdiv(std::max<int64_t>(k_units, 1), a.kt_per_split);
     if (units > INT32_MAX / a.splits || !fits_a_launch(units * a.splits, 512)) return DG_ERR_OVERFLOW;
@@ -315,9 +323,13 @@ dg_status gemm_entry(const dg_view *A, const dg_view *SA, const dg_view *offsets
         if (spans_overlap(c, *m)) return DG_ERR_ALIAS;
     if (c.empty()) return nothing(r);
     const int64_t mean = cdiv(M, experts ? std::min(q.E, M) : 1);
-    // Few rows: the kernel's own waves share K (N = 14336, K = 4096: 16 rows 14.4 us BF16 and
-    // 10.6 codes, beside 17.6 and 15.9 of the kernels below; 32 rows of codes 16.0, 16.3).
-    if (mean <= (codes ? 32 : 16)) return few_product(x, codes ? &sx : nullptr, off, q, s, c, act, experts, stream, r);
+    // Few rows: that kernel's waves share K and read A again for every 16 or 32 columns, which
+    // pays up to 32 rows of codes (N = 14336, K = 4096: 14.8 us beside 16.3), 16 of 16 bits
+    // (12.9 beside 17.6), and 36 where one workgroup to a CU takes all columns (32 x 4096 x
+    // 4096: 7.1 us beside 15.0; 33 x 4096 x 14336: 19.5 beside 20.6; 32 x 14336 x 4096: 18.0
+    // beside 16.5).
+    const bool more = few_aligned(x) && !experts && N <= 16 * 256;
+    if (mean <= (codes ? 32 : more ? 36 : 16)) return few_product(x, codes ? &sx : nullptr, off, q, s, c, act, experts, stream, r);
     if (codes) return codes_product(x, sx, off, q, s, c, act, experts, stream, r);
     bool done_here = false;
     const dg_status st = half_product(x, off, q, s, c, act, experts, stream, r, &done_here);

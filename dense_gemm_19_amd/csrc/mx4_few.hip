@@ -6,14 +6,15 @@
 // A workgroup's 8 waves share 16 NF columns and split K: a unit is 512 elements, 256 bytes
 // of a row of codes and 16 of its scales.  Lane (g, n), n = lane % 16, loads of row n the 16
 // bytes 64 j + 16 g at each of four steps j, a whole block, and all 16 scale bytes.
-// Bytes of codes bound it; what it reaches (BF16 / codes): 1 x 14336 x 4096, 31 MB, 10.1 /
-// 8.6 us, 3.6 TB/s with a launch of 1.5 in it; 16 x 4096 x 14336 14.8 / 11.3 us.
+// Bytes of codes bound it for a few rows, the way of A from the caches beyond (all columns'
+// workgroups read it): 1 x 14336 x 4096, 31 MB, 8.8 us BF16 and 8.5 codes, 3.6 TB/s with a
+// launch of 1.5 us in it; 16 rows 12.8 / 10.5; 33 x 4096 x 14336 19.5 us BF16.
 //   A in codes: those are the operands of v_mfma_scale_f32_16x16x128_f8f6f4 as they lie.
 //   A in 16 bits: the lanes of a row first exchange words (a 4 x 4 transpose in four
 //   instructions), so that an instruction of 32 elements meets one block of every row.
-//   BF16 weights are converted times their scale, exactly; FP16 does not hold every
-//   scale, so its codes are converted as they are and a block's sum, in FP32, is added
-//   times its scale.
+//   The weights are converted times their scale, exactly, in BF16 always and for STEPS (see
+//   below) in FP16, too, where it holds the products; elsewhere FP16's codes are converted
+//   as they are and a block's sum, in FP32, is added times its scale.
 #include <algorithm>
 
 #include "bytes.hpp"
@@ -66,15 +67,29 @@ __device__ __forceinline__ u32x4 decode(uint32_t q, float s) {
     return v;
 }
 
-// STAGED (16-bit A at aligned words): a wave brings its units of A to LDS by loads of whole
-// rows, 1 KB each, and reads fragments there: straight to registers a fragment takes as
-// much of the way from the cache whether its 16 rows differ or not (1 x 14336 x 4096: 11.6
-// us, staged 10.1).
-template <int KIND, int TM, int NF, bool STAGED>
+// Waits until at most n loads of this wave are on the way (n: 1 to MAX, the same in all lanes).
+template <int MAX>
+__device__ __forceinline__ void all_but(int n) {
+    if constexpr (MAX > 1) {
+        if (n < MAX) return all_but<MAX - 1>(n);
+    }
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(MAX) : "memory");
+}
+
+// How a 16-bit A gets to the lanes.  Straight to registers a fragment takes as much of the
+// way from the cache whether its 16 rows differ or not (1 x 14336 x 4096: 11.6 us), so
+// where A's rows begin at whole words they go through a wave's own part of LDS:
+//  ROWS : the rows of whole units, 1 KB to a load, of 8 rows at most (8.8 us);
+//  STEPS: 128 elements of 4 rows to a load, a step ahead of their use.
+enum { STRAIGHT = 0, ROWS = 1, STEPS = 2 };
+
+// MR rows (16 TM, or as many of them as LDS has room for) x 16 NF columns.  (Codes of four
+// units on the way at once, or A's lines touched ahead, gave nothing.)
+template <int KIND, int TM, int NF, int HOW>
 __global__ void __launch_bounds__(NT) mx4_few(Mx4GemmArgs a) {
-    constexpr int MR = 16 * TM, NC = 16 * NF, REGS = TM * NF * 256, PER = (REGS + NT - 1) / NT;
-    constexpr int AP = KIND == CODES ? 4 : 16;     // 16-byte pieces of A in a unit, of a lane
-    extern __shared__ __attribute__((aligned(16))) char lds[];   // the waves' sums; STAGED before: [wave][row] 1 KB of A
+    constexpr int MR = mx4_few_rows(TM), NC = 16 * NF, REGS = TM * NF * 256, PER = (REGS + NT - 1) / NT;
+    constexpr bool CHECK = KIND == IN_F16 && HOW == STEPS;   // FP16: are the scales in its range?
+    extern __shared__ __attribute__((aligned(16))) char lds[];   // A, see above; then the waves' sums
     float *red = reinterpret_cast<float *>(lds);
     __shared__ int is_last;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -116,91 +131,194 @@ __global__ void __launch_bounds__(NT) mx4_few(Mx4GemmArgs a) {
     for (int t = 0; t < TM; ++t)
 #pragma unroll
         for (int f = 0; f < NF; ++f) acc[t][f] = f32x4{0.f, 0.f, 0.f, 0.f};
-    auto one = [&](auto wholec, int u) __attribute__((always_inline)) {
-        constexpr bool WHOLE = decltype(wholec)::value;
-        constexpr bool LDS_A = STAGED && WHOLE;
-        u32x4 w[NF][4], s[NF], x[TM][LDS_A ? 1 : AP], sx[TM];
-        char *own = lds + wave * (a.a_rows * 1024);
-        if constexpr (LDS_A) {
-            // chunk c of row r at c ^ r, so that 16 rows' reads fall on distinct banks
-            const uint32_t to = dtl::lds_addr(own);
-            const char *base = a.A + (int64_t)(begin + m0) * a.a_rs + u * (4 * UNIT);
-#pragma unroll 1
-            for (int r = 0; r < min(M - m0, MR); ++r) dtl::lds_load16(base + r * a.a_rs, 16 * (lane ^ r), to + r * 1024);
-        }
-        auto piece = [&](const char *row, int at, int bytes) __attribute__((always_inline)) {
-            return WHOLE ? *reinterpret_cast<const u32x4_any *>(row + at) : row_piece(row, at, bytes);
-        };
-        auto scales = [&](const char *row, int64_t cs) __attribute__((always_inline)) {
-            return WHOLE ? *reinterpret_cast<const u32x4_any *>(row + 16 * u) : load_part<1>(row + 16 * u * cs, cs, min(a.blocks - 16 * u, 16));
-        };
-        // all loads at once, in the order of use
+    // the products of a step (128 elements) of row blocks t0 on and columns f: codes w, scales
+    // s.  one: the codes are taken times their scale
+    auto step16 = [&](auto one, const u32x4 w, uint32_t s, int f, int t0, const auto &x) __attribute__((always_inline)) {
+        constexpr int T = sizeof(x) / sizeof(x[0]);
+        const u32x4 q = exchange(w);
 #pragma unroll
-        for (int f = 0; f < NF; ++f) s[f] = scales(srow[f], a.s_cs);
-        if constexpr (KIND == CODES) {
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (decltype(one)::value) {
+                // byte i of the word at the exponent's bits, the only ones that count
+                const u32x4 y = decode<KIND>(q[i], __builtin_bit_cast(float, i < 3 ? s << (23 - 8 * i) : s >> 1));
 #pragma unroll
-            for (int t = 0; t < TM; ++t) sx[t] = scales(sarow[t], a.sa_cs);
-        }
-        const int at = u * UNIT + 16 * g, x_at = KIND == CODES ? at : u * (4 * UNIT) + 16 * g;
+                for (int t = 0; t < T; ++t) acc[t0 + t][f] = dtl::mfma16<KIND>(x[t][i], y, acc[t0 + t][f]);
+            } else {
+                const u32x4 y = decode<KIND>(q[i], 1.0f);
+                const float sc = power((s >> (8 * i)) & 255u);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+                for (int t = 0; t < T; ++t) {
+                    const f32x4 b = dtl::mfma16<KIND>(x[t][i], y, f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-            for (int f = 0; f < NF; ++f) w[f][j] = piece(wrow[f], at + 64 * j, a.row_bytes);
-            if constexpr (!LDS_A) {
-#pragma unroll
-                for (int t = 0; t < TM; ++t)
-#pragma unroll
-                    for (int i = j * (AP / 4); i < (j + 1) * (AP / 4); ++i) x[t][i] = piece(arow[t], x_at + 64 * i, KIND == CODES ? a.row_bytes : 2 * a.K);
+                    for (int r = 0; r < 4; ++r) acc[t0 + t][f][r] = fmaf(sc, b[r], acc[t0 + t][f][r]);
+                }
+                __builtin_amdgcn_sched_barrier(0);   // (registers)
             }
         }
-        if constexpr (LDS_A) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(5 * NF) : "memory");   // A, but not the codes
-        else __builtin_amdgcn_sched_barrier(0);
-        const int row = min(n, M - m0 - 1);
-        auto fragment = [&](int t, int i) __attribute__((always_inline)) {
-            if constexpr (LDS_A) return *reinterpret_cast<const u32x4 *>(own + row * 1024 + 16 * ((4 * i + g) ^ row));
-            else return x[t][i];
-        };
+    };
+    auto step4 = [&](const u32x4 w, uint32_t s, int f, const u32x4 (&x)[TM], const uint32_t (&sx)[TM]) __attribute__((always_inline)) {
+        const i32x8 y = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int t = 0; t < TM; ++t) {
+            const i32x8 v = {(int)x[t][0], (int)x[t][1], (int)x[t][2], (int)x[t][3], 0, 0, 0, 0};
+            acc[t][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v, y, acc[t][f], 4, 4, 0, (int)(sx[t] >> (8 * g)), 0, (int)(s >> (8 * g)));
+        }
+    };
+
+    // A unit as it comes: an end in it, scales apart, or (FP16) scales that FP16 does not hold.
+    auto any_unit = [&](int u) __attribute__((always_inline)) {
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+            const int at = u * UNIT + 16 * g + 64 * j, b = 16 * u + 4 * j;
+            auto scales = [&](const char *row, int64_t cs) __attribute__((always_inline)) {
+                uint32_t v = 0;
 #pragma unroll
-            for (int f = 0; f < NF; ++f) {
-                if constexpr (KIND == CODES) {
-                    const i32x8 y = {(int)w[f][j][0], (int)w[f][j][1], (int)w[f][j][2], (int)w[f][j][3], 0, 0, 0, 0};
+                for (int i = 0; i < 4; ++i)
+                    if (b + i < a.blocks) v |= (uint32_t)*reinterpret_cast<const uint8_t *>(row + (b + i) * cs) << (8 * i);
+                return v;
+            };
+            if constexpr (KIND == CODES) {
+                u32x4 x[TM];
+                uint32_t sx[TM];
 #pragma unroll
-                    for (int t = 0; t < TM; ++t) {
-                        const i32x8 v = {(int)x[t][j][0], (int)x[t][j][1], (int)x[t][j][2], (int)x[t][j][3], 0, 0, 0, 0};
-                        acc[t][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v, y, acc[t][f], 4, 4, 0, (int)(sx[t][j] >> (8 * g)), 0, (int)(s[f][j] >> (8 * g)));
-                    }
-                } else {
-                    const u32x4 q = exchange(w[f][j]);
+                for (int t = 0; t < TM; ++t) { x[t] = row_piece(arow[t], at, a.row_bytes); sx[t] = scales(sarow[t], a.sa_cs); }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        // byte i of the word as a power of two, or where only its exponent counts
-                        const float sc = KIND == IN_F16 ? power((s[f][j] >> (8 * i)) & 255u)
-                                                        : __builtin_bit_cast(float, i < 3 ? s[f][j] << (23 - 8 * i) : s[f][j] >> 1);
-                        const u32x4 y = decode<KIND>(q[i], KIND == IN_BF16 ? sc : 1.0f);
+                for (int f = 0; f < NF; ++f) step4(row_piece(wrow[f], at, a.row_bytes), scales(srow[f], a.s_cs), f, x, sx);
+            } else {
+                u32x4 w[NF];
+                uint32_t sw[NF];
 #pragma unroll
-                        for (int t = 0; t < TM; ++t) {
-                            if constexpr (KIND == IN_BF16) acc[t][f] = dtl::mfma16<KIND>(fragment(t, 4 * j + i), y, acc[t][f]);
-                            else {
-                                const f32x4 b = dtl::mfma16<KIND>(fragment(t, 4 * j + i), y, f32x4{0.f, 0.f, 0.f, 0.f});
+                for (int f = 0; f < NF; ++f) { w[f] = row_piece(wrow[f], at, a.row_bytes); sw[f] = scales(srow[f], a.s_cs); }
 #pragma unroll
-                                for (int r = 0; r < 4; ++r) acc[t][f][r] = fmaf(sc, b[r], acc[t][f][r]);
-                            }
-                        }
+                for (int t = 0; t < TM; ++t) {
+                    u32x4 x[1][4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[0][i] = row_piece(arow[t], u * (4 * UNIT) + 16 * g + 256 * j + 64 * i, 2 * a.K);
+#pragma unroll
+                    for (int f = 0; f < NF; ++f) {
+                        step16(Int<KIND == IN_BF16>(), w[f], sw[f], f, t, x);
+                        __builtin_amdgcn_sched_barrier(0);
                     }
                 }
             }
+        }
     };
-    // units without an end in them, whose scales lie side by side
-    const int whole = a.s_cs == 1 && (KIND != CODES || a.sa_cs == 1) ? min(u1, a.K / (2 * UNIT)) : u0;
-    int u = u0 + wave;
-#pragma unroll 1
-    for (; u < whole; u += WAVES) one(Int<1>(), u);
-#pragma unroll 1
-    for (; u < u1; u += WAVES) one(Int<0>(), u);
 
-    if (STAGED) __syncthreads();                   // every wave has read its rows of A
+    // Units without an end in them, whose scales lie side by side.
+    const int whole = a.s_cs == 1 && (KIND != CODES || a.sa_cs == 1) ? min(u1, a.K / (2 * UNIT)) : u0;
+    const int rows = min(M - m0, MR);
+    const char *base = a.A + (int64_t)(begin + m0) * a.a_rs;
+    char *own = lds + wave * (HOW == STEPS ? 2 * ((a.a_rows + 3) / 4) * 1024 : a.a_rows * 1024);
+    const uint32_t to = dtl::lds_addr(own);
+    // STEPS: load i brings rows 4 i to 4 i + 3, chunk c of row r at c ^ r % 16 (16 rows' reads
+    // fall on distinct banks; ROWS: c ^ r)
+    constexpr int LOADS = (MR + 3) / 4;
+    const int loads = (rows + 3) / 4, flip = 1024 * ((a.a_rows + 3) / 4);
+    uint32_t a_off[LOADS];
+    if constexpr (HOW == STEPS) {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i)
+            a_off[i] = (uint32_t)min(4 * i + g, rows - 1) * (uint32_t)a.a_rs + 16 * (n ^ ((4 * i + g) & 15));
+    }
+    auto load_step = [&](int u, int j) __attribute__((always_inline)) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // what was there has been read
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i)
+            if (i < loads) dtl::lds_load16(base + u * (4 * UNIT) + j * UNIT, a_off[i], to + (j & 1) * flip + i * 1024);
+    };
+    int u = u0 + wave;
+    auto whole_units = [&]() __attribute__((always_inline)) {
+        if constexpr (HOW == STEPS) {
+            if (u < whole) load_step(u, 0);
+        }
+#pragma unroll 1
+        for (; u < whole; u += WAVES) {
+            u32x4 w[NF][4], s[NF], x4[TM][4], sx[TM];
+            if constexpr (HOW == ROWS) {
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the last unit's have been read
+#pragma unroll 1
+                for (int r = 0; r < rows; ++r) dtl::lds_load16(base + (int64_t)r * a.a_rs + u * (4 * UNIT), 16 * (lane ^ r), to + r * 1024);
+            }
+            // all loads at once, in the order of use
+#pragma unroll
+            for (int f = 0; f < NF; ++f) s[f] = *reinterpret_cast<const u32x4_any *>(srow[f] + 16 * u);
+            if constexpr (KIND == CODES) {
+#pragma unroll
+                for (int t = 0; t < TM; ++t) sx[t] = *reinterpret_cast<const u32x4_any *>(sarow[t] + 16 * u);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                for (int f = 0; f < NF; ++f) w[f][j] = *reinterpret_cast<const u32x4_any *>(wrow[f] + u * UNIT + 16 * g + 64 * j);
+                if constexpr (KIND == CODES) {
+#pragma unroll
+                    for (int t = 0; t < TM; ++t) x4[t][j] = *reinterpret_cast<const u32x4_any *>(arow[t] + u * UNIT + 16 * g + 64 * j);
+                }
+            }
+            if constexpr (HOW == ROWS) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(5 * NF) : "memory");   // A, but not the codes
+            else __builtin_amdgcn_sched_barrier(0);
+            if constexpr (CHECK) {
+                // FP16 holds codes times 2^-23 .. 2^13; zeros whatever their scale, if it is a number
+                uint32_t far = 0;
+#pragma unroll
+                for (int f = 0; f < NF; ++f)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const u32x4 c = w[f][j];
+                        const uint32_t b = (s[f][j] >> (8 * g)) & 255u, some = (c[0] | c[1] | c[2] | c[3]) & 0x77777777u;
+                        far |= b - 104u > 36u && (some != 0 || b == 255u);
+                    }
+                if (__builtin_amdgcn_ballot_w64(far != 0)) break;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (KIND == CODES) {
+                    u32x4 x[TM];
+                    uint32_t sj[TM];
+#pragma unroll
+                    for (int t = 0; t < TM; ++t) { x[t] = x4[t][j]; sj[t] = sx[t][j]; }
+#pragma unroll
+                    for (int f = 0; f < NF; ++f) step4(w[f][j], s[f][j], f, x, sj);
+                } else {
+                    u32x4 x[TM][4];
+                    if constexpr (HOW == STEPS) {
+                        load_step(j < 3 || u + WAVES >= whole ? u : u + WAVES, (j + 1) & 3);   // (at the end: one that is not used)
+                        all_but<LOADS>(loads);
+                    }
+#pragma unroll
+                    for (int t = 0; t < TM; ++t) {
+                        const int r = min(16 * t + n, rows - 1);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int c = 16 * j + 4 * i + g;   // chunk of the unit
+                            if constexpr (HOW == STEPS) x[t][i] = *reinterpret_cast<const u32x4 *>(own + (j & 1) * flip + r * 256 + 16 * ((c & 15) ^ (r & 15)));
+                            else if constexpr (HOW == ROWS) x[t][i] = *reinterpret_cast<const u32x4 *>(own + r * 1024 + 16 * (c ^ r));
+                            else x[t][i] = *reinterpret_cast<const u32x4_any *>(arow[t] + u * (4 * UNIT) + 16 * c);
+                        }
+                    }
+#pragma unroll
+                    for (int f = 0; f < NF; ++f) step16(Int<KIND == IN_BF16 || CHECK>(), w[f][j], s[f][j], f, 0, x);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+        }
+    };
+    if constexpr (CHECK) {                         // (each there once: registers)
+#pragma unroll 1
+        while (true) {
+            whole_units();
+            if (u >= u1) break;
+            any_unit(u);
+            u += WAVES;
+        }
+    } else {
+        whole_units();
+#pragma unroll 1
+        for (; u < u1; u += WAVES) any_unit(u);
+    }
+
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    if (HOW != STRAIGHT) __syncthreads();          // every wave has read its rows of A, none is on the way
     // the waves' sums: register r of lane (g, n) is C[16 t + 4 g + r][16 f + n]
 #pragma unroll
     for (int t = 0; t < TM; ++t)
@@ -244,10 +362,10 @@ __global__ void __launch_bounds__(NT) mx4_few(Mx4GemmArgs a) {
     }
 }
 
-template <int KIND, int TM, int NF, bool STAGED>
+template <int KIND, int TM, int NF, int HOW>
 hipError_t launch(const Mx4GemmArgs &a, int64_t units, hipStream_t s) {
-    const auto k = mx4_few<KIND, TM, NF, STAGED>;
-    const int bytes = std::max(WAVES * TM * NF * 1024, STAGED ? WAVES * a.a_rows * 1024 : 0);
+    const auto k = mx4_few<KIND, TM, NF, HOW>;
+    const int lines = HOW == ROWS ? a.a_rows : HOW == STEPS ? 2 * ((a.a_rows + 3) / 4) : 0, bytes = WAVES * 1024 * std::max(TM * NF, lines);
     if (bytes > 64 * 1024) {
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(k), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;
@@ -255,21 +373,27 @@ hipError_t launch(const Mx4GemmArgs &a, int64_t units, hipStream_t s) {
     hipLaunchKernelGGL(k, dim3((unsigned)units), dim3(NT), bytes, s, a);
     return hipGetLastError();
 }
-
+template <int KIND, int TM, int HOW>
+hipError_t launch_columns(int nf, const Mx4GemmArgs &a, int64_t units, hipStream_t s) {
+    return nf == 1 ? launch<KIND, TM, 1, HOW>(a, units, s) : nf == 2 ? launch<KIND, TM, 2, HOW>(a, units, s) : hipErrorInvalidValue;
+}
 template <int KIND>
-hipError_t launch_rows(int nf, const Mx4GemmArgs &a, int64_t units, hipStream_t s) {
-    if (a.a_rows) return nf == 1 ? launch<KIND, 1, 1, true>(a, units, s) : launch<KIND, 1, 2, true>(a, units, s);
-    return nf == 1 ? launch<KIND, 1, 1, false>(a, units, s) : launch<KIND, 1, 2, false>(a, units, s);
+hipError_t launch_half(int tm, int nf, const Mx4GemmArgs &a, int64_t units, hipStream_t s) {
+    if (tm == 1 && nf == 1 && a.a_rows == 0) return launch<KIND, 1, 1, STRAIGHT>(a, units, s);
+    if (a.a_rows <= 0 || a.a_rows > mx4_few_rows(tm)) return hipErrorInvalidValue;
+    if (tm == 1 && nf == 1 && a.a_rows <= 8 && !a.offsets) return launch<KIND, 1, 1, ROWS>(a, units, s);
+    if (tm == 1) return launch_columns<KIND, 1, STEPS>(nf, a, units, s);
+    if (tm == 2) return launch_columns<KIND, 2, STEPS>(nf, a, units, s);
+    return tm == 3 ? launch_columns<KIND, 3, STEPS>(nf, a, units, s) : hipErrorInvalidValue;
 }
 
 }  // namespace
 
 hipError_t launch_mx4_few(int kind, int tm, int nf, const Mx4GemmArgs &a, int64_t units, hipStream_t s) {
-    if (nf != 1 && nf != 2) return hipErrorInvalidValue;
-    if (kind == MX4_CODES && tm == 1) return nf == 1 ? launch<CODES, 1, 1, false>(a, units, s) : launch<CODES, 1, 2, false>(a, units, s);
-    if (kind == MX4_CODES && tm == 2) return nf == 1 ? launch<CODES, 2, 1, false>(a, units, s) : launch<CODES, 2, 2, false>(a, units, s);
-    if (kind == IN_BF16 && tm == 1) return launch_rows<IN_BF16>(nf, a, units, s);
-    if (kind == IN_F16 && tm == 1) return launch_rows<IN_F16>(nf, a, units, s);
+    if (kind == MX4_CODES && tm == 1) return launch_columns<CODES, 1, STRAIGHT>(nf, a, units, s);
+    if (kind == MX4_CODES && tm == 2) return launch_columns<CODES, 2, STRAIGHT>(nf, a, units, s);
+    if (kind == IN_BF16) return launch_half<IN_BF16>(tm, nf, a, units, s);
+    if (kind == IN_F16) return launch_half<IN_F16>(tm, nf, a, units, s);
     return hipErrorInvalidValue;
 }
 

@@ -5,9 +5,10 @@
 //
 // BF16: the weights of a block times their scale are BF16 numbers, exactly (E2M1 has two
 // significant bits), which one instruction converts two at a time; the matrix cores do the
-// rest.  FP16 does not hold every scale: there the codes are converted as they are, a
-// block's sum is formed in FP32 on the matrix cores and enters the FP32 accumulator times
-// its scale.
+// rest.  FP16 does not hold every scale: a workgroup whose scales all lie in its range goes
+// the same way, in another the codes are converted as they are, a block's sum is formed in
+// FP32 on the matrix cores and enters the FP32 accumulator times its scale (2048 x 4096 x
+// 4096: 64 us, 85 that way; BF16 62).
 #include "bytes.hpp"
 #include "device_common.hpp"
 #include "gemm_dtl.hpp"
@@ -75,7 +76,9 @@ __device__ __forceinline__ f32x16 mfma(u32x4 a, u32x4 b, f32x16 c) {
 //  - Loads return in order and every wave issues the same number, so the waits count them.
 //  - A ragged K: parts past the end are not computed; what the last one holds past it is
 //    cleared, scales and codes too, since a large scale makes infinities of what is there.
-// WORDS: the scales come four to a word (side by side, aligned, K in whole groups of 128).
+// WORDS: the scales come four to a word (side by side, aligned, K in whole groups of 128): a
+// load of 64 rows takes as long for a byte of each as for a word, 28 ns (BF16 2048 x 4096 x
+// 4096: 62 us, byte by byte 71).
 template <int IN, int BM, int BN, int WGM, int WGN, bool WORDS>
 __global__ void __launch_bounds__(64 * WGM * WGN) mx4_half(Mx4GemmArgs a) {
     constexpr int NW = WGM * WGN, NT = 64 * NW, WTM = BM / WGM, WTN = BN / WGN, TM = WTM / 32, TN = WTN / 32;

@@ -61,7 +61,7 @@ template <int TN> constexpr int MX4_STORE_LDS = 32 * (32 * TN + 4) * 4;
 template <int TM, int TN, bool ROWS = false>
 __device__ __forceinline__ void mx4_store(const Mx4GemmArgs &a, const Mx4Part &p, const f32x16 (&acc)[TM][TN], int r0, int c0, int lane, char *lds) {
     constexpr int PITCH = 32 * TN + 4, CPR = 4 * TN;   // floats of a row, chunks of 8 columns in it
-    const int l = lane & 31, h = lane >> 5, esize = a.out_kind == OUT_F32 ? 4 : 2;
+    const int l = lane & 31, h = lane >> 5;
     float *buf = reinterpret_cast<float *>(lds);
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
