@@ -218,7 +218,7 @@ dg_status few_product(const Mat &x, const Mat *sx, const Mat &off, const Stack &
     if (r) return r->say("few rows, %dx%d tiles, K in %d pieces, %d workgroups", (int)rows, 16 * nf, a.splits, a.units);
     WsLease lease;
     if (a.splits > 1) {
-        if (lease_workspace(stream, (size_t)units * a.splits * rows * 16 * nf * sizeof(float), (size_t)units, &lease) != hipSuccess) {
+        if (lease_workspace(stream, (size_t)units * a.splits * mx4_few_sums(tm, nf) * sizeof(float), (size_t)units, &lease) != hipSuccess) {
             (void)hipGetLastError();
             return DG_ERR_HIP;
         }

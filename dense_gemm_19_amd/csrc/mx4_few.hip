@@ -87,7 +87,7 @@ enum { STRAIGHT = 0, ROWS = 1, STEPS = 2 };
 // units on the way at once, or A's lines touched ahead, gave nothing.)
 template <int KIND, int TM, int NF, int HOW>
 __global__ void __launch_bounds__(NT) mx4_few(Mx4GemmArgs a) {
-    constexpr int MR = mx4_few_rows(TM), NC = 16 * NF, REGS = TM * NF * 256, PER = (REGS + NT - 1) / NT;
+    constexpr int MR = mx4_few_rows(TM), NC = 16 * NF, REGS = mx4_few_sums(TM, NF), PER = (REGS + NT - 1) / NT;
     constexpr bool CHECK = KIND == IN_F16 && HOW == STEPS;   // FP16: are the scales in its range?
     extern __shared__ __attribute__((aligned(16))) char lds[];   // A, see above; then the waves' sums
     float *red = reinterpret_cast<float *>(lds);
