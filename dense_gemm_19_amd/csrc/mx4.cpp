@@ -199,10 +199,11 @@ dg_status few_product(const Mat &x, const Mat *sx, const Mat &off, const Stack &
     // 32 columns to a workgroup halve the reads of A.  They pay where they still fill the
     // device (N = 14336, K = 4096, 16 rows: BF16 12.9 us beside 16.5, codes 10.4 beside 12.0)
     // or fill it with a long K in two pieces (N = 4096, K = 14336: 32 rows 17.5 beside 20,
-    // 16 rows 14.1 beside 14.5, codes 11.1 beside 11.3), and not for so few rows that A is
-    // little (N = 14336, 1 row: 10.0 beside 8.9; N = 4096, 8 rows: 13.3 beside 12.4).
+    // 16 rows 14.1 beside 14.5, codes 11.1 beside 11.3; 16 rows of 16 experts, N = 7168, K =
+    // 4096: 37 beside 50), and not for so few rows that A is little (N = 57344, 1 row: 29.6
+    // beside 24.1; N = 4096, 8 rows: 13.3 beside 12.4).
     const bool wide = sx || aligned;
-    const int nf = wide && mean > 8 && (tiles >= d.cus || (pieces && 2 * tiles >= d.cus)) ? 2 : 1;
+    const int nf = wide && M > 8 && (tiles >= d.cus || (pieces && 2 * tiles >= d.cus)) ? 2 : 1;
     a.tiles_n = (int)cdiv(N, 16 * nf);
     const int64_t units = (experts ? (M + std::min(q.E + 1, M) * (rows - 1)) / rows : cdiv(M, rows)) * a.tiles_n;
     // K in pieces where two of every tile fit the device at once and K is long (16 x 1024 x

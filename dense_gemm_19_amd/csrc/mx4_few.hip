@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(NT) mx4_few(Mx4GemmArgs a) {
     for (int k = 0; k < PER; ++k) {
         const int i = k * NT + tid, b = i >> 8, t = b / NF, f = b - t * NF;
         const int m = m0 + 16 * t + 4 * ((i >> 4) & 3) + ((i >> 6) & 3), col = n0 + 16 * f + (i & 15);
-        if (i < REGS && m < M && col < a.N)
+        if (i < REGS && m < m0 + rows && col < a.N)
             store_out(a.C + (int64_t)(begin + m) * a.c_rs + (int64_t)col * a.c_cs, a.out_kind, activate(a.act, v[k]));
     }
 }
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(NT) mx4_few(Mx4GemmArgs a) {
 template <int KIND, int TM, int NF, int HOW>
 hipError_t launch(const Mx4GemmArgs &a, int64_t units, hipStream_t s) {
     const auto k = mx4_few<KIND, TM, NF, HOW>;
-    const int lines = HOW == ROWS ? a.a_rows : HOW == STEPS ? 2 * ((a.a_rows + 3) / 4) : 0, bytes = WAVES * 1024 * std::max(TM * NF, lines);
+    const int lines = HOW == ROWS ? a.a_rows : HOW == STEPS ? 2 * ((a.a_rows + 3) / 4) : 0, bytes = WAVES * std::max(4 * mx4_few_sums(TM, NF), 1024 * lines);
     if (bytes > 64 * 1024) {
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(k), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;

@@ -141,8 +141,9 @@ def test_many_rows_of_codes(dg, M, N, K, plan):
 @pytest.mark.parametrize("counts,N,K,kinds", [
     ([300, 0, 520, 200], 4096, 512, {"codes": "ring loads, 128x128", F16: many(128, 256), BF16: many(128, 256)}),
     ([60, 70, 0, 90, 64], 4096, 640, {"codes": "direct loads, 64x64", F16: many(64, 128), BF16: many(64, 128)}),
-    ([1, 5, 0, 30, 2, 9], 4096, 1024, {"codes": few(16, 16), F16: few(16, 16), BF16: few(16, 16)}),
+    ([1, 5, 0, 30, 2, 9], 4096, 1024, {"codes": few(16, 32), F16: few(16, 32), BF16: few(16, 32)}),
     ([1, 0, 0, 1], 70, 4096, {"codes": few(16, 16), F16: few(16, 16), BF16: few(16, 16)}),
+    ([1, 0, 7, 2, 0, 4, 0, 0], 4096, 1100, {"codes": few(16, 32), F16: few(16, 32), BF16: few(16, 32)}),
     ([40, 9, 20, 22, 21], 2048, 520, {"codes": few(32, 32), F16: "", BF16: ""})])
 def test_experts(dg, counts, N, K, kinds):
     g = gen(sum(counts), N)
