@@ -29,13 +29,16 @@ dg_status codes_of(const Stack &q, const Stack &s, int64_t E, int64_t M, int64_t
     return DG_SUCCESS;
 }
 
-// Workgroups of the kernels whose threads take MX4_RUN chunks of 8 elements each.
-dg_status runs(int64_t E, int64_t M, int64_t K, int *chunks, uint32_t *mul, int64_t *units) {
+// Workgroups of the kernels whose threads take `run` chunks of 8 elements each.
+dg_status runs(const Device &d, int64_t E, int64_t M, int64_t K, int *chunks, uint32_t *mul, int *run, int64_t *units) {
     *chunks = (int)(4 * cdiv(K, 32));
     *mul = (uint32_t)((((uint64_t)1 << 32) + *chunks - 1) / *chunks);
     int64_t total;
     if (__builtin_mul_overflow(E, M, &total) || __builtin_mul_overflow(total, (int64_t)*chunks, &total)) return DG_ERR_OVERFLOW;
-    *units = cdiv(total, 256 * MX4_RUN);
+    // One chunk a thread where four leave most of the device idle: 1024 x 4096 quantised in
+    // 3.9 us beside 5.0, 777 x 2055 read in 3.9 beside 5.5.
+    *run = total < 4096 * (int64_t)std::max(d.cus, 1) ? 1 : MX4_RUN;
+    *units = cdiv(total, 256 * *run);
     return fits_a_launch(*units, 256) ? DG_SUCCESS : DG_ERR_OVERFLOW;
 }
 
@@ -70,7 +73,7 @@ dg_status quant_entry(const dg_view *X, const dg_view *Q, const dg_view *S, int 
         const int64_t tiles = (int64_t)a.tiles_m * a.tiles_k;
         if (tiles > INT32_MAX || __builtin_mul_overflow(tiles, x.E, &units) || !fits_a_launch(units, 512)) return DG_ERR_OVERFLOW;
     } else {
-        DG_TRY(runs(x.E, M, K, &a.chunks, &a.chunk_mul, &units));
+        DG_TRY(runs(d, x.E, M, K, &a.chunks, &a.chunk_mul, &a.run, &units));
     }
     return done(launch_mx4_quant(by_columns, a, units, stream), stream);
 }
@@ -97,7 +100,7 @@ dg_status dequant_entry(const dg_view *Q, const dg_view *S, const dg_view *Y, hi
     a.M = (int)M; a.K = (int)K; a.E = (int)y.E;
     a.vec = y.one.cols_contig();
     int64_t units;
-    DG_TRY(runs(y.E, M, K, &a.chunks, &a.chunk_mul, &units));
+    DG_TRY(runs(d, y.E, M, K, &a.chunks, &a.chunk_mul, &a.run, &units));
     return done(launch_mx4_dequant(a, units, stream), stream);
 }
 

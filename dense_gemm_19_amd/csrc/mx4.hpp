@@ -14,9 +14,9 @@ namespace dg {
 
 // ---------------------------------------------------------------- quantiser (mx4_quant.hip)
 
-constexpr int MX4_RUN = 4;         // 8-element chunks of a thread (rows kernels)
+constexpr int MX4_RUN = 4;         // 8-element chunks of a thread (rows kernels), or one
 constexpr int MX4_TILE_M = 256;    // tile of the columns kernel: rows of X, and K
-constexpr int MX4_TILE_K = 256;
+constexpr int MX4_TILE_K = 128;
 
 struct Mx4QuantArgs {
     const char *X; int64_t x_es, x_rs, x_cs;   // [E][M][K]
@@ -26,6 +26,7 @@ struct Mx4QuantArgs {
     int M, K, E;
     int chunks;                                // of a row: 4 * ceil(K / 32)
     uint32_t chunk_mul;                        // ceil(2^32 / chunks), for chunks < 4096
+    int run;                                   // 1 or MX4_RUN
     int tiles_m, tiles_k;                      // columns kernel
     int ceil;                                  // the scale at which nothing saturates
     int vec;                                   // columns kernel: rows of X are adjacent
@@ -40,7 +41,7 @@ struct Mx4DequantArgs {
     char *Y; int64_t y_es, y_rs, y_cs;         // [E][M][K]
     int y_kind;
     int M, K, E;
-    int chunks;
+    int chunks, run;
     uint32_t chunk_mul;
     int vec;                                   // rows of Y are contiguous
 };
