@@ -139,9 +139,14 @@ dg_status codes_product(const Mat &x, const Mat &sx, const Mat &off, const Stack
         const int64_t bm = mx4_tile_m(t);
         return (experts ? std::max(used, used / 2 + cdiv(M, bm)) : cdiv(M, bm)) * cdiv(N, mx4_tile_n(t));
     };
+    // The largest tile that gives three quarters of the CUs work, K = 4096: 256 over 128 at
+    // 192 tiles (1536 x 8192: 40.1 us beside 46.6) and 256 (4096 x 4096: 43.4, 55.4), not at
+    // 128 (2048 x 4096: 38.2, 29.5); 128 over 64 at 224 (256 x 14336: 21.9, 31.8) and 256
+    // (1024 x 4096: 21.1, 27.3), not at 128 (512 x 4096: 16.3, 13.4).
+    auto fills = [&](int t) { return 4 * expected(t) >= 3 * (int64_t)d.cus; };
     int tile = MX4_T64;
-    if (load == MX4_DIRECT && mean > 128 && expected(MX4_T256) >= d.cus) tile = MX4_T256;
-    else if (load != MX4_ANY && mean > 64 && expected(MX4_T128) >= d.cus / 2) tile = MX4_T128;
+    if (load == MX4_DIRECT && mean > 128 && fills(MX4_T256)) tile = MX4_T256;
+    else if (load != MX4_ANY && mean > 64 && fills(MX4_T128)) tile = MX4_T128;
     const int64_t q_es = q.E > 1 ? q.es : 0, s_es = q.E > 1 ? s.es : 0;
     const bool ring = tile != MX4_T64 && bytes % 256 == 0 && a.sa_cs == 1 && a.s_cs == 1 && pieces(x, 0) && pieces(q.one, q_es) && pieces(sx, 0) &&
                       pieces(s.one, s_es);
