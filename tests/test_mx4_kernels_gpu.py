@@ -129,7 +129,10 @@ def test_between_few_and_many(dg, M, N, K, kind):
 # ---------------------------------------------------------------- many rows of codes
 
 @pytest.mark.parametrize("M,N,K,plan", [
-    (4096, 3300, 512, "ring loads, 256x256"), (1030, 2900, 512, "ring loads, 128x128"), (1100, 2900, 1536, "ring loads, 128x128"),
+    (4096, 3300, 512, "ring loads, 256x256"), (1030, 2900, 512, "ring loads, 128x128"),
+    (4096, 4200, 512, "ring loads, 256x256 tiles, K in 1 pieces, 256 workgroups; direct loads, 64x64 tiles"),
+    (4000, 4500, 304, "direct loads, 256x256 tiles, K in 1 pieces, 256 workgroups; direct loads, 64x64 tiles"),
+    (1100, 2900, 1536, "ring loads, 128x128"),
     (4000, 3300, 304, "direct loads, 256x256"), (1030, 2900, 1000, "direct loads, 128x128"), (40, 50, 264, "direct loads, 64x64"),
     (70, 130, 9000, "direct loads, 64x64"), (1100, 2900, 333, "vector loads, 128x128"), (70, 130, 777, "vector loads, 64x64"), (70, 50, 90, "element loads")])
 def test_many_rows_of_codes(dg, M, N, K, plan):
