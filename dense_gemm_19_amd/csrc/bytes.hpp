@@ -53,4 +53,13 @@ __device__ __forceinline__ u32x4 first_bytes(u32x4 v, int n) {
     return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
 }
 
+// 16 bytes from `at` on of a row of `bytes`, zeros past its end.
+__device__ __forceinline__ u32x4 row_piece(const char *row, int at, int bytes) {
+    const int n = bytes - at;
+    if (n >= 16) return *reinterpret_cast<const u32x4_any *>(row + at);
+    if (n <= 0) return u32x4{0u, 0u, 0u, 0u};
+    if (bytes >= 16) return down_bytes(*reinterpret_cast<const u32x4_any *>(row + bytes - 16), 16 - n);
+    return load_part<1>(row + at, 1, n);
+}
+
 }  // namespace dg

@@ -264,8 +264,7 @@ dg_status half_product(const Mat &x, const Mat &off, const Stack &q, const Stack
     const int64_t used = experts ? std::min(q.E, M) : 1, mean = M / used;
     const int64_t s_cs = s.one.cols > 1 ? s.one.cs : 1, near = (int64_t)1 << 31;
     auto at = [](const Mat &m, int64_t es, int64_t n) { return reinterpret_cast<uintptr_t>(m.ptr) % n == 0 && es % n == 0 && (m.rows <= 1 || m.rs % n == 0); };
-    *taken = mean > 48 && K >= 32 && K % 8 == 0 && at(x, 0, 16) && at(q.one, q.E > 1 ? q.es : 0, 4) && (N <= 1 || q.one.rs >= bytes) &&
-             128 * x.rs + 2 * K < near && 256 * q.one.rs + bytes < near && 256 * s.one.rs + s.one.cols * s_cs < near;
+    *taken = mean > 48 && K >= 32 && 128 * x.rs + 2 * K < near && 256 * q.one.rs + bytes < near && 256 * s.one.rs + s.one.cols * s_cs < near;
     if (!*taken) return DG_SUCCESS;
     Device d;
     DG_TRY(ready({&x, &off, &q.span, &s.span, &c}, &d, r));
@@ -282,7 +281,9 @@ dg_status half_product(const Mat &x, const Mat &off, const Stack &q, const Stack
     if (!experts && tile == MX4_T64x128 && 2 * units <= d.cus && ktiles >= 8 && !capturing(stream, r)) splits = std::min<int64_t>(d.cus / units, ktiles / 4);
     // Few rows leave too little work here where the pieces are few, too (64 x 1024 x 8192: 14.2
     // us beside 10.1 of the kernel for few rows; 64 x 4096 x 14336: 21.8 beside 26.8; 64 x
-    // 14336 x 4096: 19.1 beside 30.5; 33 x 4096 x 14336: 21.1 beside 20.6).
+    // 14336 x 4096: 19.1 beside 30.5; 33 x 4096 x 14336: 21.1 beside 20.6).  At any address: 64 x
+    // 14336 x 4100 35 us beside 51, 64 x 4096 x 4100 19.4 beside 17.3, 2048 x 4096 x 4100 93
+    // beside 338.
     *taken = mean > 128 || 2 * splits * expected(bm, bn) >= d.cus;
     if (!*taken) return DG_SUCCESS;
     Mx4GemmArgs a = {};
@@ -296,6 +297,7 @@ dg_status half_product(const Mat &x, const Mat &off, const Stack &q, const Stack
     a.blocks = (int)cdiv(K, 32);
     if (experts) { a.offsets = off.ptr; a.o_s = off.cs; }
     a.E = (int)q.E;
+    a.via = !(K % 8 == 0 && at(x, 0, 16) && at(q.one, q.E > 1 ? q.es : 0, 4) && (N <= 1 || q.one.rs >= bytes));
     a.s_words = K % 128 == 0 && s_cs == 1 && at(s.one, s.E > 1 ? s.es : 0, 4);
     a.tiles_n = (int)cdiv(N, bn);
     a.group_m = 8;
@@ -303,7 +305,7 @@ dg_status half_product(const Mat &x, const Mat &off, const Stack &q, const Stack
     a.splits = (int)cdiv(ktiles, a.kt_per_split);
     if (units > INT32_MAX / a.splits || !fits_a_launch(units * a.splits, 512)) return DG_ERR_OVERFLOW;
     a.units = (int)(units * a.splits);
-    if (r) return r->say("many rows, %dx%d tiles, K in %d pieces, %d workgroups", (int)bm, (int)bn, a.splits, a.units);
+    if (r) return r->say("many rows%s, %dx%d tiles, K in %d pieces, %d workgroups", a.via ? " at any address" : "", (int)bm, (int)bn, a.splits, a.units);
     WsLease lease;
     if (a.splits > 1) {
         if (lease_workspace(stream, (size_t)units * a.splits * bm * bn * sizeof(float), (size_t)units, &lease) != hipSuccess) {

@@ -66,6 +66,7 @@ struct Mx4GemmArgs {
     int units;                                 // workgroups of the grid
     int splits, kt_per_split;                  // K in pieces (one matrix only)
     int s_words;                               // mx4_half.hip: scales at aligned words, K a multiple of 128
+    int via;                                   // mx4_half.hip: any K and alignment, through registers
     int a_rows;                                // mx4_few.hip: rows of a 16-bit A that a workgroup stages in LDS, or 0
     float *ws; int *counters;
 };
@@ -87,8 +88,8 @@ hipError_t launch_mx4_gemm(int tile, int load, const Mx4GemmArgs &a, int64_t uni
 // at multiples of 16 bytes.
 hipError_t launch_mx4_ring(int tile, const Mx4GemmArgs &a, int64_t units, hipStream_t stream);
 
-// 16-bit A (mx4_half.hip): K a multiple of 8 and 32 at least, A's rows at multiples of 16
-// bytes, W's at multiples of 4.
+// 16-bit A (mx4_half.hip): K 32 at least; without `via` a multiple of 8, A's rows at
+// multiples of 16 bytes, W's at multiples of 4 and apart.
 enum Mx4HalfTile : int { MX4_T128x256 = 0, MX4_T64x128 = 1 };
 hipError_t launch_mx4_half(int in_kind, int tile, const Mx4GemmArgs &a, int64_t units, hipStream_t stream);
 

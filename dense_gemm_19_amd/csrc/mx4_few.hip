@@ -32,15 +32,6 @@ constexpr int CODES = MX4_CODES;   // beside IN_F16, IN_BF16
 
 template <int N> using Int = std::integral_constant<int, N>;
 
-// 16 bytes from `at` on of a row of `bytes`, zeros past its end.
-__device__ __forceinline__ u32x4 row_piece(const char *row, int at, int bytes) {
-    const int n = bytes - at;
-    if (n >= 16) return *reinterpret_cast<const u32x4_any *>(row + at);
-    if (n <= 0) return u32x4{0u, 0u, 0u, 0u};
-    if (bytes >= 16) return down_bytes(*reinterpret_cast<const u32x4_any *>(row + bytes - 16), 16 - n);
-    return load_part<1>(row + at, 1, n);
-}
-
 // words[i] of lane row g <- words[g] of lane row i (lane rows of 16 lanes)
 __device__ __forceinline__ u32x4 exchange(u32x4 v) {
     auto s0 = __builtin_amdgcn_permlane32_swap(v[0], v[2], false, false);

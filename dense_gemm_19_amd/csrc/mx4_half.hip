@@ -79,7 +79,10 @@ __device__ __forceinline__ f32x16 mfma(u32x4 a, u32x4 b, f32x16 c) {
 // WORDS: the scales come four to a word (side by side, aligned, K in whole groups of 128): a
 // load of 64 rows takes as long for a byte of each as for a word, 28 ns (BF16 2048 x 4096 x
 // 4096: 62 us, byte by byte 71).
-template <int IN, int BM, int BN, int WGM, int WGN, bool WORDS>
+// VIA: A and W at any alignment, any K: through registers, each load a part (W: a tile) on
+// the way before it is written where a load to LDS would have put it; the end of K apart
+// (BF16 2048 x 4096 x 4100: 93 us).
+template <int IN, int BM, int BN, int WGM, int WGN, bool WORDS, bool VIA>
 __global__ void __launch_bounds__(64 * WGM * WGN) mx4_half(Mx4GemmArgs a) {
     constexpr int NW = WGM * WGN, NT = 64 * NW, WTM = BM / WGM, WTN = BN / WGN, TM = WTM / 32, TN = WTN / 32;
     constexpr bool SPLIT = BM == 64;               // K in pieces
@@ -115,11 +118,16 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_half(Mx4GemmArgs a) {
         w_most[j] = row == last_n ? row_bytes - 16 : (row_bytes - 1) & ~15;
     }
     s_off = (uint32_t)min((wave % SR) * 64 + lane, last_n) * (uint32_t)a.s_rs;
+    u32x4 va[VIA ? AI : 1], vw[VIA ? WI : 1];      // VIA: on the way
+    auto put_a = [&](int j, int t) __attribute__((always_inline)) { *reinterpret_cast<u32x4 *>(lds + (t & 3) * PART + (wave + NW * j) * 1024 + 16 * lane) = va[j]; };
+    auto put_w = [&](int j, int T) __attribute__((always_inline)) { *reinterpret_cast<u32x4 *>(lds + W_OFF + (T & 1) * WTILE + (wave + NW * j) * 1024 + 16 * lane) = vw[j]; };
     auto load_a = [&](int j, int t) __attribute__((always_inline)) {   // chunks past K: the last one
-        load_lds16(pa, a_off[j] + (uint32_t)min(t * KB + chunk, 2 * K - 16), lds0 + (uint32_t)((t & 3) * PART + (wave + NW * j) * 1024));
+        if constexpr (VIA) va[j] = *reinterpret_cast<const u32x4_any *>(pa + (a_off[j] + (uint32_t)min(t * KB + chunk, 2 * K - 16)));
+        else load_lds16(pa, a_off[j] + (uint32_t)min(t * KB + chunk, 2 * K - 16), lds0 + (uint32_t)((t & 3) * PART + (wave + NW * j) * 1024));
     };
     auto load_w = [&](int j, int T) __attribute__((always_inline)) {
-        load_lds16(pw, w_off[j] + (uint32_t)min(T * KB + chunk, w_most[j]), lds0 + (uint32_t)(W_OFF + (T & 1) * WTILE + (wave + NW * j) * 1024));
+        if constexpr (VIA) vw[j] = *reinterpret_cast<const u32x4_any *>(pw + (w_off[j] + (uint32_t)min(T * KB + chunk, row_bytes - 16)));
+        else load_lds16(pw, w_off[j] + (uint32_t)min(T * KB + chunk, w_most[j]), lds0 + (uint32_t)(W_OFF + (T & 1) * WTILE + (wave + NW * j) * 1024));
     };
     auto load_s = [&](int j, int T) __attribute__((always_inline)) {   // one block, or word, of 64 rows
         const int b = wave / SR + (NW / SR) * j;
@@ -211,7 +219,7 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_half(Mx4GemmArgs a) {
             next(3);
             multiply(Int<2>(), Q);
             if constexpr (decltype(more)::value) {
-                arrive<decltype(left)::value>();
+                arrive<VIA ? 0 : decltype(left)::value>();
 #pragma unroll
                 for (int i = 0; i < TM; ++i) read_a(0, i, (Q + 1) & 3);
 #pragma unroll
@@ -223,7 +231,14 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_half(Mx4GemmArgs a) {
                 }
                 if constexpr (decltype(refill)::value) {
 #pragma unroll
-                    for (int j = 0; j < AI; ++j) load_a(j, t + 4);
+                    for (int j = 0; j < AI; ++j) {
+                        if constexpr (VIA) put_a(j, t + 3);
+                        load_a(j, t + 4);
+                    }
+                }
+                if constexpr (VIA && decltype(refill)::value && Q == 0) {
+#pragma unroll
+                    for (int j = 0; j < WI; ++j) put_w(j, T + 1);
                 }
                 if constexpr (decltype(refill)::value && Q == 3) {
 #pragma unroll
@@ -238,7 +253,7 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_half(Mx4GemmArgs a) {
 
         const int whole = K / 64;                  // parts without an end in them
         if (whole > 0) {
-            arrive<3 * AI + WI>();
+            arrive<VIA ? 0 : 3 * AI + WI>();
 #pragma unroll
             for (int i = 0; i < TM; ++i) read_a(0, i, 0);
 #pragma unroll
@@ -253,6 +268,10 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_half(Mx4GemmArgs a) {
             part(Int<1>(), Yes(), Yes(), Int<2 * AI + WI + S1>(), T);
             part(Int<2>(), Yes(), Yes(), Int<2 * AI + SI>(), T);
             part(Int<3>(), Yes(), Yes(), Int<2 * AI>(), T);
+        }
+        if constexpr (VIA) {
+#pragma unroll
+            for (int j = 0; j < AI; ++j) put_a(j, 4 * T + 3);
         }
         // the last one to four whole parts
         const int rest = whole - 4 * T;
@@ -274,19 +293,30 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_half(Mx4GemmArgs a) {
             if (q == 0 && t > 0) {                 // the first of its tile: no part before loaded these
 #pragma unroll
                 for (int j = 0; j < SI; ++j) load_s(j, TT);
+                if constexpr (!VIA) {
 #pragma unroll
-                for (int j = 0; j < AI; ++j) load_a(j, t);
+                    for (int j = 0; j < AI; ++j) load_a(j, t);
+                }
             }
             arrive<0>();
+            if constexpr (VIA) {
 #pragma unroll 1
-            for (int i = tid; i < BM * 8; i += NT)   // A: chunks from K on (K is a multiple of 8)
-                if (64 * t + 8 * ((i & 7) ^ ((i >> 4) & 7)) >= K) *reinterpret_cast<u32x4 *>(lds + (t & 3) * PART + 16 * i) = u32x4{0u, 0u, 0u, 0u};
-            if (n != 0) {                          // W: the last chunk of the rows
+                for (int i = tid; i < BM * 8; i += NT)
+                    *reinterpret_cast<u32x4 *>(lds + (t & 3) * PART + 16 * i) = row_piece(pa + (uint32_t)min(i >> 3, last_m) * (uint32_t)a.a_rs, t * KB + 16 * ((i & 7) ^ ((i >> 4) & 7)), 2 * K);
 #pragma unroll 1
-                for (int r = tid; r < BN; r += NT) {
-                    u32x4 *c = reinterpret_cast<u32x4 *>(lds + W_OFF + (TT & 1) * WTILE + r * KB + (((left >> 4) ^ ((r >> 1) & 7)) << 4));
-                    *c = r >= last_n ? down_bytes(*c, 16 - n) : first_bytes(*c, n);
-                }
+                for (int i = tid; i < BN * 8; i += NT)
+                    *reinterpret_cast<u32x4 *>(lds + W_OFF + (TT & 1) * WTILE + 16 * i) = row_piece(pw + (uint32_t)min(i >> 3, last_n) * (uint32_t)a.q_rs, TT * KB + 16 * ((i & 7) ^ ((i >> 4) & 7)), row_bytes);
+            } else {
+#pragma unroll 1
+                for (int i = tid; i < BM * 8; i += NT)   // A: chunks from K on (K is a multiple of 8)
+                    if (64 * t + 8 * ((i & 7) ^ ((i >> 4) & 7)) >= K) *reinterpret_cast<u32x4 *>(lds + (t & 3) * PART + 16 * i) = u32x4{0u, 0u, 0u, 0u};
+                if (n != 0) {                          // W: the last chunk of the rows
+#pragma unroll 1
+                    for (int r = tid; r < BN; r += NT) {
+                        u32x4 *c = reinterpret_cast<u32x4 *>(lds + W_OFF + (TT & 1) * WTILE + r * KB + (((left >> 4) ^ ((r >> 1) & 7)) << 4));
+                        *c = r >= last_n ? down_bytes(*c, 16 - n) : first_bytes(*c, n);
+                    }
+            }
             }
 #pragma unroll 1
             for (int i = tid; i < 8 * BN; i += NT)   // scales of blocks past the end
@@ -309,7 +339,10 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_half(Mx4GemmArgs a) {
     if (parts > 0) {
         // as the four parts before the first would have issued them
 #pragma unroll
-        for (int j = 0; j < WI; ++j) load_w(j, 0);
+        for (int j = 0; j < WI; ++j) {
+            load_w(j, 0);
+            if constexpr (VIA) put_w(j, 0);
+        }
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             if (t < 2) {
@@ -317,7 +350,10 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_half(Mx4GemmArgs a) {
                 for (int j = t * S1; j < (t ? SI : S1); ++j) load_s(j, 0);
             }
 #pragma unroll
-            for (int j = 0; j < AI; ++j) load_a(j, t);
+            for (int j = 0; j < AI; ++j) {
+                load_a(j, t);
+                if (VIA && t < 3) put_a(j, t);
+            }
         }
 #pragma unroll
         for (int j = 0; j < WI; ++j) load_w(j, 1);   // (past the end: the rows' ends)
@@ -380,8 +416,9 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_half(Mx4GemmArgs a) {
 hipError_t launch_mx4_half(int in_kind, int tile, const Mx4GemmArgs &a, int64_t units, hipStream_t s) {
 #define DG_HALF(IN, BM, BN, GM, GN)                                                                                                                     \
     do {                                                                                                                                                \
-        if (a.s_words) hipLaunchKernelGGL((mx4_half<IN, BM, BN, GM, GN, true>), dim3((unsigned)units), dim3(64 * GM * GN), 0, s, a);                    \
-        else hipLaunchKernelGGL((mx4_half<IN, BM, BN, GM, GN, false>), dim3((unsigned)units), dim3(64 * GM * GN), 0, s, a);                             \
+        if (a.via) hipLaunchKernelGGL((mx4_half<IN, BM, BN, GM, GN, false, true>), dim3((unsigned)units), dim3(64 * GM * GN), 0, s, a);                 \
+        else if (a.s_words) hipLaunchKernelGGL((mx4_half<IN, BM, BN, GM, GN, true, false>), dim3((unsigned)units), dim3(64 * GM * GN), 0, s, a);        \
+        else hipLaunchKernelGGL((mx4_half<IN, BM, BN, GM, GN, false, false>), dim3((unsigned)units), dim3(64 * GM * GN), 0, s, a);                      \
     } while (0)
     if (tile == MX4_T128x256 && in_kind == IN_BF16) DG_HALF(IN_BF16, 128, 256, 2, 4);
     else if (tile == MX4_T128x256) DG_HALF(IN_F16, 128, 256, 2, 4);

@@ -120,6 +120,30 @@ def test_scales_at_odd_addresses(dg, kind):
     run(dg, kind, 140, 200, 1056, many(64, 128))
 
 
+@pytest.mark.parametrize("M,N,K,rows,cols,pieces", [
+    (65, 8200, 333, 64, 128, 1), (129, 100, 1001, 64, 128, 1), (140, 70, 33, 64, 128, 1), (200, 300, 8201, 64, 128, 8), (150, 130, 2564, 64, 128, 2),
+    (1030, 4400, 614, 128, 256, 1), (1100, 4096, 260, 128, 256, 1), (1100, 4096, 75, 128, 256, 1)])
+@pytest.mark.parametrize("kind", [F16, BF16])
+def test_many_rows_of_16_bits_at_any_address(dg, M, N, K, rows, cols, pieces, kind):
+    plan = many(rows, cols, pieces).replace("rows,", "rows at any address,")
+    run(dg, kind, M, N, K, plan, lambda t: in_ones(t) if t.dtype == U8 else t.to(DEV), out=[F32, kind][M % 2])
+
+
+@pytest.mark.parametrize("K", [256, 320, 584, 1024, 1152])
+@pytest.mark.parametrize("kind", [F16, BF16])
+def test_many_rows_whose_addresses_are_odd(dg, K, kind):
+    # a K that would do, rows that do not: A at odd multiples of 2 bytes, what lies between its rows NaN
+    def place(t):
+        if t.dtype == U8:
+            return in_ones(t)
+        buf = torch.full((t.shape[0] * (K + 3) + 1,), NAN, dtype=kind, device=DEV)
+        v = buf[1:].view(-1, K + 3)[:, :K]
+        v.copy_(t)
+        return v
+    run(dg, kind, 140, 300, K, "many rows at any address, 64x128", place)
+    run(dg, kind, 1100, 4096, K, "many rows at any address, 128x256", place)
+
+
 @pytest.mark.parametrize("M,N,K", [(40, 100, 1024), (48, 5000, 333), (20, 4200, 512), (33, 70, 1001)])
 @pytest.mark.parametrize("kind", [F16, BF16])
 def test_between_few_and_many(dg, M, N, K, kind):
@@ -143,6 +167,7 @@ def test_many_rows_of_codes(dg, M, N, K, plan):
 
 @pytest.mark.parametrize("counts,N,K,kinds", [
     ([300, 0, 520, 200], 4096, 512, {"codes": "ring loads, 128x128", F16: many(128, 256), BF16: many(128, 256)}),
+    ([300, 0, 520, 200], 4096, 333, {"codes": "vector loads, 128x128", F16: "many rows at any address, 128x256", BF16: "many rows at any address, 128x256"}),
     ([60, 70, 0, 90, 64], 4096, 640, {"codes": "direct loads, 64x64", F16: many(64, 128), BF16: many(64, 128)}),
     ([1, 5, 0, 30, 2, 9], 4096, 1024, {"codes": few(16, 32), F16: few(16, 32), BF16: few(16, 32)}),
     ([1, 0, 0, 1], 70, 4096, {"codes": few(16, 16), F16: few(16, 16), BF16: few(16, 16)}),
