@@ -272,13 +272,18 @@ dg_status half_product(const Mat &x, const Mat &off, const Stack &q, const Stack
     const int tile = expected(128, 256) > d.cus / 2 ? MX4_T128x256 : MX4_T64x128;
     const int64_t bm = tile == MX4_T128x256 ? 128 : 64, bn = 2 * bm;
     const int64_t units = experts ? ((M + std::min(q.E + 1, M) * (bm - 1)) / bm) * cdiv(N, bn) : cdiv(M, bm) * cdiv(N, bn);
-    // K in pieces of whole tiles of 256, four at least, where that fills idle CUs but each
-    // only once (64 x 4096 x 14336, 32 tiles: 71.9 us whole, 26.7 in four pieces, 21.8 in
-    // eight, 28.1 in 16; 64 x 4096 x 4096: 14.7 in two, 12.6 in four, 14.2 in eight).  A
-    // captured call runs whole, as above.
+    // K in pieces of whole tiles of 256 where that fills idle CUs but each only once: of four
+    // tiles (64 x 4096 x 4096: 14.7 us in two pieces, 12.6 in four, 14.2 in eight; 64 x 4096 x
+    // 14336, 32 tiles of C: 71.9 whole, 26.7 in four, 21.8 in eight, 28.1 in 16), of two where
+    // a tile of K takes longer (any address: 150 x 1000 x 4100 18.9 in eight, 21.8 in four) or
+    // four pieces are not reached (309 x 160 x 1792: 10.3 in three, 11.0 whole; with four
+    // tiles in all, 129 x 1024 x 1024, 10.9 in two, 10.4 whole).  A captured call runs whole,
+    // as above.
     const int64_t ktiles = std::max<int64_t>(K / 256, 1);
     int64_t splits = 1;
-    if (!experts && tile == MX4_T64x128 && 2 * units <= d.cus && ktiles >= 8 && !capturing(stream, r)) splits = std::min<int64_t>(d.cus / units, ktiles / 4);
+    const bool via = !(K % 8 == 0 && at(x, 0, 16) && at(q.one, q.E > 1 ? q.es : 0, 4) && (N <= 1 || q.one.rs >= bytes));
+    if (!experts && tile == MX4_T64x128 && 2 * units <= d.cus && ktiles >= 6 && !capturing(stream, r))
+        splits = std::min<int64_t>(d.cus / units, std::max<int64_t>(ktiles / (via ? 2 : 4), std::min<int64_t>(4, ktiles / 2)));
     // Few rows leave too little work here where the pieces are few, too (64 x 1024 x 8192: 14.2
     // us beside 10.1 of the kernel for few rows; 64 x 4096 x 14336: 21.8 beside 26.8; 64 x
     // 14336 x 4096: 19.1 beside 30.5; 33 x 4096 x 14336: 21.1 beside 20.6).  At any address: 64 x
@@ -297,7 +302,7 @@ dg_status half_product(const Mat &x, const Mat &off, const Stack &q, const Stack
     a.blocks = (int)cdiv(K, 32);
     if (experts) { a.offsets = off.ptr; a.o_s = off.cs; }
     a.E = (int)q.E;
-    a.via = !(K % 8 == 0 && at(x, 0, 16) && at(q.one, q.E > 1 ? q.es : 0, 4) && (N <= 1 || q.one.rs >= bytes));
+    a.via = via;
     a.s_words = K % 128 == 0 && s_cs == 1 && at(s.one, s.E > 1 ? s.es : 0, 4);
     a.tiles_n = (int)cdiv(N, bn);
     a.group_m = 8;

@@ -105,7 +105,7 @@ def test_scales_of_fp16(dg, M, N, K, plan, change):
 
 @pytest.mark.parametrize("M,N,K,rows,cols,pieces", [
     (65, 8200, 512, 64, 128, 1), (129, 100, 640, 64, 128, 1), (200, 1000, 1160, 64, 128, 1), (129, 70, 32, 64, 128, 1), (200, 300, 8200, 64, 128, 8),
-    (70, 4096, 4096, 64, 128, 4), (64, 4096, 4096, 64, 128, 4), (150, 200, 2568, 64, 128, 2), (1030, 4400, 384, 128, 256, 1), (1100, 4096, 584, 128, 256, 1)])
+    (70, 4096, 4096, 64, 128, 4), (64, 4096, 4096, 64, 128, 4), (150, 200, 2568, 64, 128, 4), (1030, 4400, 384, 128, 256, 1), (1100, 4096, 584, 128, 256, 1)])
 @pytest.mark.parametrize("kind", [F16, BF16])
 def test_many_rows_of_16_bits(dg, M, N, K, rows, cols, pieces, kind):
     run(dg, kind, M, N, K, many(rows, cols, pieces), out=[F32, kind][M % 2])
@@ -121,7 +121,7 @@ def test_scales_at_odd_addresses(dg, kind):
 
 
 @pytest.mark.parametrize("M,N,K,rows,cols,pieces", [
-    (65, 8200, 333, 64, 128, 1), (129, 100, 1001, 64, 128, 1), (140, 70, 33, 64, 128, 1), (200, 300, 8201, 64, 128, 8), (150, 130, 2564, 64, 128, 2),
+    (65, 8200, 333, 64, 128, 1), (129, 100, 1001, 64, 128, 1), (140, 70, 33, 64, 128, 1), (200, 300, 8201, 64, 128, 16), (150, 130, 2564, 64, 128, 5),
     (1030, 4400, 614, 128, 256, 1), (1100, 4096, 260, 128, 256, 1), (1100, 4096, 75, 128, 256, 1)])
 @pytest.mark.parametrize("kind", [F16, BF16])
 def test_many_rows_of_16_bits_at_any_address(dg, M, N, K, rows, cols, pieces, kind):
