@@ -565,8 +565,8 @@ dg_status dg_dequant_mx4(const dg_view *Q, const dg_view *S, const dg_view *Y, h
  * FP32 accumulation, one rounding to C's dtype.  No operand is rounded.
  * Training: with Y = X W^T, dX = dY W is the product of dY and of W's transpose, both
  * quantised along N, and dW = dY^T X that of both transposes quantised along the rows.
- * Codes are quickest where their rows begin at multiples of 4 bytes; 16-bit A where its
- * layout is dg_gemm_w4's quickest one.
+ * Quickest with scales side by side and rows of codes and scales at multiples of 16 bytes,
+ * K a multiple of 512; 16-bit A with its own rows there and K a multiple of 128.
  * Errors: DG_ERR_NULL (codes without SA), DG_ERR_INVALID_ARG (SA with a 16-bit A, act),
  * DG_ERR_DTYPE, DG_ERR_SHAPE_MISMATCH, DG_ERR_UNSUPPORTED_VIEW (A's or Q's rows not
  * contiguous), DG_ERR_STRIDE, DG_ERR_ALIAS, DG_ERR_OVERFLOW (16-bit A: K above 2^20, row

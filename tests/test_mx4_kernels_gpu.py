@@ -213,3 +213,38 @@ def test_pieces_of_every_kernel_on_one_stream(dg):
         stream.synchronize()
         for C, (_, _, want, shape) in zip(outs, order):
             om.check(C, want, str(shape))
+
+
+def test_every_kernel_in_a_graph(dg):
+    # captured together (whole, without workspaces), replayed with other inputs between the program's own calls
+    g = gen(78)
+    calls = []
+    for kind, M, N, K in [("codes", 16, 1000, 8192), (F16, 33, 300, 8192), (BF16, 5, 300, 1024), (BF16, 70, 4096, 4096), (F16, 140, 200, 1001),
+                          ("codes", 70, 130, 2000), ("codes", 4096, 4200, 512), (F16, 40, 300, 2048)]:
+        A, SA = coded(g, M, K, (118, 128)) if kind == "codes" else (normal(g, M, K, dtype=kind, spread=0.5), None)
+        Q, S = coded(g, N, K, (118, 128))
+        calls.append(([t.to(DEV) for t in (A, Q, S)], None if SA is None else SA.to(DEV), torch.zeros(M, N, device=DEV), K))
+
+    def step():
+        for args, sa, C, _ in calls:
+            dg.gemm_mx4(*args, C, SA=sa)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for rep in range(3):
+        for (A, Q, S), sa, C, K in calls:
+            A.copy_(A.roll(rep + 1, 0))
+            C.fill_(NAN)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [C.clone() for _, _, C, _ in calls]
+        step()
+        torch.cuda.synchronize()
+        for (args, sa, C, K), once in zip(calls, got):
+            A, Q, S = (t.cpu() for t in args)
+            want = ox.gemm(A, None if sa is None else sa.cpu(), Q, S, K, 0, F32)
+            om.check(once, want, f"replay {rep}: {tuple(C.shape)} {K}")
+            om.check(C, want, f"call {rep}: {tuple(C.shape)} {K}")
