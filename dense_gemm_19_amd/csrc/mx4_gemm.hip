@@ -5,8 +5,14 @@
 //
 // gfx950 multiplies the format as it is: one v_mfma_scale_f32_32x32x64_f8f6f4 takes 32
 // rows of each operand x 64 elements of K and a scale byte for each row and block, and
-// adds into FP32.  (Register-only loops on this part: 7.9 PFLOP/s; the 16x16x128 form
-// 4.2.)
+// adds into FP32.  (Register-only loops on this part: 9.6 PFLOP/s on zeros, 6.5 on random
+// codes; the 16x16x128 form 4.2.)
+//
+// This kernel takes any K, layout and number of rows; large tiles of a regular K go to
+// mx4_ring.hip, few rows to mx4_few.hip.  Two stages of 256 elements.  What bounds it: with
+// 256 x 256 tiles the wait for the next stage beside the matrix instructions (4096 x 4096 x
+// 5000: 58 us, 2.9 PFLOP/s), with 64 x 64 tiles the bytes in flight of one stage (64 x 14336
+// x 4096: 16.7 us, 2.0 TB/s).
 #include "bytes.hpp"
 #include "mx4_tile.hpp"
 
@@ -14,15 +20,6 @@ namespace dg {
 namespace {
 
 constexpr int KB = 128;          // bytes of K in a tile: 256 elements, 8 blocks
-
-// 16 bytes from `at` on of a row of `bytes`, zeros past its end.
-__device__ __forceinline__ u32x4 row_chunk(const char *row, int at, int bytes) {
-    const int n = bytes - at;
-    if (n >= 16) return *reinterpret_cast<const u32x4_any *>(row + at);
-    if (n <= 0) return u32x4{0u, 0u, 0u, 0u};
-    if (bytes >= 16) return down_bytes(*reinterpret_cast<const u32x4_any *>(row + bytes - 16), 16 - n);
-    return load_part<1>(row + at, 1, n);
-}
 
 // The scale bytes of 8 blocks from `at` on of a row of `blocks`, zeros past its end: the
 // codes read there, whatever they are, then count 2^-254 times at most 36, nothing.
@@ -80,7 +77,7 @@ struct TileIO {
 #pragma unroll
         for (int i = 0; i < CHUNKS; ++i) {
             const int pos = tid + i * 64 * NW, row = pos >> 3;
-            reg[i] = row_chunk(base + (int64_t)min(row, lim - 1 - r0) * rs, at + (((pos & 7) ^ ((row >> 1) & 7)) << 4), bytes);
+            reg[i] = row_piece(base + (int64_t)min(row, lim - 1 - r0) * rs, at + (((pos & 7) ^ ((row >> 1) & 7)) << 4), bytes);
         }
     }
     __device__ static void store(char *lds, const u32x4 (&reg)[CHUNKS], int tid) {

@@ -1,5 +1,5 @@
 // mx4_half.hip -- products of 16-bit activations with microscaled 4-bit weights where many
-// rows meet every weight (few rows: w4.hpp):
+// rows meet every weight (few: mx4_few.hip; between: w4.hpp):
 //
 //   C[m][n] = act(sum over blocks b of 32 k's of 2^(s[n][b] - 127) * sum over k in b of A[m][k] w[n][k])
 //
@@ -9,6 +9,9 @@
 // the same way, in another the codes are converted as they are, a block's sum is formed in
 // FP32 on the matrix cores and enters the FP32 accumulator times its scale (2048 x 4096 x
 // 4096: 64 us, 85 that way; BF16 62).
+// What bounds it: the matrix instructions, 27 us of those 62 at the full clock, with 4.5
+// vector instructions to each, and one round of tiles whose first loads and stores
+// nothing overlaps (8192^3: 875 us, 1.26 PFLOP/s).
 #include "bytes.hpp"
 #include "device_common.hpp"
 #include "gemm_dtl.hpp"

@@ -2,7 +2,7 @@
 // of 512 and whose rows and scale rows begin at multiples of 16 bytes: large tiles whose
 // loads, fragment reads and matrix instructions overlap.
 //
-// What bounds it (4096 x 4096 x 4096: 41 us, 3.3 PFLOP/s; 8192^3: 283 us, 3.9): the matrix
+// What bounds it (4096 x 4096 x 4096: 43 us, 3.2 PFLOP/s; 8192^3: 274 us, 4.0): the matrix
 // cores on operands like these run at 1.65 to 1.75 GHz for power (register-only loops of
 // 32x32x64 instructions: 9.6 PFLOP/s on zeros, 6.5 on random codes), where the loop
 // without its loads takes 2330 cycles for a tile of K and its matrix instructions alone

@@ -1,5 +1,6 @@
 // w4_mx.hip -- products of 16-bit activations with microscaled 4-bit weights (E2M1
-// codes, an E8M0 scale byte for 32 of them): the kernels of w4.hpp with that decoding.
+// codes, an E8M0 scale byte for 32 of them): the kernels of w4.hpp with that decoding, for
+// 17 to 48 rows (33 x 4096 x 14336: 20.6 us).
 #include "w4.hpp"
 
 namespace dg {
