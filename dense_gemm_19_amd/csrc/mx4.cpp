@@ -218,7 +218,7 @@ dg_status few_product(const Mat &x, const Mat *sx, const Mat &off, const Stack &
     a.E = (int)q.E;
     const int64_t used = experts ? std::min(q.E, M) : 1, mean = cdiv(M, used);
     const bool aligned = !sx && few_aligned(x);
-    const int tm = mean > 32 ? 3 : mean > 16 ? 2 : 1;
+    const int tm = mean > 32 ? sx ? 4 : 3 : mean > 16 ? 2 : 1;
     const int64_t rows = mx4_few_rows(tm);
     if (aligned) a.a_rows = (int)std::min<int64_t>(M, rows);
     const int64_t k_units = cdiv(bytes, 256), tiles = cdiv(N, 32) * used;
@@ -359,12 +359,14 @@ dg_status gemm_entry(const dg_view *A, const dg_view *SA, const dg_view *offsets
     if (c.empty()) return nothing(r);
     const int64_t mean = cdiv(M, experts ? std::min(q.E, M) : 1);
     // Few rows: that kernel's waves share K and read A again for every 16 or 32 columns, which
-    // pays up to 32 rows of codes (N = 14336, K = 4096: 14.8 us beside 16.3), 16 of 16 bits
-    // (12.9 beside 17.6), and 36 where one workgroup to a CU takes all columns (32 x 4096 x
-    // 4096: 7.1 us beside 15.0; 33 x 4096 x 14336: 19.5 beside 20.6; 32 x 14336 x 4096: 18.0
-    // beside 16.5).
-    const bool more = few_aligned(x) && !experts && N <= 16 * 256;
-    if (mean <= (codes ? 32 : more ? 36 : 16)) return few_product(x, codes ? &sx : nullptr, off, q, s, c, act, experts, stream, r);
+    // pays up to 32 rows of codes (N = 14336, K = 4096: 14.8 us beside 16.3; 48: 17.9 beside
+    // 16.5) and 16 of 16 bits (12.9 beside 17.6; 32: 18.0 beside 16.5), and up to 64 and 36 where
+    // one workgroup to a CU takes all columns (64 rows of codes, 4096 x 4096: 8.4 us beside 9.6,
+    // 4096 x 14336 18.7 beside 19.2, 1024 x 8192 8.2 beside 16.1; 32 of 16 bits, 4096 x 4096: 7.1
+    // beside 15.0, 33, 4096 x 14336: 19.5 beside 20.6).
+    const bool narrow = !experts && N <= 16 * 256;
+    const int64_t few = codes ? narrow ? 64 : 32 : narrow && few_aligned(x) ? 36 : 16;
+    if (mean <= few) return few_product(x, codes ? &sx : nullptr, off, q, s, c, act, experts, stream, r);
     if (codes) return codes_product(x, sx, off, q, s, c, act, experts, stream, r);
     bool done_here = false;
     const dg_status st = half_product(x, off, q, s, c, act, experts, stream, r, &done_here);

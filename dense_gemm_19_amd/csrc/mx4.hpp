@@ -94,7 +94,7 @@ enum Mx4HalfTile : int { MX4_T128x256 = 0, MX4_T64x128 = 1 };
 hipError_t launch_mx4_half(int in_kind, int tile, const Mx4GemmArgs &a, int64_t units, hipStream_t stream);
 
 // Few rows (mx4_few.hip): any layout.  kind: MX4_CODES, or the type of a 16-bit A; tm, nf:
-// tm 1 to 3 (codes: to 2) for mx4_few_rows(tm) rows, x 16 nf columns, of a workgroup; pieces of K of kt_per_split units of 512.
+// tm 1 to 3 (codes: 1, 2, 4) for mx4_few_rows(tm) rows, x 16 nf columns, of a workgroup; pieces of K of kt_per_split units of 512.
 constexpr int MX4_CODES = 3;               // beside IN_F16 and IN_BF16
 constexpr int mx4_few_rows(int tm) { return tm == 3 ? 36 : 16 * tm; }   // of a workgroup (36: two steps of them fill LDS)
 constexpr int mx4_few_sums(int tm, int nf) { return 256 * tm * nf; }   // of a workgroup: FP32, of whole 16 x 16 blocks

@@ -383,6 +383,7 @@ hipError_t launch_half(int tm, int nf, const Mx4GemmArgs &a, int64_t units, hipS
 hipError_t launch_mx4_few(int kind, int tm, int nf, const Mx4GemmArgs &a, int64_t units, hipStream_t s) {
     if (kind == MX4_CODES && tm == 1) return launch_columns<CODES, 1, STRAIGHT>(nf, a, units, s);
     if (kind == MX4_CODES && tm == 2) return launch_columns<CODES, 2, STRAIGHT>(nf, a, units, s);
+    if (kind == MX4_CODES && tm == 4) return launch_columns<CODES, 4, STRAIGHT>(nf, a, units, s);
     if (kind == IN_BF16) return launch_half<IN_BF16>(tm, nf, a, units, s);
     if (kind == IN_F16) return launch_half<IN_F16>(tm, nf, a, units, s);
     return hipErrorInvalidValue;

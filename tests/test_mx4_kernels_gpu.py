@@ -49,7 +49,8 @@ def many(rows, cols, pieces=1):
 
 @pytest.mark.parametrize("M,N,K,rows,cols,pieces", [
     (1, 40, 512, 16, 16, 1), (16, 33, 4096, 16, 16, 1), (13, 8200, 1024, 16, 32, 1), (5, 100, 5000, 16, 16, 1), (17, 50, 4608, 32, 16, 1),
-    (32, 8192, 520, 32, 32, 1), (16, 1000, 8192, 16, 16, 4), (3, 70, 40000, 16, 16, 16), (20, 4096, 8192, 32, 32, 2), (16, 4100, 9000, 16, 32, 0)])
+    (32, 8192, 520, 32, 32, 1), (16, 1000, 8192, 16, 16, 4), (3, 70, 40000, 16, 16, 16), (20, 4096, 8192, 32, 32, 2), (16, 4100, 9000, 16, 32, 0),
+    (33, 40, 512, 64, 16, 1), (50, 1000, 5000, 64, 16, 1), (64, 4096, 8192, 64, 32, 2), (63, 1024, 8200, 64, 16, 4)])
 def test_few_rows_of_codes(dg, M, N, K, rows, cols, pieces):
     plan = few(rows, cols, pieces) if pieces else f"few rows, {rows}x{cols} tiles"
     run(dg, "codes", M, N, K, plan)
@@ -157,7 +158,7 @@ def test_between_few_and_many(dg, M, N, K, kind):
     (4096, 4200, 512, "ring loads, 256x256 tiles, K in 1 pieces, 256 workgroups; direct loads, 64x64 tiles"),
     (4000, 4500, 304, "direct loads, 256x256 tiles, K in 1 pieces, 256 workgroups; direct loads, 64x64 tiles"),
     (1100, 2900, 1536, "ring loads, 128x128"),
-    (4000, 3300, 304, "direct loads, 256x256"), (1030, 2900, 1000, "direct loads, 128x128"), (40, 50, 264, "direct loads, 64x64"),
+    (4000, 3300, 304, "direct loads, 256x256"), (1030, 2900, 1000, "direct loads, 128x128"), (70, 50, 264, "direct loads, 64x64"), (40, 4200, 264, "direct loads, 64x64"),
     (70, 130, 9000, "direct loads, 64x64"), (1100, 2900, 333, "vector loads, 128x128"), (70, 130, 777, "vector loads, 64x64"), (70, 50, 90, "element loads")])
 def test_many_rows_of_codes(dg, M, N, K, plan):
     run(dg, "codes", M, N, K, plan, out=[F32, BF16][M * N > 1 << 20])
