@@ -156,40 +156,38 @@ __global__ void __launch_bounds__(NT) mx4_few(Mx4GemmArgs a) {
         }
     };
 
-    // A unit as it comes: an end in it, scales apart, or (FP16) scales that FP16 does not hold.
-    auto any_unit = [&](int u) __attribute__((always_inline)) {
-#pragma unroll 1
-        for (int j = 0; j < 4; ++j) {
-            const int at = u * UNIT + 16 * g + 64 * j, b = 16 * u + 4 * j;
-            auto scales = [&](const char *row, int64_t cs) __attribute__((always_inline)) {
-                uint32_t v = 0;
+    // Step st of 128 elements as it comes: an end in it, scales apart, or (FP16) scales that
+    // FP16 does not hold.
+    auto any_step = [&](int st) __attribute__((always_inline)) {
+        const int u = st >> 2, j = st & 3, at = u * UNIT + 16 * g + 64 * j, b = 16 * u + 4 * j;
+        auto scales = [&](const char *row, int64_t cs) __attribute__((always_inline)) {
+            uint32_t v = 0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (b + i < a.blocks) v |= (uint32_t)*reinterpret_cast<const uint8_t *>(row + (b + i) * cs) << (8 * i);
-                return v;
-            };
-            if constexpr (KIND == CODES) {
-                u32x4 x[TM];
-                uint32_t sx[TM];
+            for (int i = 0; i < 4; ++i)
+                if (b + i < a.blocks) v |= (uint32_t)*reinterpret_cast<const uint8_t *>(row + (b + i) * cs) << (8 * i);
+            return v;
+        };
+        if constexpr (KIND == CODES) {
+            u32x4 x[TM];
+            uint32_t sx[TM];
 #pragma unroll
-                for (int t = 0; t < TM; ++t) { x[t] = row_piece(arow[t], at, a.row_bytes); sx[t] = scales(sarow[t], a.sa_cs); }
+            for (int t = 0; t < TM; ++t) { x[t] = row_piece(arow[t], at, a.row_bytes); sx[t] = scales(sarow[t], a.sa_cs); }
 #pragma unroll
-                for (int f = 0; f < NF; ++f) step4(row_piece(wrow[f], at, a.row_bytes), scales(srow[f], a.s_cs), f, x, sx);
-            } else {
-                u32x4 w[NF];
-                uint32_t sw[NF];
+            for (int f = 0; f < NF; ++f) step4(row_piece(wrow[f], at, a.row_bytes), scales(srow[f], a.s_cs), f, x, sx);
+        } else {
+            u32x4 w[NF];
+            uint32_t sw[NF];
 #pragma unroll
-                for (int f = 0; f < NF; ++f) { w[f] = row_piece(wrow[f], at, a.row_bytes); sw[f] = scales(srow[f], a.s_cs); }
+            for (int f = 0; f < NF; ++f) { w[f] = row_piece(wrow[f], at, a.row_bytes); sw[f] = scales(srow[f], a.s_cs); }
 #pragma unroll
-                for (int t = 0; t < TM; ++t) {
-                    u32x4 x[1][4];
+            for (int t = 0; t < TM; ++t) {
+                u32x4 x[1][4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[0][i] = row_piece(arow[t], u * (4 * UNIT) + 16 * g + 256 * j + 64 * i, 2 * a.K);
+                for (int i = 0; i < 4; ++i) x[0][i] = row_piece(arow[t], u * (4 * UNIT) + 16 * g + 256 * j + 64 * i, 2 * a.K);
 #pragma unroll
-                    for (int f = 0; f < NF; ++f) {
-                        step16(Int<KIND == IN_BF16>(), w[f], sw[f], f, t, x);
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
+                for (int f = 0; f < NF; ++f) {
+                    step16(Int<KIND == IN_BF16>(), w[f], sw[f], f, t, x);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
         }
@@ -294,18 +292,23 @@ __global__ void __launch_bounds__(NT) mx4_few(Mx4GemmArgs a) {
             }
         }
     };
+    // The steps that are not of whole units, shared by the waves (a wave's four one after
+    // another: 40 x 333 x 1000 codes 11.5 us beside 5.7).
+    const int rest = 4 * max(whole, u0) + wave;
     if constexpr (CHECK) {                         // (each there once: registers)
 #pragma unroll 1
         while (true) {
             whole_units();
-            if (u >= u1) break;
-            any_unit(u);
+            const bool far = u < whole;            // this unit's scales, else the rest
+#pragma unroll 1
+            for (int st = far ? 4 * u : rest; st < (far ? 4 * u + 4 : 4 * u1); st += far ? 1 : WAVES) any_step(st);
+            if (!far) break;
             u += WAVES;
         }
     } else {
         whole_units();
 #pragma unroll 1
-        for (; u < u1; u += WAVES) any_unit(u);
+        for (int st = rest; st < 4 * u1; st += WAVES) any_step(st);
     }
 
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
