@@ -12,13 +12,14 @@
 //   A in codes: those are the operands of v_mfma_scale_f32_16x16x128_f8f6f4 as they lie.
 //   A in 16 bits: the lanes of a row first exchange words (a 4 x 4 transpose in four
 //   instructions), so that an instruction of 32 elements meets one block of every row.
-//   The weights are converted times their scale, exactly, in BF16 always and for STEPS (see
-//   below) in FP16, too, where it holds the products; elsewhere FP16's codes are converted
-//   as they are and a block's sum, in FP32, is added times its scale.
+//   The weights are converted times their scale, exactly, in BF16 and for STEPS (see below)
+//   in FP16, too, where the type holds them; elsewhere as block_scale says, and a block's
+//   sum, in FP32, is added times its factor.
 #include <algorithm>
 
 #include "bytes.hpp"
 #include "device_common.hpp"
+#include "e8m0.hpp"
 #include "gemm_dtl.hpp"
 #include "moe_slot.hpp"
 #include "mx4_tile.hpp"
@@ -39,10 +40,6 @@ __device__ __forceinline__ u32x4 exchange(u32x4 v) {
     auto t0 = __builtin_amdgcn_permlane16_swap(s0[0], s1[0], false, false);
     auto t1 = __builtin_amdgcn_permlane16_swap(s0[1], s1[1], false, false);
     return u32x4{t0[0], t0[1], t1[0], t1[1]};
-}
-
-__device__ __forceinline__ float power(uint32_t b) {   // 2^(b - 127); 0: subnormal, 255: NaN
-    return __builtin_bit_cast(float, max(b << 23, 0x00400000u) | (b == 255u ? 0x00400000u : 0u));
 }
 
 // 8 codes as 16-bit numbers, times the power of two in the exponent bits of s (the
@@ -135,13 +132,13 @@ __global__ void __launch_bounds__(NT) mx4_few(Mx4GemmArgs a) {
 #pragma unroll
                 for (int t = 0; t < T; ++t) acc[t0 + t][f] = dtl::mfma16<KIND>(x[t][i], y, acc[t0 + t][f]);
             } else {
-                const u32x4 y = decode<KIND>(q[i], 1.0f);
-                const float sc = power((s >> (8 * i)) & 255u);
+                const BlockScale sc = block_scale<KIND>((s >> (8 * i)) & 255u);
+                const u32x4 y = decode<KIND>(q[i], sc.in);
 #pragma unroll
                 for (int t = 0; t < T; ++t) {
                     const f32x4 b = dtl::mfma16<KIND>(x[t][i], y, f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[t0 + t][f][r] = fmaf(sc, b[r], acc[t0 + t][f][r]);
+                    for (int r = 0; r < 4; ++r) acc[t0 + t][f][r] = fmaf(sc.out, b[r], acc[t0 + t][f][r]);
                 }
                 __builtin_amdgcn_sched_barrier(0);   // (registers)
             }
@@ -156,8 +153,8 @@ __global__ void __launch_bounds__(NT) mx4_few(Mx4GemmArgs a) {
         }
     };
 
-    // Step st of 128 elements as it comes: an end in it, scales apart, or (FP16) scales that
-    // FP16 does not hold.
+    // Step st of 128 elements as it comes: an end in it, scales apart, or scales that the
+    // type does not hold.
     auto any_step = [&](int st) __attribute__((always_inline)) {
         const int u = st >> 2, j = st & 3, at = u * UNIT + 16 * g + 64 * j, b = 16 * u + 4 * j;
         auto scales = [&](const char *row, int64_t cs) __attribute__((always_inline)) {
@@ -186,7 +183,8 @@ __global__ void __launch_bounds__(NT) mx4_few(Mx4GemmArgs a) {
                 for (int i = 0; i < 4; ++i) x[0][i] = row_piece(arow[t], u * (4 * UNIT) + 16 * g + 256 * j + 64 * i, 2 * a.K);
 #pragma unroll
                 for (int f = 0; f < NF; ++f) {
-                    step16(Int<KIND == IN_BF16>(), w[f], sw[f], f, t, x);
+                    if (KIND == IN_BF16 && !__builtin_amdgcn_ballot_w64(top_scales(sw[f]) != 0)) step16(Int<1>(), w[f], sw[f], f, t, x);
+                    else step16(Int<0>(), w[f], sw[f], f, t, x);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
@@ -307,8 +305,39 @@ __global__ void __launch_bounds__(NT) mx4_few(Mx4GemmArgs a) {
         }
     } else {
         whole_units();
+        // BF16: a weight past its range makes a sum infinite or NaN, whatever A holds.  Units with
+        // such a sum are summed once more, by steps (a look at every scale takes 3 to 7 % of a
+        // call of one row).
+        bool again = false;
+        if constexpr (KIND == IN_BF16) {
+            float odd = 0.f;                       // NaN then
+#pragma unroll
+            for (int t = 0; t < TM; ++t)
+#pragma unroll
+                for (int f = 0; f < NF; ++f)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) odd = fmaf(acc[t][f][r], 0.f, odd);
+            again = __builtin_expect(__builtin_amdgcn_ballot_w64(odd != 0.f) != 0, 0);
+        }
+        if (again) {
+#pragma unroll
+            for (int t = 0; t < TM; ++t)
+#pragma unroll
+                for (int f = 0; f < NF; ++f) acc[t][f] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+        int st = again ? 4 * (u0 + wave) : rest;
+        if (__builtin_expect(st < 4 * u1, 0)) {    // (code that a K of whole units does not fetch)
 #pragma unroll 1
-        for (int st = rest; st < 4 * u1; st += WAVES) any_step(st);
+            do {
+                any_step(st);
+                if (st >= 4 * whole) {
+                    st += WAVES;
+                } else if ((++st & 3) == 0) {      // the wave's next unit, or the rest
+                    st += 4 * (WAVES - 1);
+                    if (st >= 4 * whole) st = rest;
+                }
+            } while (st < 4 * u1);
+        }
     }
 
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");

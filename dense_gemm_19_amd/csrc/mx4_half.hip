@@ -4,16 +4,18 @@
 //   C[m][n] = act(sum over blocks b of 32 k's of 2^(s[n][b] - 127) * sum over k in b of A[m][k] w[n][k])
 //
 // BF16: the weights of a block times their scale are BF16 numbers, exactly (E2M1 has two
-// significant bits), which one instruction converts two at a time; the matrix cores do the
-// rest.  FP16 does not hold every scale: a workgroup whose scales all lie in its range goes
-// the same way, in another the codes are converted as they are, a block's sum is formed in
-// FP32 on the matrix cores and enters the FP32 accumulator times its scale (2048 x 4096 x
-// 4096: 64 us, 85 that way; BF16 62).
+// significant bits; the two largest scales apart), which one instruction converts two at a
+// time; the matrix cores do the rest.  FP16 does not hold every scale: a workgroup whose
+// scales all lie in its range goes the same way, in another the codes are converted as they
+// are, a block's sum is formed in FP32 on the matrix cores and enters the FP32 accumulator
+// times its scale (2048 x 4096 x 4096: 64 us, 85 that way; BF16 62).  A BF16 workgroup that
+// met one of the largest scales sums its tile once more that way, as block_scale says.
 // What bounds it: the matrix instructions, 27 us of those 62 at the full clock, with 4.5
 // vector instructions to each, and one round of tiles whose first loads and stores
 // nothing overlaps (8192^3: 875 us, 1.26 PFLOP/s).
 #include "bytes.hpp"
 #include "device_common.hpp"
+#include "e8m0.hpp"
 #include "gemm_dtl.hpp"
 #include "moe_slot.hpp"
 #include "mx4_tile.hpp"
@@ -40,12 +42,11 @@ __device__ __forceinline__ void arrive() {   // all but the last N loads of this
 
 template <int N> using Int = std::integral_constant<int, N>;
 
-// 2^(b - 127) (0: subnormal, 255: NaN).  BF16: its exponent, which is all that the
-// conversion reads.
+// 2^(b - 127) for the conversion, which reads its exponent alone.
 template <int IN>
 __device__ __forceinline__ float power(uint32_t b) {
     if constexpr (IN == IN_BF16) return __builtin_bit_cast(float, b << 23);
-    return __builtin_bit_cast(float, max(b << 23, 0x00400000u) | (b == 255u ? 0x00400000u : 0u));
+    return e8m0_value(b);
 }
 
 // 8 codes as 16-bit numbers, times the scale.
@@ -139,19 +140,24 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_half(Mx4GemmArgs a) {
     };
 
     f32x16 acc[TM][TN];
+    auto zero_sums = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+        for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
+            for (int j = 0; j < TN; ++j)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+                for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+    };
+    zero_sums();
+    uint32_t top = 0;                              // BF16: the largest scale byte that this lane met
+    __shared__ int past;                           // and whether BF16 does not hold one of them
     // ONE: a lane's elements of a part are of one block, and W's are taken times its scale.
     auto run = [&](auto one) __attribute__((always_inline)) {
         constexpr bool ONE = decltype(one)::value;
         constexpr int CH = ONE ? 1 : 2;            // W: chunks and scales of a part that a lane reads
         u32x4 fa[2][TM], wq[2][TN][CH];                // of even and odd steps; of even and odd parts
         uint32_t sw[2][TN][CH];                        // scale bytes
-        float sc[TN][CH];                              // what they stand for: the part at hand
+        BlockScale sc[TN][CH];                         // what they stand for (ONE: all in the conversion): the part at hand
         const int ra = (wm * WTM + l) * KB, rw = W_OFF + (wn * WTN + l) * KB, rs = S_OFF + (wn * WTN + l) * 4, swz = (l >> 1) & 7;
         auto read_a = [&](int step, int i, int slot) __attribute__((always_inline)) {
             fa[step & 1][i] = *reinterpret_cast<const u32x4 *>(lds + ra + slot * PART + 32 * i * KB + (((ONE ? 4 * h + step : 2 * step + h) ^ swz) << 4));
@@ -166,16 +172,16 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_half(Mx4GemmArgs a) {
                 else sw[q & 1][j][c] = *reinterpret_cast<const uint32_t *>(at + b * (BN * 4));
             }
         };
-        f32x16 blk[ONE ? 1 : TM][ONE ? 1 : TN];          // FP16: a block's sums
+        f32x16 blk[ONE ? 1 : TM][ONE ? 1 : TN];          // a block's sums
         auto multiply = [&](auto s, int q) __attribute__((always_inline)) {
             constexpr int STEP = decltype(s)::value;
             u32x4 fb[TN];
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
-                if constexpr (ONE) fb[j] = decode<IN>(wq[q & 1][j][0][STEP], sc[j][0]);
+                if constexpr (ONE) fb[j] = decode<IN>(wq[q & 1][j][0][STEP], sc[j][0].in);
                 else {
                     const u32x4 c = wq[q & 1][j][STEP >> 1];
-                    fb[j] = decode<IN>(h ? c[2 * (STEP & 1) + 1] : c[2 * (STEP & 1)], 1.0f);
+                    fb[j] = decode<IN>(h ? c[2 * (STEP & 1) + 1] : c[2 * (STEP & 1)], sc[j][STEP >> 1].in);
                 }
             }
 #pragma unroll
@@ -196,7 +202,7 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_half(Mx4GemmArgs a) {
 #pragma unroll
                     for (int j = 0; j < TN; ++j)
 #pragma unroll
-                        for (int r = 0; r < 16; ++r) acc[i][j][r] = fmaf(sc[j][STEP >> 1], blk[i][j][r], acc[i][j][r]);
+                        for (int r = 0; r < 16; ++r) acc[i][j][r] = fmaf(sc[j][STEP >> 1].out, blk[i][j][r], acc[i][j][r]);
             }
             __builtin_amdgcn_sched_barrier(0);
         };
@@ -215,7 +221,12 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_half(Mx4GemmArgs a) {
 #pragma unroll
             for (int j = 0; j < TN; ++j)
 #pragma unroll
-                for (int c = 0; c < CH; ++c) sc[j][c] = power<IN>(sw[Q & 1][j][c]);
+                for (int c = 0; c < CH; ++c) {
+                    const uint32_t b = sw[Q & 1][j][c];
+                    if constexpr (ONE) sc[j][c] = {power<IN>(b), 1.0f};
+                    else sc[j][c] = block_scale<IN>(b);
+                    if (ONE && IN == IN_BF16) top = max(top, b);
+                }
             multiply(Int<0>(), Q);
             next(2);
             multiply(Int<1>(), Q);
@@ -339,8 +350,8 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_half(Mx4GemmArgs a) {
             else ragged(Int<3>());
         }
     };
-    if (parts > 0) {
-        // as the four parts before the first would have issued them
+    // as the four parts before the first would have issued them
+    auto first_loads = [&]() __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < WI; ++j) {
             load_w(j, 0);
@@ -360,8 +371,20 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_half(Mx4GemmArgs a) {
         }
 #pragma unroll
         for (int j = 0; j < WI; ++j) load_w(j, 1);   // (past the end: the rows' ends)
-        if constexpr (IN == IN_BF16) run(Int<1>());
-        else if constexpr (!WORDS) run(Int<0>());
+    };
+    if (parts > 0) {
+        first_loads();
+        if constexpr (IN == IN_BF16) {
+            if (tid == 0) past = 0;                // (barriers lie between)
+            run(Int<1>());
+            if (top >= 253u) past = 1;
+            arrive<0>();                           // every wave has read its last fragments
+            if (__builtin_expect(__builtin_amdgcn_readfirstlane(past), 0)) {
+                zero_sums();
+                first_loads();
+                run(Int<0>());
+            }
+        } else if constexpr (!WORDS) run(Int<0>());
         else {
             // does FP16 hold every code times its scale: 2^-24 .. 2^15, scales 2^-23 .. 2^13?
             uint32_t far = 0;
