@@ -11,7 +11,8 @@
 //
 // Microscaled weights (SB = 1, a byte per scale) differ in two places only: a code is
 // an E2M1 number, exact in both types, which gfx950 converts two at a time, and a
-// group's scale is the power of two that its byte names.
+// group's scale is the power of two that its byte names.  BF16 codes are converted times
+// their scale (block_scale): a group's sum without it may pass FP32.
 //
 // Bound by the bytes of the codes where few rows meet many weights (half a byte
 // per weight), by the latency of the loads and the instructions fetched for small
@@ -19,6 +20,7 @@
 #pragma once
 #include "bytes.hpp"
 #include "device_common.hpp"
+#include "e8m0.hpp"
 #include "gemm_dtl.hpp"
 #include "moe.hpp"
 #include "moe_slot.hpp"
@@ -71,17 +73,12 @@ __device__ __forceinline__ u32x4 decode(uint32_t x, float z) {
     return out;
 }
 
-// The power of two that a scale byte stands for, 2^(b - 127) (0: subnormal, 255: NaN).
-__device__ __forceinline__ float e8m0_value(uint32_t b) {
-    return __builtin_bit_cast(float, max(b << 23, 0x00400000u) | (b == 255u ? 0x00400000u : 0u));
-}
-
-// 8 E2M1 codes as FP16 or BF16 (4 instructions).
+// 8 E2M1 codes times a scale as FP16 or BF16 (4 instructions).
 template <int IN>
-__device__ __forceinline__ u32x4 decode_e2m1(uint32_t x) {
+__device__ __forceinline__ u32x4 decode_e2m1(uint32_t x, float scale) {
     u32x4 out;
-    auto pair = [&](auto j) { if constexpr (IN == IN_F16) return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(x, 1.0f, decltype(j)::value));
-                              else return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, 1.0f, decltype(j)::value)); };
+    auto pair = [&](auto j) { if constexpr (IN == IN_F16) return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(x, scale, decltype(j)::value));
+                              else return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, scale, decltype(j)::value)); };
     out[0] = pair(std::integral_constant<int, 0>());
     out[1] = pair(std::integral_constant<int, 1>());
     out[2] = pair(std::integral_constant<int, 2>());
@@ -381,12 +378,15 @@ __global__ void __launch_bounds__(NT, TM == 1 ? 4 : 2) w4_whole(W4Args a) {
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int t = 0; t < TM; ++t) fa[i][t] = *reinterpret_cast<const u32x4 *>(lds + as + fa_at[i][t] + 256 * w);
-            float s[GV], zp[GV];
+            float s[GV], zp[GV], in[GV];           // (in: microscaled, the codes' part of the scale)
 #pragma unroll
             for (int v = 0; v < GV; ++v) {
                 const int gi = group_of(k0 / 32 + 4 * w + v * (4 / GV)) - g0;
-                if constexpr (SB == 1) s[v] = e8m0_value(*reinterpret_cast<const uint8_t *>(ls + gi));
-                else if constexpr (SB == 4) s[v] = *reinterpret_cast<const float *>(ls + 4 * gi);
+                if constexpr (SB == 1) {
+                    const BlockScale b = block_scale<IN>(*reinterpret_cast<const uint8_t *>(ls + gi));
+                    s[v] = b.out;
+                    in[v] = b.in;
+                } else if constexpr (SB == 4) s[v] = *reinterpret_cast<const float *>(ls + 4 * gi);
                 else {
                     const uint16_t h = *reinterpret_cast<const uint16_t *>(ls + 2 * gi);
                     s[v] = a.s_kind == OUT_BF16 ? bf16_bits_to_f32(h) : f16_bits_to_f32(h);
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(NT, TM == 1 ? 4 : 2) w4_whole(W4Args a) {
             for (int i = 0; i < 4; ++i) {
                 constexpr int PER = 4 / GV;        // 32-wide steps of a group
                 const bool first = i % PER == 0;
-                const u32x4 fb = SB == 1 ? decode_e2m1<IN>(q[i]) : decode<IN>(q[i], zp[i / PER]);
+                const u32x4 fb = SB == 1 ? decode_e2m1<IN>(q[i], in[i / PER]) : decode<IN>(q[i], zp[i / PER]);
 #pragma unroll
                 for (int t = 0; t < TM; ++t) blk[t] = mfma<IN>(fa[i][t], fb, first ? f32x4{0.f, 0.f, 0.f, 0.f} : blk[t]);
                 if (i % PER == PER - 1) {
@@ -573,12 +573,15 @@ __global__ void __launch_bounds__(NT, TM == 1 ? 4 : 2) w4_stream(W4Args a) {
             uint32_t q[4];                         // lane row g: bytes 4 g .. + 3 of the step's 16
 #pragma unroll
             for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const uint32_t *>(lq + l * 128 + 4 * g + 16 * ((4 * w + i) ^ (l & 7)));
-            float s[GV], zp[GV];
+            float s[GV], zp[GV], in[GV];           // (in: microscaled, the codes' part of the scale)
 #pragma unroll
             for (int v = 0; v < GV; ++v) {
                 const int gi = group_of(k0 / 32 + 4 * w + v * (4 / GV)) - seg_g0;
-                if constexpr (SB == 1) s[v] = e8m0_value(*reinterpret_cast<const uint8_t *>(ls + gi));
-                else if constexpr (SB == 4) s[v] = *reinterpret_cast<const float *>(ls + 4 * gi);
+                if constexpr (SB == 1) {
+                    const BlockScale b = block_scale<IN>(*reinterpret_cast<const uint8_t *>(ls + gi));
+                    s[v] = b.out;
+                    in[v] = b.in;
+                } else if constexpr (SB == 4) s[v] = *reinterpret_cast<const float *>(ls + 4 * gi);
                 else {
                     const uint16_t h = *reinterpret_cast<const uint16_t *>(ls + 2 * gi);
                     s[v] = a.s_kind == OUT_BF16 ? bf16_bits_to_f32(h) : f16_bits_to_f32(h);
@@ -596,7 +599,7 @@ __global__ void __launch_bounds__(NT, TM == 1 ? 4 : 2) w4_stream(W4Args a) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 constexpr int PER = 4 / GV;        // 32-wide steps of a group
-                const u32x4 fb = SB == 1 ? decode_e2m1<IN>(q[i]) : decode<IN>(q[i], zp[i / PER]);
+                const u32x4 fb = SB == 1 ? decode_e2m1<IN>(q[i], in[i / PER]) : decode<IN>(q[i], zp[i / PER]);
 #pragma unroll
                 for (int t = 0; t < TM; ++t) {
                     const u32x4 fa = *reinterpret_cast<const u32x4 *>(buf + arow[t] * ROW + 16 * ((wk * 32 + 16 * w + 4 * i + g) ^ (arow[t] & 15)));

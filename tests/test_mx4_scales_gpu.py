@@ -133,11 +133,13 @@ def test_scales_past_bf16_here_and_there(dg, M, N, K, plan, place):
 
 
 @pytest.mark.parametrize("M,N,K,plan,place", KERNELS)
-@pytest.mark.parametrize("size,scales", [(2.0 ** 20, (0, 3)), (2.0 ** -100, (225, 255))])
+@pytest.mark.parametrize("size,scales", [(2.0 ** 120, (40, 61)), (2.0 ** 20, (0, 3)), (2.0 ** -100, (225, 255))])
 def test_largest_and_least_operands(dg, M, N, K, plan, place, size, scales):
-    # the least weights, and the largest against small rows
+    # BF16 rows whose sums without the scales pass FP32, the least weights, and the largest against small rows
     g = gen(M, N, K, 4)
     A = ((1 + torch.rand(M, K, generator=g)) * size * (2 * torch.randint(0, 2, (M, K), generator=g) - 1)).to(BF16)
+    if size > 1e30:
+        A *= 2.0 ** torch.randint(0, 7, (M, K), generator=g).to(BF16)       # up to 2^127
     Q, S = coded(g, N, K, scales)
     a, q, s = place(A), place(Q), place(S)
     C = torch.full((M, N), NAN, device=DEV)
