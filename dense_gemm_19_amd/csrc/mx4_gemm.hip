@@ -86,24 +86,31 @@ struct TileIO {
     }
 };
 
+// How codes get to LDS: through registers; by load-to-LDS instructions, from addresses of
+// whole words; or so but for the ends of the last rows, where a row is no whole words long.
+enum { REGS = 0, WORDS = 1, WORDS_ENDS = 2 };
+
 // BM x BN tiles, waves WGM x WGN, a two-stage LDS ring.  DIRECT: rows begin at multiples
 // of 4 bytes and codes go from memory to LDS by load-to-LDS instructions; else through
-// registers.  RUN: see row_scales.
+// registers.  RUN: see load_scales.
 // K order within a tile: lanes 0-31 take blocks 0-3 and lanes 32-63 blocks 4-7, one at
 // each of the four steps, so that a row's four scale bytes of a lane are one word and
 // the step picks the byte.
 // A ragged K, DIRECT: chunks past the end of a row read the next row, or for the last row its
 // end again.  Whole blocks past the end have scale bytes of zero; of the last block the
 // codes past the end are cleared in W's tile, and the last rows' are moved to where they
-// belong in both.
-template <int BM, int BN, int WGM, int WGN, bool DIRECT, bool RUN, bool SPLIT>
+// belong in both (WORDS_ENDS: their last 16 bytes, which begin at any address, on their
+// way in registers beside the tile).
+template <int BM, int BN, int WGM, int WGN, int LOADS, bool RUN, bool SPLIT>
 __global__ void __launch_bounds__(64 * WGM * WGN) mx4_tile(Mx4GemmArgs a) {
+    constexpr bool DIRECT = LOADS != REGS, ENDS = LOADS == WORDS_ENDS;
     constexpr int NW = WGM * WGN, NT = 64 * NW, WTM = BM / WGM, WTN = BN / WGN, TM = WTM / 32, TN = WTN / 32;
     constexpr int A_BYTES = BM * KB, B_BYTES = BN * KB, SA_OFF = A_BYTES + B_BYTES, SB_OFF = SA_OFF + BM * 8, STAGE = SB_OFF + BN * 8;
     constexpr int SROWS = (BM + BN + NT - 1) / NT;  // scale rows of a thread
     using AIO = TileIO<BM, NW>;
     using BIO = TileIO<BN, NW>;
     static_assert((BM + BN) % NT == 0 || BM + BN < NT, "whole scale rows");
+    static_assert(!ENDS || BM + BN <= NT, "a row's end for a thread");
     static_assert(2 * STAGE <= 160 * 1024 - 64 && NW * MX4_STORE_LDS<TN> <= 2 * STAGE, "LDS");
     __shared__ __attribute__((aligned(16))) char ring[2 * STAGE];
     __shared__ int is_last;
@@ -151,17 +158,21 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_tile(Mx4GemmArgs a) {
             BIO::load(rb, pb, a.q_rs, n0, N, kt * KB, a.row_bytes, tid);
         }
     };
-    // The ragged last tile, DIRECT: chunks begin at row_bytes - 16 at the latest in the
-    // last rows, and anywhere up to the row's end in the others, whose next row is there.
+    // The ragged last tile, DIRECT: chunks begin at row_bytes - 16 (the last word before it) at
+    // the latest in the last rows, and anywhere up to the row's end in the others, whose next
+    // row is there.
+    u32x4 end;                                     // ENDS: of the last row of the operand whose row is this thread's in mend
     auto fetch_ragged = [&](int stage, int kt) __attribute__((always_inline)) {
         fetch_scales(kt);
+        if constexpr (ENDS)
+            end = *reinterpret_cast<const u32x4_any *>((tid < BM ? pa + (int64_t)(M - 1 - m0) * a.a_rs : pb + (int64_t)(N - 1 - n0) * a.q_rs) + a.row_bytes - 16);
         const uint32_t st = ring_lds + (uint32_t)(stage * STAGE);
         auto issue = [&](auto io, uint32_t lds, const char *base, int64_t stride, int r0, int lim) __attribute__((always_inline)) {
 #pragma unroll 1
             for (int j = 0; j < decltype(io)::INSTS; ++j) {
                 const int pos = (wave + NW * j) * 64 + lane, row = min(pos >> 3, lim - 1 - r0);
                 const int at = kt * KB + (((pos & 7) ^ ((pos >> 4) & 7)) << 4);
-                const int most = row == lim - 1 - r0 ? a.row_bytes - 16 : (a.row_bytes - 1) & ~15;
+                const int most = row == lim - 1 - r0 ? (ENDS ? (a.row_bytes - 16) & ~3 : a.row_bytes - 16) : (a.row_bytes - 1) & ~15;
                 dtl::lds_load16(base, (uint32_t)row * (uint32_t)stride + (uint32_t)min(at, most), lds + (uint32_t)((wave_u + NW * j) * 1024));
             }
         };
@@ -189,7 +200,7 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_tile(Mx4GemmArgs a) {
             if (is_a && !last) continue;
             u32x4 *p = reinterpret_cast<u32x4 *>(ring + stage * STAGE + (is_a ? 0 : A_BYTES) + chunk_off(is_a ? r : r - BM, left >> 4));
             const u32x4 v = *p;
-            *p = last ? down_bytes(v, 16 - n) : first_bytes(v, n);
+            *p = last ? down_bytes(ENDS ? end : v, 16 - n) : first_bytes(v, n);
         }
     };
 
@@ -300,18 +311,25 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_tile(Mx4GemmArgs a) {
 }  // namespace
 
 hipError_t launch_mx4_gemm(int tile, int load, const Mx4GemmArgs &a, int64_t units, hipStream_t s) {
-#define DG_TILE(B, GM, GN, D, R, S) hipLaunchKernelGGL((mx4_tile<B, B, GM, GN, D, R, S>), dim3((unsigned)units), dim3(64 * GM * GN), 0, s, a)
-#define DG_SPLITS(B, D, R)                              \
+    const bool ends = a.row_bytes % 4 != 0;
+#define DG_TILE(B, GM, GN, L, R, S) hipLaunchKernelGGL((mx4_tile<B, B, GM, GN, L, R, S>), dim3((unsigned)units), dim3(64 * GM * GN), 0, s, a)
+#define DG_SPLITS(B, L, R)                              \
     do {                                                \
-        if (a.splits > 1) DG_TILE(B, 2, 2, D, R, true); \
-        else DG_TILE(B, 2, 2, D, R, false);             \
+        if (a.splits > 1) DG_TILE(B, 2, 2, L, R, true); \
+        else DG_TILE(B, 2, 2, L, R, false);             \
     } while (0)
-    if (tile == MX4_T256 && load == MX4_DIRECT && a.splits <= 1) DG_TILE(256, 2, 4, true, true, false);
-    else if (tile == MX4_T128 && load == MX4_DIRECT) DG_SPLITS(128, true, true);
-    else if (tile == MX4_T128 && load == MX4_BYTES) DG_SPLITS(128, false, true);
-    else if (tile == MX4_T64 && load == MX4_DIRECT) DG_SPLITS(64, true, true);
-    else if (tile == MX4_T64 && load == MX4_BYTES) DG_SPLITS(64, false, true);
-    else if (tile == MX4_T64 && load == MX4_ANY) DG_SPLITS(64, false, false);
+    if (tile == MX4_T256 && load == MX4_DIRECT && a.splits <= 1) {
+        if (ends) DG_TILE(256, 2, 4, WORDS_ENDS, true, false);
+        else DG_TILE(256, 2, 4, WORDS, true, false);
+    } else if (tile == MX4_T128 && load == MX4_DIRECT) {
+        if (ends) DG_SPLITS(128, WORDS_ENDS, true);
+        else DG_SPLITS(128, WORDS, true);
+    } else if (tile == MX4_T128 && load == MX4_BYTES) DG_SPLITS(128, REGS, true);
+    else if (tile == MX4_T64 && load == MX4_DIRECT) {
+        if (ends) DG_SPLITS(64, WORDS_ENDS, true);
+        else DG_SPLITS(64, WORDS, true);
+    } else if (tile == MX4_T64 && load == MX4_BYTES) DG_SPLITS(64, REGS, true);
+    else if (tile == MX4_T64 && load == MX4_ANY) DG_SPLITS(64, REGS, false);
     else return hipErrorInvalidValue;
 #undef DG_SPLITS
 #undef DG_TILE
