@@ -104,9 +104,9 @@ dg_status dequant_entry(const dg_view *Q, const dg_view *S, const dg_view *Y, hi
     return done(launch_mx4_dequant(a, units, stream), stream);
 }
 
-// The product of codes with codes, its arguments checked.
+// The product of codes with codes, its arguments checked.  part: of the columns of a call.
 dg_status codes_product(const Mat &x, const Mat &sx, const Mat &off, const Stack &q, const Stack &s, const Mat &c, int act, bool experts,
-                        hipStream_t stream, Report *r) {
+                        hipStream_t stream, Report *r, bool part = false) {
     Device d;
     DG_TRY(ready({&x, &sx, &off, &q.span, &s.span, &c}, &d, r));
     const int64_t M = x.rows, N = c.cols, bytes = x.cols;
@@ -147,12 +147,15 @@ dg_status codes_product(const Mat &x, const Mat &sx, const Mat &off, const Stack
     int tile = MX4_T64;
     if (load == MX4_DIRECT && mean > 128 && fills(MX4_T256)) tile = MX4_T256;
     else if (load != MX4_ANY && mean > 64 && fills(MX4_T128)) tile = MX4_T128;
-    // A last round of tiles that half the CUs would sit out: its columns in smaller tiles, of
-    // a launch of their own (4096 x 14336 x 4096, 3 rounds and a half: 149 us
-    // beside 155; 2048 x 8400 x 4096, 264 tiles: 55 beside 69).
+    // A last round of tiles that half the CUs would sit out: the columns past the rounds
+    // before it in smaller tiles, of a launch of their own (4096 x 14336 x 4096, 3 rounds and
+    // a half: 149 us beside 155; 2048 x 8400 x 4096, 264 tiles: 55 beside 69), where they are
+    // too few to take 256-tiles themselves (51200 x 1024: 200 of 800 tiles).  The first part is
+    // not split again (263168 x 7680 would be in 30 parts, each with a last round of its own).
     const int64_t down = cdiv(M, 256), rounds = down * cdiv(N, 256) / d.cus, over = down * cdiv(N, 256) - rounds * d.cus;
     const int64_t first = rounds * d.cus / down * 256;   // columns of the whole rounds
-    if (tile == MX4_T256 && !experts && rounds >= 1 && over > 0 && 2 * over <= d.cus && first > 0 && first < N) {
+    const int64_t rest = down * cdiv(N - first, 256);
+    if (tile == MX4_T256 && !experts && !part && rounds >= 1 && over > 0 && 2 * over <= d.cus && first > 0 && 4 * rest < 3 * (int64_t)d.cus) {
         Stack q1 = q, s1 = s, q2 = q, s2 = s;
         Mat c1 = c, c2 = c;
         q1.one.rows = s1.one.rows = c1.cols = first;
@@ -162,8 +165,8 @@ dg_status codes_product(const Mat &x, const Mat &sx, const Mat &off, const Stack
         c2.ptr += first * c.cs;
         char b1[128], b2[128];
         Report r1 = {b1, sizeof b1}, r2 = {b2, sizeof b2};
-        DG_TRY(codes_product(x, sx, off, q1, s1, c1, act, false, stream, r ? &r1 : nullptr));
-        DG_TRY(codes_product(x, sx, off, q2, s2, c2, act, false, stream, r ? &r2 : nullptr));
+        DG_TRY(codes_product(x, sx, off, q1, s1, c1, act, false, stream, r ? &r1 : nullptr, true));
+        DG_TRY(codes_product(x, sx, off, q2, s2, c2, act, false, stream, r ? &r2 : nullptr, true));
         return r ? r->say("%s; %s", b1, b2) : DG_SUCCESS;
     }
     const int64_t q_es = q.E > 1 ? q.es : 0, s_es = q.E > 1 ? s.es : 0;
