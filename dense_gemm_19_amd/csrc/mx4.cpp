@@ -104,11 +104,17 @@ dg_status dequant_entry(const dg_view *Q, const dg_view *S, const dg_view *Y, hi
     return done(launch_mx4_dequant(a, units, stream), stream);
 }
 
-// The product of codes with codes, its arguments checked.  part: of the columns of a call.
-dg_status codes_product(const Mat &x, const Mat &sx, const Mat &off, const Stack &q, const Stack &s, const Mat &c, int act, bool experts,
-                        hipStream_t stream, Report *r, bool part = false) {
-    Device d;
-    DG_TRY(ready({&x, &sx, &off, &q.span, &s.span, &c}, &d, r));
+// A launch of the product of codes with codes.
+struct CodesLaunch {
+    Mx4GemmArgs a;
+    int tile, load;
+    bool ring;
+};
+
+// The launches of that product, two at most, appended to out[*n].  cut: K may be cut into
+// pieces.  part: of the columns of a call.
+dg_status codes_plan(const Mat &x, const Mat &sx, const Mat &off, const Stack &q, const Stack &s, const Mat &c, int act, bool experts,
+                     const Device &d, bool cut, bool part, CodesLaunch *out, int *n) {
     const int64_t M = x.rows, N = c.cols, bytes = x.cols;
     Mx4GemmArgs a = {};
     a.A = x.ptr; a.a_rs = x.rs;
@@ -163,11 +169,8 @@ dg_status codes_product(const Mat &x, const Mat &sx, const Mat &off, const Stack
         q2.one.ptr += first * q.one.rs;
         s2.one.ptr += first * s.one.rs;
         c2.ptr += first * c.cs;
-        char b1[128], b2[128];
-        Report r1 = {b1, sizeof b1}, r2 = {b2, sizeof b2};
-        DG_TRY(codes_product(x, sx, off, q1, s1, c1, act, false, stream, r ? &r1 : nullptr, true));
-        DG_TRY(codes_product(x, sx, off, q2, s2, c2, act, false, stream, r ? &r2 : nullptr, true));
-        return r ? r->say("%s; %s", b1, b2) : DG_SUCCESS;
+        DG_TRY(codes_plan(x, sx, off, q1, s1, c1, act, false, d, cut, true, out, n));
+        return codes_plan(x, sx, off, q2, s2, c2, act, false, d, cut, true, out, n);
     }
     const int64_t q_es = q.E > 1 ? q.es : 0, s_es = q.E > 1 ? s.es : 0;
     const bool ring = tile != MX4_T64 && bytes % 256 == 0 && a.sa_cs == 1 && a.s_cs == 1 && pieces(x, 0) && pieces(q.one, q_es) && pieces(sx, 0) &&
@@ -179,24 +182,54 @@ dg_status codes_product(const Mat &x, const Mat &sx, const Mat &off, const Stack
     // K in pieces where the tiles leave most of the device idle; a captured call runs
     // whole: the pieces' workspace may have to be allocated.
     int64_t splits = 1;
-    if (!experts && !ring && tile != MX4_T256 && 2 * units <= d.cus && a.ktiles >= 4 && !capturing(stream, r))
+    if (!experts && !ring && tile != MX4_T256 && 2 * units <= d.cus && a.ktiles >= 4 && cut)
         splits = std::min<int64_t>(d.cus / units, a.ktiles / 2);
     a.kt_per_split = (int)cdiv(std::max(a.ktiles, 1), splits);
     a.splits = (int)cdiv(std::max(a.ktiles, 1), a.kt_per_split);
     if (units > INT32_MAX / a.splits || !fits_a_launch(units * a.splits, 512)) return DG_ERR_OVERFLOW;
     a.units = (int)(units * a.splits);
-    if (r)
-        return r->say("%s loads, %dx%d tiles, K in %d pieces, %d workgroups", ring ? "ring" : load == MX4_DIRECT ? "direct" : load == MX4_BYTES ? "vector" : "element", (int)bm, (int)bn, a.splits, a.units);
+    out[(*n)++] = {a, tile, load, ring};
+    return DG_SUCCESS;
+}
+
+// The product of codes with codes, its arguments checked.
+dg_status codes_product(const Mat &x, const Mat &sx, const Mat &off, const Stack &q, const Stack &s, const Mat &c, int act, bool experts,
+                        hipStream_t stream, Report *r) {
+    Device d;
+    DG_TRY(ready({&x, &sx, &off, &q.span, &s.span, &c}, &d, r));
+    CodesLaunch todo[2];
+    int n = 0;
+    DG_TRY(codes_plan(x, sx, off, q, s, c, act, experts, d, !capturing(stream, r), false, todo, &n));
+    if (r) {
+        char text[2][128];
+        for (int i = 0; i < n; ++i) {
+            const CodesLaunch &l = todo[i];
+            Report one = {text[i], sizeof text[i]};
+            one.say("%s loads, %dx%d tiles, K in %d pieces, %d workgroups", l.ring ? "ring" : l.load == MX4_DIRECT ? "direct" : l.load == MX4_BYTES ? "vector" : "element",
+                    mx4_tile_m(l.tile), mx4_tile_n(l.tile), l.a.splits, l.a.units);
+        }
+        return n > 1 ? r->say("%s; %s", text[0], text[1]) : r->say("%s", text[0]);
+    }
+    // The workspace comes before the first launch: without it nothing is written.  One of
+    // the launches at most has pieces of K (256-tiles have none).
     WsLease lease;
-    if (a.splits > 1) {
-        if (lease_workspace(stream, (size_t)units * a.splits * bm * bn * sizeof(float), (size_t)units, &lease) != hipSuccess) {
+    for (int i = 0; i < n; ++i) {
+        Mx4GemmArgs &a = todo[i].a;
+        if (a.splits == 1) continue;
+        const size_t tile = (size_t)mx4_tile_m(todo[i].tile) * mx4_tile_n(todo[i].tile);
+        if (lease_workspace(stream, a.units * tile * sizeof(float), (size_t)(a.units / a.splits), &lease) != hipSuccess) {
             (void)hipGetLastError();
             return DG_ERR_HIP;
         }
         a.ws = lease.ws;
         a.counters = lease.counters;
+        break;
     }
-    return done(ring ? launch_mx4_ring(tile, a, a.units, stream) : launch_mx4_gemm(tile, load, a, a.units, stream), stream);
+    for (int i = 0; i < n; ++i) {
+        const CodesLaunch &l = todo[i];
+        DG_TRY(done(l.ring ? launch_mx4_ring(l.tile, l.a, l.a.units, stream) : launch_mx4_gemm(l.tile, l.load, l.a, l.a.units, stream), stream));
+    }
+    return DG_SUCCESS;
 }
 
 // A 16-bit A that the kernel for few rows stages in LDS.

@@ -1,5 +1,6 @@
-"""The launches of an MXFP4 call, on the CPU: csrc/mx4.cpp and csrc/view.cpp compiled against stand-ins that note
-launches and leases of the workspace and enqueue nothing."""
+"""What an MXFP4 call does before its first launch, on the CPU: csrc/mx4.cpp and csrc/view.cpp compiled against
+stand-ins that note launches and leases of the workspace and enqueue nothing.  Whatever can fail (here the lease) has to
+come before anything is enqueued, since outputs stay untouched on error."""
 import os
 import subprocess
 
@@ -83,6 +84,22 @@ def call(tmp_path_factory):
     subprocess.run(["g++", "-O0", "-std=c++17", "-D__HIP_PLATFORM_AMD__=1", "-I" + os.path.join(ROOT, "include"), "-I" + CSRC,
                     "-isystem/opt/rocm/include", os.path.join(CSRC, "mx4.cpp"), os.path.join(CSRC, "view.cpp"), str(src), "-o", exe], check=True)
     return lambda *args: subprocess.run([exe, *map(str, args)], check=True, capture_output=True, text=True).stdout.split()
+
+
+# few rows, tiles of codes, whole rounds of tiles with the other columns in a launch of their own whose K is cut, many rows
+PIECES = [("codes", 16, 1000, 8192, ["few-pieces"]), ("half", 16, 1000, 8192, ["few-pieces"]), ("codes", 70, 130, 9000, ["tile-pieces"]),
+          ("codes", 300, 33024, 1024, ["ring", "tile-pieces"]), ("codes", 300, 33024, 1000, ["tile", "tile-pieces"]),
+          ("half", 100, 4096, 4096, ["half-pieces"])]
+
+
+@pytest.mark.parametrize("kind,M,N,K,launches", PIECES)
+def test_the_workspace_is_there_before_the_first_launch(call, kind, M, N, K, launches):
+    assert call(kind, M, N, K, "work") == ["lease", *launches, "success"]
+
+
+@pytest.mark.parametrize("kind,M,N,K,launches", PIECES)
+def test_without_a_workspace_nothing_is_launched(call, kind, M, N, K, launches):
+    assert call(kind, M, N, K, "fail") == ["lease", "error"]
 
 
 @pytest.mark.parametrize("kind,M,N,K,launches", [("codes", 4096, 4200, 512, ["ring", "tile"]), ("codes", 4096, 14336, 4096, ["ring", "ring"]),
