@@ -179,10 +179,10 @@ dg_status codes_plan(const Mat &x, const Mat &sx, const Mat &off, const Stack &q
     a.tiles_n = (int)cdiv(N, bn);
     a.group_m = tile == MX4_T256 ? 4 : 8;
     int64_t units = experts ? ((M + std::min(q.E + 1, M) * (bm - 1)) / bm) * a.tiles_n : cdiv(M, bm) * a.tiles_n;
-    // K in pieces where the tiles leave most of the device idle; a captured call runs
-    // whole: the pieces' workspace may have to be allocated.
+    // K in pieces where the tiles leave most of the device idle, which larger ones never do; a
+    // captured call runs whole: the pieces' workspace may have to be allocated.
     int64_t splits = 1;
-    if (!experts && !ring && tile != MX4_T256 && 2 * units <= d.cus && a.ktiles >= 4 && cut)
+    if (!experts && tile == MX4_T64 && 2 * units <= d.cus && a.ktiles >= 4 && cut)
         splits = std::min<int64_t>(d.cus / units, a.ktiles / 2);
     a.kt_per_split = (int)cdiv(std::max(a.ktiles, 1), splits);
     a.splits = (int)cdiv(std::max(a.ktiles, 1), a.kt_per_split);
@@ -211,7 +211,7 @@ dg_status codes_product(const Mat &x, const Mat &sx, const Mat &off, const Stack
         return n > 1 ? r->say("%s; %s", text[0], text[1]) : r->say("%s", text[0]);
     }
     // The workspace comes before the first launch: without it nothing is written.  One of
-    // the launches at most has pieces of K (256-tiles have none).
+    // the launches at most has pieces of K: the first of two has larger tiles.
     WsLease lease;
     for (int i = 0; i < n; ++i) {
         Mx4GemmArgs &a = todo[i].a;

@@ -313,25 +313,26 @@ __global__ void __launch_bounds__(64 * WGM * WGN) mx4_tile(Mx4GemmArgs a) {
 hipError_t launch_mx4_gemm(int tile, int load, const Mx4GemmArgs &a, int64_t units, hipStream_t s) {
     const bool ends = a.row_bytes % 4 != 0;
 #define DG_TILE(B, GM, GN, L, R, S) hipLaunchKernelGGL((mx4_tile<B, B, GM, GN, L, R, S>), dim3((unsigned)units), dim3(64 * GM * GN), 0, s, a)
-#define DG_SPLITS(B, L, R)                              \
-    do {                                                \
-        if (a.splits > 1) DG_TILE(B, 2, 2, L, R, true); \
-        else DG_TILE(B, 2, 2, L, R, false);             \
+#define DG_64(L, R)                                      \
+    do {                                                 \
+        if (a.splits > 1) DG_TILE(64, 2, 2, L, R, true); \
+        else DG_TILE(64, 2, 2, L, R, false);             \
     } while (0)
-    if (tile == MX4_T256 && load == MX4_DIRECT && a.splits <= 1) {
+    if (tile != MX4_T64 && a.splits > 1) return hipErrorInvalidValue;
+    if (tile == MX4_T256 && load == MX4_DIRECT) {
         if (ends) DG_TILE(256, 2, 4, WORDS_ENDS, true, false);
         else DG_TILE(256, 2, 4, WORDS, true, false);
     } else if (tile == MX4_T128 && load == MX4_DIRECT) {
-        if (ends) DG_SPLITS(128, WORDS_ENDS, true);
-        else DG_SPLITS(128, WORDS, true);
-    } else if (tile == MX4_T128 && load == MX4_BYTES) DG_SPLITS(128, REGS, true);
+        if (ends) DG_TILE(128, 2, 2, WORDS_ENDS, true, false);
+        else DG_TILE(128, 2, 2, WORDS, true, false);
+    } else if (tile == MX4_T128 && load == MX4_BYTES) DG_TILE(128, 2, 2, REGS, true, false);
     else if (tile == MX4_T64 && load == MX4_DIRECT) {
-        if (ends) DG_SPLITS(64, WORDS_ENDS, true);
-        else DG_SPLITS(64, WORDS, true);
-    } else if (tile == MX4_T64 && load == MX4_BYTES) DG_SPLITS(64, REGS, true);
-    else if (tile == MX4_T64 && load == MX4_ANY) DG_SPLITS(64, REGS, false);
+        if (ends) DG_64(WORDS_ENDS, true);
+        else DG_64(WORDS, true);
+    } else if (tile == MX4_T64 && load == MX4_BYTES) DG_64(REGS, true);
+    else if (tile == MX4_T64 && load == MX4_ANY) DG_64(REGS, false);
     else return hipErrorInvalidValue;
-#undef DG_SPLITS
+#undef DG_64
 #undef DG_TILE
     return hipGetLastError();
 }
