@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(256) mx4_quant_rows(Mx4QuantArgs a) {
 template <int KIND, bool VEC>
 __global__ void __launch_bounds__(2 * MX4_TILE_K) mx4_quant_columns(Mx4QuantArgs a) {
     constexpr int NT = 2 * MX4_TILE_K, BLOCKS = MX4_TILE_K / 32;   // a wave for every block of a row
-    constexpr int PITCH = MX4_TILE_K / 2 + 16;     // rows 4 words apart on the banks
+    constexpr int PITCH = MX4_TILE_K / 2 + 16;     // (a lane's rows are 4 apart, 16 words on the banks: the codes' way in conflicts)
     __shared__ __attribute__((aligned(16))) char lq[MX4_TILE_M * PITCH];
     __shared__ uint8_t ls[MX4_TILE_M * BLOCKS];    // [row][block]
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;

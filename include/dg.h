@@ -550,9 +550,10 @@ typedef enum { DG_MX4_FLOOR = 0, DG_MX4_CEIL = 1 } dg_mx4_mode;
 
 dg_status dg_quant_mx4(const dg_view *X, const dg_view *Q, const dg_view *S, dg_mx4_mode mode, hipStream_t stream);
 
-/* Y <- the numbers that codes and scales stand for, rounded once to Y's dtype (exact in
- * DG_F32, but 4 and 6 times 2^126 or 2^127, which are infinite where they pass its range;
- * exact in DG_BF16 and DG_F16 within theirs).
+/* Y <- the numbers that codes and scales stand for, rounded once to Y's dtype.  Exact in
+ * DG_F32, but that 4 and 6 times 2^126 and 2, 3, 4 and 6 times 2^127 pass its range and are
+ * infinite (DG_MX4_CEIL writes 4 times 2^126 for sizes from 1.75 * 2^127 on); exact in
+ * DG_BF16 and DG_F16 within theirs.
  *   Q, S as written by dg_quant_mx4; Y [M][K] DG_F32, DG_F16 or DG_BF16, any strides
  *   (written); matrices or 3-D stacks.
  * Errors as for dg_quant_mx4. */
@@ -562,7 +563,8 @@ dg_status dg_dequant_mx4(const dg_view *Q, const dg_view *S, const dg_view *Y, h
  *   A  codes [M][ceil(K / 2)] DG_U8 with scales SA [M][ceil(K / 32)], or [M][K] DG_F16 or
  *      DG_BF16, K-contiguous, with SA NULL.
  *   C  [M][N] DG_F32, DG_F16 or DG_BF16.  act: a dg_act value.
- * FP32 accumulation, one rounding to C's dtype.  No operand is rounded.
+ * FP32 accumulation, one rounding to C's dtype.  No operand is rounded, weights beyond
+ * FP32's range (above) among them: a sum is infinite where it passes FP32 itself.
  * Training: with Y = X W^T, dX = dY W is the product of dY and of W's transpose, both
  * quantised along N, and dW = dY^T X that of both transposes quantised along the rows.
  * Quickest with scales side by side and rows of codes and scales at multiples of 16 bytes,

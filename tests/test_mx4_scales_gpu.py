@@ -147,3 +147,20 @@ def test_largest_and_least_operands(dg, M, N, K, plan, place, size, scales):
     dg.gemm_mx4(a, q, s, C)
     assert A.isfinite().all() and C.isfinite().all(), f"{int((~C.isfinite()).sum())} not finite"
     om.check(C, ox.gemm(A, None, Q, S, K, 0, F32), plan)
+
+
+def test_the_largest_number_quantised(dg):
+    # DG_MX4_CEIL gives FP32's largest number 4 times 2^126: infinite read back, finite in every product with small rows
+    f = torch.finfo(F32)
+    W = torch.full((40, 64), f.max, device=DEV)
+    W[1:, 3] = 1.75 * 2.0 ** 127
+    W[::2] *= -1
+    Q, S = torch.zeros(40, 32, dtype=U8, device=DEV), torch.zeros(40, 2, dtype=U8, device=DEV)
+    dg.quant_mx4(W, Q, S, dg.DG_MX4_CEIL)
+    assert (S == 253).all() and ((Q & 0x77) == 0x66).all()
+    assert torch.equal(dg.dequant_mx4(Q, S, torch.zeros_like(W)), W * float("inf"))
+    for M in (1, 13, 40, 200):
+        A = torch.zeros(M, 64, dtype=BF16, device=DEV)
+        A[:, ::2] = 2.0 ** -30
+        C = dg.gemm_mx4(A, Q, S, torch.full((M, 40), NAN, device=DEV))
+        assert torch.equal(C, (torch.sign(W[:, 0]) * 2.0 ** 103).expand(M, -1))                      # 32 times 2^128 times 2^-30
