@@ -164,3 +164,56 @@ def test_the_largest_number_quantised(dg):
         A[:, ::2] = 2.0 ** -30
         C = dg.gemm_mx4(A, Q, S, torch.full((M, 40), NAN, device=DEV))
         assert torch.equal(C, (torch.sign(W[:, 0]) * 2.0 ** 103).expand(M, -1))                      # 32 times 2^128 times 2^-30
+
+
+def zeros_of_both_signs(g, *shape):
+    return (torch.randint(0, 2, shape, generator=g) * 8 + torch.randint(0, 2, shape, generator=g) * 128).to(U8)
+
+
+@pytest.mark.parametrize("M,N,K,plan,place", KERNELS)
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_zeros_under_any_scale(dg, M, N, K, plan, place, dtype):
+    # blocks of zeros of both signs count nothing, whatever scale they are under (but NaN)
+    g = gen(M, N, K, 5)
+    A = normal(g, M, K, dtype=dtype, spread=0.5)
+    Q, S = coded(g, N, K, (118, 128))
+    blocks = S.shape[1]
+    zero = torch.rand(N, blocks, generator=g) < 0.2
+    S = torch.where(zero, scale_bytes(g, 0, 254, N, blocks), S)
+    mask = zero.repeat_interleave(16, 1)[:, :Q.shape[1]]
+    Q = torch.where(mask, zeros_of_both_signs(g, *Q.shape), Q)
+    if K % 2:
+        Q[:, -1] &= 15
+    a, q, s = place(A), place(Q), place(S)
+    C = torch.full((M, N), NAN, device=DEV)
+    assert dg.gemm_mx4_plan(a, q, s, C).startswith(plan)
+    dg.gemm_mx4(a, q, s, C)
+    om.check(C, ox.gemm(A, None, Q, S, K, 0, F32), plan)
+
+
+@pytest.mark.parametrize("M,N,K,plan", [
+    (5, 300, 1100, few(16, 16)), (30, 300, 1101, few(32, 16)), (50, 300, 1024, few(64, 16)), (70, 300, 90, "element loads"), (70, 300, 777, "vector loads, 64x64"),
+    (70, 300, 1000, "direct loads, 64x64"), (1030, 2900, 512, "ring loads, 128x128"), (1030, 2900, 500, "vector loads, 128x128"), (1030, 2900, 1000, "direct loads, 128x128"),
+    (4000, 3300, 512, "ring loads, 256x256"), (4000, 3300, 304, "direct loads, 256x256")])
+def test_zeros_of_codes_under_any_scale(dg, M, N, K, plan):
+    # and so for blocks of either operand in products of codes, the other's largest scale against them
+    g = gen(M, N, K, 6)
+    ops = []
+    for rows in (M, N):
+        Q, S = coded(g, rows, K, (118, 128))
+        zero = torch.rand(rows, S.shape[1], generator=g) < 0.2
+        S = torch.where(zero, scale_bytes(g, 0, 254, rows, S.shape[1]), S)
+        Q = torch.where(zero.repeat_interleave(16, 1)[:, :Q.shape[1]], zeros_of_both_signs(g, *Q.shape), Q)
+        if K % 2:
+            Q[:, -1] &= 15
+        ops += [Q, S]
+    A, SA, Q, S = ops
+    # the last block of either operand: zeros of one under the largest scale, codes of the other under it
+    A[0, 16 * (S.shape[1] - 1):], SA[0, -1], S[:, -1] = 0, 254, 254
+    if M > 1:
+        SA[1:, -1] = 1
+    C = torch.full((M, N), NAN, device=DEV)
+    args = here(A), here(Q), here(S), C
+    assert dg.gemm_mx4_plan(*args, SA=here(SA)).startswith(plan), dg.gemm_mx4_plan(*args, SA=here(SA))
+    dg.gemm_mx4(*args, SA=here(SA))
+    om.check(C, ox.gemm(A, SA, Q, S, K, 0, F32), plan)
