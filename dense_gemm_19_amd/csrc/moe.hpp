@@ -141,7 +141,7 @@ constexpr int w4_chunk(int tm) { return tm == 1 ? 1024 : 512; }
 // tm: rows of a workgroup / 16, 1 to W4_MAX_TM (4, whose chunk of A leaves LDS
 // no room for a second, took 26 us for 248 x 1452 x 2592 where 3 takes 14.2 to 21)
 hipError_t launch_w4(int in_kind, int tm, const W4Args &a, int64_t units, hipStream_t stream);
-// The same for microscaled weights (w4_mx.hip): E2M1 codes, E8M0 scale bytes, G = 32, no zero points
+// The same for microscaled weights (w4_mx.hip): E2M1 codes, E8M0 scale bytes, G = 32, no zero points; tm 2 or 3
 hipError_t launch_w4_mx(int in_kind, int tm, const W4Args &a, int64_t units, hipStream_t stream);
 
 // Row strides below this keep lane offsets within a workgroup's 64 rows or columns in 32 bits.

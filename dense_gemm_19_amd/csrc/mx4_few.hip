@@ -7,8 +7,8 @@
 // of a row of codes and 16 of its scales.  Lane (g, n), n = lane % 16, loads of row n the 16
 // bytes 64 j + 16 g at each of four steps j, a whole block, and all 16 scale bytes.
 // Bytes of codes bound it for a few rows, the way of A from the caches beyond (all columns'
-// workgroups read it): 1 x 14336 x 4096, 31 MB, 8.8 us BF16 and 8.5 codes, 3.6 TB/s with a
-// launch of 1.5 us in it; 16 rows 12.8 / 10.5; 33 x 4096 x 14336 19.5 us BF16.
+// workgroups read it): 1 x 14336 x 4096, 31 MB, 8.7 us BF16 and 8.1 codes, 3.6 TB/s with a
+// launch of 1.5 us in it; 16 rows 11.3 / 9.2; 33 x 4096 x 14336 17.5 us BF16.
 //   A in codes: those are the operands of v_mfma_scale_f32_16x16x128_f8f6f4 as they lie.
 //   A in 16 bits: the lanes of a row first exchange words (a 4 x 4 transpose in four
 //   instructions), so that an instruction of 32 elements meets one block of every row.
